@@ -261,7 +261,8 @@ KDA_API kda_status kda_decode_layer_step(const void* q_in, const void* k_in, con
 /*
  * Reads and clears this device's error word (on the current device), after
  * waiting for `stream`.  *code receives the raw word (0 = none).  Returns
- * KDA_OK when it was 0, KDA_ERR_INVALID_ARG for a malformed cu_seqlens,
+ * KDA_OK when it was 0, KDA_ERR_INVALID_ARG for a malformed cu_seqlens or for
+ * what the calls of kda_kv4.h report (a page, slot or length out of range),
  * KDA_ERR_DEVICE_TIMEOUT for a device-side wait that ran out,
  * KDA_ERR_NONFINITE when a tensor-core prefill wrote an inf or NaN output or
  * final state (the fp16 range of kda_chunk_fwd exceeded, or non-finite

@@ -1,0 +1,102 @@
+/*
+ * kda_kv4.h -- C ABI of the paged 4-bit key/value cache for the
+ * softmax-attention layers that a hybrid decoder keeps between its recurrent
+ * layers (page "Kimi K3：架构、训练与百万 Token Agentic RL 技术解读" §2: three KDA layers
+ * to one attention layer; §9: the physical blocks of the prefix cache): block
+ * tables and slot maps, the cache's write and read-back, and attention over it.
+ *
+ * The conventions of kda.h hold: device pointers owned by the caller, nothing
+ * allocated, asynchronous on `stream`, argument errors found on the host before
+ * anything is launched, conditions that only the device sees (a page, slot,
+ * length or prefix-sum array out of range) reported through kda_device_error()
+ * as KDA_ERR_INVALID_ARG after the work, never by an access out of range.
+ *
+ * The cache is uint8 [num_pages][Hkv][page_size / 16][17 D], 16-byte aligned: for
+ * each page and key/value head, units of 16 tokens of 17 D bytes.  A unit holds
+ *   keys    [16 rows][D / 2]: row r's 32-bit word at place t (D / 32) + j holds channels
+ *           32 j + 8 t .. + 7, four bits each, the lowest channel in the lowest bits;
+ *   values  [2 blocks of 8 tokens][8 g][8 tokens][D / 32 j] 16-bit words: channels
+ *           32 j + 4 g .. + 3, in the same order;
+ *   key scales [16][D / 32] and value scales [16][D / 32], one byte for 32 channels.
+ * A stored value is the E2M1 code (sign bit over 0, 0.5, 1, 1.5, 2, 3, 4, 6) times
+ * 2^(scale byte - 127).  The scale is the smallest power of two, 2^-126 at least,
+ * that leaves no channel of the 32 above 6; codes are rounded to nearest, ties to
+ * the even code.  32 channels with an inf or NaN among them are stored as scale
+ * byte 255, which reads back as NaN.  (This is the block format that the OCP
+ * microscaling specification calls MXFP4, with a scale rule that never saturates;
+ * the order inside a unit is the order in which the attention kernel's matrix
+ * instructions take their operands.)
+ * Token p of a sequence lies in page block_table[p / page_size], place p % page_size;
+ * its slot is page * page_size + place.
+ * page_size is a multiple of 16, at most 4096; D is 64 or 128;
+ * num_pages * page_size is at most 2^31 - 1.
+ */
+#ifndef KDA_GB300_KDA_KV4_H
+#define KDA_GB300_KDA_KV4_H
+
+#include "kda.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Bytes of a cache of num_pages pages, or SIZE_MAX when the sizes are invalid. */
+KDA_API size_t kda_kv4_cache_bytes(int64_t num_pages, int32_t Hkv, int32_t page_size, int32_t D);
+
+/*
+ * Block tables and slot maps of one step from request lengths.
+ *
+ *  cached_lens, new_lens  int32[N]: tokens of each request in the cache, and tokens that
+ *               this step adds (either may be 0)
+ *  block_table  int32[N][max_pages], row stride max_pages: the first
+ *               ceil(cached / page_size) entries of a row are read (only the last, partly
+ *               filled one is); the entries of the pages that the new tokens begin are
+ *               written, request by request, with the next entries of free_pages
+ *  free_pages   int32[num_free], free_start int32[1]: the pages that are free are
+ *               free_pages[free_start ..]
+ *  cu_seqlens   int32[N + 1]: prefix sums of new_lens (what kda_chunk_fwd takes)
+ *  seq_lens     int32[N]: cached + new (what kda_kv4_attention takes)
+ *  slot_map, positions  int32[num_tokens], 16-byte aligned: each new token's slot, and its
+ *               position in its request; -1 behind the last new token
+ *  free_next    int32[1]: the first entry of free_pages that is still free afterwards
+ * num_tokens is the room in slot_map and positions.  Not every request may get what it
+ * asks for: tokens whose page is not there (the free pages used up, the row too short, a
+ * partly filled page with a negative entry) get slot -1, table entries without a free page
+ * get -1; negative lengths count as 0; of more than num_tokens new tokens the first are
+ * mapped.  Each of these is reported (kda_device_error).  The same inputs give the same
+ * outputs, whatever the table's entries behind the cached pages hold.
+ * N is at most 28672 (its prefix sums are held in shared memory), else KDA_ERR_UNSUPPORTED.
+ * No output may overlap an input or another output.
+ */
+KDA_API kda_status kda_page_map(const int32_t* cached_lens, const int32_t* new_lens, int32_t N,
+                                int32_t* block_table, int32_t max_pages, const int32_t* free_pages,
+                                int64_t num_free, const int32_t* free_start, int32_t page_size,
+                                int64_t num_tokens, int32_t* cu_seqlens, int32_t* seq_lens, int32_t* slot_map,
+                                int32_t* positions, int32_t* free_next, cudaStream_t stream);
+
+/*
+ * Writes T tokens' keys and values into the cache.
+ *  k, v      [T][Hkv][D] dtype dt, 16-byte aligned; the strides from token to token and from
+ *            head to head are given in elements, multiples of 16 bytes, channels contiguous
+ *  slot_map  int32[T]: slots; a negative one leaves its token out; one beyond the cache is
+ *            reported and left out.  No two tokens may have the same slot.
+ */
+KDA_API kda_status kda_kv4_append(const void* k, const void* v, const int32_t* slot_map, int64_t T, int32_t Hkv,
+                                  int32_t D, int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                                  int64_t v_head_stride, kda_dtype dt, void* cache, int64_t num_pages,
+                                  int32_t page_size, cudaStream_t stream);
+
+/*
+ * Reads tokens back: k, v [T][Hkv][D] dtype dt, dense, get the values that the cache holds at
+ * the slots (exact in either type); zeros for a negative slot, and for one beyond the cache,
+ * which is reported.  k, v 16-byte aligned.
+ */
+KDA_API kda_status kda_kv4_gather(const void* cache, int64_t num_pages, int32_t page_size, const int32_t* slot_map,
+                                  int64_t T, int32_t Hkv, int32_t D, kda_dtype dt, void* k, void* v,
+                                  cudaStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* KDA_GB300_KDA_KV4_H */

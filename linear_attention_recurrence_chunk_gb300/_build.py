@@ -1,6 +1,6 @@
 """In-tree build of the CUDA library ``libkda_gb300.so`` for sm_103a.
 
-Each ``csrc/*.cu`` translation unit is compiled by its own ``nvcc`` process (in
+Each ``csrc/**/*.cu`` translation unit is compiled by its own ``nvcc`` process (in
 parallel), then linked into one shared library beside this file.  No cmake,
 no torch extension machinery: the library is plain C ABI (``include/kda.h``).
 """
@@ -32,11 +32,11 @@ def _nvcc() -> str:
 
 
 def sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    return sorted(glob.glob(os.path.join(CSRC, "**", "*.cu"), recursive=True))
 
 
 def _inputs():
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
+    return sources() + glob.glob(os.path.join(CSRC, "**", "*.cuh"), recursive=True) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
 
 
 def up_to_date() -> bool:
@@ -58,7 +58,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             flags += ["-Xptxas", "-v"]
 
         def compile_one(src):
-            obj = os.path.join(tmpdir, os.path.basename(src) + ".o")
+            obj = os.path.join(tmpdir, os.path.relpath(src, CSRC).replace(os.sep, "_") + ".o")
             r = subprocess.run([nvcc, *flags, "-c", src, "-o", obj], capture_output=True, text=True)
             if r.returncode != 0:
                 raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stderr}")

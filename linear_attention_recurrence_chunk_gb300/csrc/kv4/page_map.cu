@@ -1,0 +1,173 @@
+// Block tables and slot maps of one step from request lengths.
+//
+//   cu_i   = sum_{m<i} new_m
+//   need_i = ceil((cached_i + new_i) / ps) - ceil(cached_i / ps),  first_i = start + sum_{m<i} need_m
+//   page(i, j) = table[i][j] for j < ceil(cached_i / ps), else free[first_i + j - ceil(cached_i / ps)]
+//   token x of request i: pos = cached_i + x - cu_i, slot = page(i, pos / ps) ps + pos % ps
+//
+// Bound: latency (8 bytes read per request, 8 written per new token).  So one
+// launch: every CTA sums all requests' lengths by itself (a read of 8 N bytes out
+// of L2 and one block scan) instead of waiting for a first kernel to do it, keeps
+// the two prefix sums in shared memory and maps its own range of tokens, each
+// thread four consecutive ones after one binary search.  A page that a request
+// begins in this step has its first token among the new ones, so that token's
+// thread writes the page's table entry: no thread reads an entry that another
+// writes.
+#include "internal.cuh"
+
+namespace kda {
+namespace kv4 {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kTokensPerThread = 4;
+constexpr int kTile = kThreads * kTokensPerThread;
+
+__device__ __forceinline__ int64_t clamped(int32_t x) { return x > 0 ? x : 0; }
+
+__global__ void __launch_bounds__(kThreads) page_map_kernel(const PageMapProblem p, int32_t n_tiles) {
+  extern __shared__ int32_t sh[];   // cu[N + 1], first[N]
+  int32_t* cu = sh;
+  int32_t* first = sh + p.N + 1;
+  __shared__ int64_t warp_sum[2][kThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t ps = p.page_size;
+  const bool lead = blockIdx.x == 0;
+
+  // prefix sums: thread tid takes requests [a, b)
+  const int per = (p.N + kThreads - 1) / kThreads;
+  const int a = min(tid * per, p.N), b = min(a + per, p.N);
+  int64_t tok = 0, pages = 0;
+  bool bad = false;
+  for (int i = a; i < b; ++i) {
+    const int32_t c0 = p.cached[i], n0 = p.fresh[i];
+    bad |= c0 < 0 || n0 < 0;
+    const int64_t c = clamped(c0), n = clamped(n0);
+    tok += n;
+    pages += (c + n + ps - 1) / ps - (c + ps - 1) / ps;
+  }
+  int64_t st = tok, sp = pages;   // inclusive sums over the warp
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, st, off), y = __shfl_up_sync(0xffffffffu, sp, off);
+    if (lane >= off) {
+      st += x;
+      sp += y;
+    }
+  }
+  if (lane == 31) {
+    warp_sum[0][warp] = st;
+    warp_sum[1][warp] = sp;
+  }
+  __syncthreads();
+  int64_t bt = 0, bp = 0, total = 0, total_pages = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w == warp) {
+      bt = total;
+      bp = total_pages;
+    }
+    total += warp_sum[0][w];
+    total_pages += warp_sum[1][w];
+  }
+  bt += st - tok;
+  bp += sp - pages;
+  const int64_t start = p.free_start[0];
+  // sums beyond int32 only come with more tokens than there is room for (reported);
+  // capped, they map no token
+  constexpr int64_t kCap = 0x7fffffff;
+  for (int i = a; i < b; ++i) {
+    const int64_t c = clamped(p.cached[i]), n = clamped(p.fresh[i]);
+    cu[i] = (int32_t)min(bt, kCap);
+    first[i] = (int32_t)min(start + bp, kCap);
+    if (lead) {
+      p.cu[i] = cu[i];
+      p.lens[i] = (int32_t)min(c + n, kCap);
+      bad |= c + n > kCap || (c + n + ps - 1) / ps > p.max_pages;
+    }
+    bt += n;
+    bp += (c + n + ps - 1) / ps - (c + ps - 1) / ps;
+  }
+  if (tid == 0) {
+    cu[p.N] = (int32_t)min(total, kCap);
+    if (lead) {
+      p.cu[p.N] = cu[p.N];
+      const int64_t end = start + total_pages;
+      bad |= start < 0 || end > p.num_free || total > p.num_tokens;
+      p.free_next[0] = (int32_t)(start < 0 ? start : min(end, max(start, p.num_free)));
+    }
+  }
+  if (bad && lead) report_bad(p.dev_err);
+  __syncthreads();
+
+  const int32_t known = cu[p.N];
+  bool lost = false;
+  for (int32_t tile = blockIdx.x; tile < n_tiles; tile += gridDim.x) {
+    const int64_t x0 = (int64_t)tile * kTile + tid * kTokensPerThread;
+    if (x0 >= p.num_tokens) break;
+    int32_t slot[kTokensPerThread], pos[kTokensPerThread];
+    // the last request i with cu[i] <= x0
+    int lo = 0, hi = p.N;
+    while (lo + 1 < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (cu[mid] <= x0) lo = mid;
+      else hi = mid;
+    }
+    int i = lo;
+#pragma unroll
+    for (int e = 0; e < kTokensPerThread; ++e) {
+      const int64_t x = x0 + e;
+      slot[e] = pos[e] = -1;
+      if (x >= known || x >= p.num_tokens) continue;
+      while (cu[i + 1] <= x) ++i;
+      const int64_t c = clamped(p.cached[i]);
+      const int64_t at = c + (x - cu[i]);
+      pos[e] = (int32_t)min(at, kCap);
+      const int64_t j = at / ps, have = (c + ps - 1) / ps;
+      int64_t page = -1;
+      if (j < p.max_pages) {
+        int32_t* entry = p.table + (int64_t)i * p.max_pages + j;
+        if (j < have) {
+          page = *entry;
+        } else {
+          const int64_t f = (int64_t)first[i] + (j - have);
+          if (f >= 0 && f < p.num_free && start >= 0) page = p.free_pages[f];
+          if (at == j * ps) *entry = (int32_t)page;
+        }
+      }
+      if (page >= 0 && page * ps + ps - 1 <= kCap) slot[e] = (int32_t)(page * ps + (at - j * ps));
+      else lost = true;
+    }
+    if (x0 + kTokensPerThread <= p.num_tokens) {
+      *reinterpret_cast<int4*>(p.slots + x0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      *reinterpret_cast<int4*>(p.pos + x0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kTokensPerThread; ++e)
+        if (x0 + e < p.num_tokens) {
+          p.slots[x0 + e] = slot[e];
+          p.pos[x0 + e] = pos[e];
+        }
+    }
+  }
+  if (lost) report_bad(p.dev_err);
+}
+
+}  // namespace
+
+cudaError_t launch_page_map(const PageMapProblem& p, cudaStream_t stream) {
+  const size_t smem = (2 * (size_t)p.N + 1) * sizeof(int32_t);
+  cudaError_t e;
+  if (smem > 47 * 1024 &&
+      (e = cudaFuncSetAttribute(page_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
+    return e;
+  const int64_t tiles = (p.num_tokens + kTile - 1) / kTile;
+  const unsigned grid = (unsigned)(tiles < 1 ? 1 : tiles > 304 ? 304 : tiles);
+  prof_begin(stream, "page_map_kernel");
+  page_map_kernel<<<grid, kThreads, smem, stream>>>(p, (int32_t)tiles);
+  prof_end(stream);
+  return cudaGetLastError();
+}
+
+}  // namespace kv4
+}  // namespace kda
