@@ -95,6 +95,49 @@ KDA_API kda_status kda_kv4_gather(const void* cache, int64_t num_pages, int32_t 
                                   int64_t T, int32_t Hkv, int32_t D, kda_dtype dt, void* k, void* v,
                                   cudaStream_t stream);
 
+/*
+ * Bytes of device scratch memory for kda_kv4_attention with these sizes, or SIZE_MAX when
+ * they are invalid.
+ */
+KDA_API size_t kda_kv4_attention_workspace_size(int64_t T, int32_t N, int32_t Hq, int32_t Hkv, int32_t D,
+                                                int32_t max_q_len, kda_dtype dt);
+
+/*
+ * Softmax attention of each sequence's newest tokens over its cached keys and values:
+ *   o = sum_p softmax_p(sm_scale q . k_p) v_p,   lse = ln sum_p exp(sm_scale q . k_p)
+ * over p <= L - n + i for the i-th of the sequence's n query tokens, L cached tokens
+ * (kda_kv4_append writes the new tokens' keys and values first).  A decode step has n = 1,
+ * the verification of draft tokens a few, a chunk of a prompt many.  Query head h reads
+ * key/value head h / (Hq / Hkv).
+ *
+ *  q    [T][Hq][D] dtype dt, strides in elements as for kda_kv4_append
+ *  o    [T][Hq][D] dtype dt, dense, 16-byte aligned;  lse fp32 [T][Hq] or NULL
+ *  block_table int32[N][max_pages], seq_lens int32[N] (L)
+ *  cu_seqlens  int32[N + 1]: sequence s has the query tokens cu_seqlens[s] .. cu_seqlens[s + 1] - 1;
+ *              NULL for one token each (then T = N)
+ *  max_q_len   the most query tokens of a sequence (>= 1)
+ *  workspace   kda_kv4_attention_workspace_size bytes, 256-byte aligned, contents do not matter
+ * A query that sees no token (L = 0, or n > L and i < n - L) gets o = 0 and lse = -inf.  What
+ * lies in the cache behind L, or at positions that a query does not see, never reaches its
+ * result; a key or value group stored as not finite makes the results of the queries that
+ * see it NaN (of a value group: its 32 channels).
+ * Scores, softmax statistics and sums are fp32.  bf16 inputs multiply exactly (a row of q is
+ * scaled by a power of two into fp16's range), the softmax weights enter the second product
+ * as fp16, relative to the largest; fp32 inputs take both products in two fp16 parts.
+ * A length beyond the table, a page beyond the cache, a cu_seqlens that decreases, does not
+ * begin at 0 or passes T, and a sequence of more than max_q_len tokens are reported; the
+ * outputs of such a sequence are unspecified, no access leaves the arrays.
+ * Query tokens of no sequence keep their o and lse.  Calls in flight at once need a workspace
+ * each.
+ * KDA_ERR_UNSUPPORTED: D not 64 or 128; N beyond 65535; Hq / Hkv beyond 128.
+ */
+KDA_API kda_status kda_kv4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* cache,
+                                     int64_t num_pages, int32_t page_size, const int32_t* block_table,
+                                     int32_t max_pages, const int32_t* seq_lens, const int32_t* cu_seqlens,
+                                     int64_t T, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_q_len,
+                                     float sm_scale, kda_dtype dt, void* o, float* lse, void* workspace,
+                                     size_t workspace_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -32,7 +32,7 @@ Functions keep the C names:
   ``kda_check_wait_timeout(limit_cycles)`` (failure-detection check).
 * from ``kv4.py``, the paged 4-bit key/value cache of the attention layers beside
   the recurrent ones: ``kda_page_map``, ``kda_kv4_cache``, ``kda_kv4_append``,
-  ``kda_kv4_gather``.
+  ``kda_kv4_gather``, ``kda_kv4_attention``, ``kda_kv4_attention_workspace_size``.
 """
 from __future__ import annotations
 
@@ -47,7 +47,8 @@ from . import _build
 __all__ = ["kda_chunk_fwd", "kda_chunk_fwd_snapshots", "kda_chunk_fwd_gated", "kda_chunk_fwd_decay_variant",
            "DECAY_BOUNDED", "DECAY_SOFTPLUS", "kda_decode_step", "kda_decode_layer_step", "kda_chunk_fwd_workspace_size", "kda_device_error",
            "kda_check_wait_timeout", "KdaError", "library_path", "load_library", "STATUS",
-           "kda_page_map", "kda_kv4_cache", "kda_kv4_append", "kda_kv4_gather"]
+           "kda_page_map", "kda_kv4_cache", "kda_kv4_append", "kda_kv4_gather", "kda_kv4_attention",
+           "kda_kv4_attention_workspace_size"]
 
 DECAY_BOUNDED, DECAY_SOFTPLUS = 0, 1   # kda_decay_map
 STATUS = {0: "KDA_OK", 1: "KDA_ERR_INVALID_ARG", 2: "KDA_ERR_UNSUPPORTED", 3: "KDA_ERR_CUDA",
@@ -320,4 +321,5 @@ def kda_check_wait_timeout(limit_cycles: int, stream=None) -> None:
     _check(load_library().kda_check_wait_timeout(int(limit_cycles), _stream(stream)), "kda_check_wait_timeout")
 
 
-from .kv4 import kda_kv4_append, kda_kv4_cache, kda_kv4_gather, kda_page_map  # noqa: E402
+from .kv4 import (kda_kv4_append, kda_kv4_attention, kda_kv4_attention_workspace_size, kda_kv4_cache,  # noqa: E402
+                  kda_kv4_gather, kda_page_map)

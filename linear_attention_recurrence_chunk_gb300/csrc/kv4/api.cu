@@ -137,3 +137,59 @@ kda_status kda_kv4_gather(const void* cache, int64_t num_pages, int32_t page_siz
 }
 
 }  // extern "C"
+
+namespace {
+
+kda_status check_attention(int64_t T, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_q, kda_dtype dt) {
+  if (dt != KDA_F32 && dt != KDA_BF16) return KDA_ERR_INVALID_ARG;
+  if (T < 0 || N < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || max_q < 1) return KDA_ERR_INVALID_ARG;
+  if (T > INT32_MAX || (int64_t)max_q * Hq > INT32_MAX || T * (int64_t)Hq > INT32_MAX) return KDA_ERR_INVALID_ARG;
+  if (Hkv > 65535) return KDA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return KDA_ERR_UNSUPPORTED;
+  if (N > 65535 || Hq / Hkv > 128) return KDA_ERR_UNSUPPORTED;
+  return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kda_kv4_attention_workspace_size(int64_t T, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_q_len,
+                                        kda_dtype dt) {
+  if (check_attention(T, N, Hq, Hkv, D, max_q_len, dt) != KDA_OK) return SIZE_MAX;
+  return kda::kv4::attention_workspace(Hq, Hkv, D, max_q_len, dt);
+}
+
+kda_status kda_kv4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* cache,
+                             int64_t num_pages, int32_t page_size, const int32_t* block_table, int32_t max_pages,
+                             const int32_t* seq_lens, const int32_t* cu_seqlens, int64_t T, int32_t N, int32_t Hq,
+                             int32_t Hkv, int32_t D, int32_t max_q_len, float sm_scale, kda_dtype dt, void* o,
+                             float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  kda_status st = check_attention(T, N, Hq, Hkv, D, max_q_len, dt);
+  if (st != KDA_OK) return st;
+  size_t bytes = 0;
+  if ((st = check_cache(num_pages, Hkv, page_size, D, &bytes)) != KDA_OK) return st;
+  if (max_pages < 0 || !isfinite(sm_scale)) return KDA_ERR_INVALID_ARG;
+  if (!cu_seqlens && (T != N || max_q_len != 1)) return KDA_ERR_INVALID_ARG;
+  if (T == 0 || N == 0) return KDA_OK;
+  if (!o || !aligned(o, 16) || !aligned(lse, 4) || !seq_lens || !aligned(seq_lens, 4) || !aligned(cu_seqlens, 4))
+    return KDA_ERR_INVALID_ARG;
+  if ((max_pages > 0 && !block_table) || !aligned(block_table, 4) || (bytes > 0 && !cache) || !aligned(cache, 16))
+    return KDA_ERR_INVALID_ARG;
+  const size_t need = kda::kv4::attention_workspace(Hq, Hkv, D, max_q_len, dt);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return KDA_ERR_INVALID_ARG;
+  Range rq;
+  if (!strides_ok(q, T, Hq, D, q_token_stride, q_head_stride, elem(dt), &rq)) return KDA_ERR_INVALID_ARG;
+  const size_t rows = (size_t)T * Hq;
+  const Range in[] = {rq, {cache, bytes}, {block_table, (size_t)N * max_pages * 4}, {seq_lens, (size_t)N * 4},
+                      {cu_seqlens, ((size_t)N + 1) * 4}};
+  const Range out[] = {{o, rows * D * elem(dt)}, {lse, rows * 4}, {workspace, need}};
+  if (!apart(in, out)) return KDA_ERR_INVALID_ARG;
+  kda::kv4::AttnProblem p{q, q_token_stride, q_head_stride, static_cast<const uint8_t*>(cache), num_pages, page_size,
+                          block_table, max_pages, seq_lens, cu_seqlens, T, N, Hq, Hkv, D, max_q_len, sm_scale, dt, o,
+                          lse, nullptr};
+  if (kda::device_error_ptr(&p.dev_err) != cudaSuccess) return KDA_ERR_CUDA;
+  return kda::kv4::launch_attention(p, workspace, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // extern "C"

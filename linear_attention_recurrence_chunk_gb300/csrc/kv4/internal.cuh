@@ -60,5 +60,25 @@ struct CopyProblem {   // append (k, v read) and gather (k, v written)
 cudaError_t launch_append(const CopyProblem& p, cudaStream_t stream);
 cudaError_t launch_gather(const CopyProblem& p, cudaStream_t stream);
 
+struct AttnProblem {
+  const void* q;
+  int64_t qt, qh;           // strides in elements
+  const uint8_t* cache;
+  int64_t num_pages;
+  int32_t page_size;
+  const int32_t* table;
+  int32_t max_pages;
+  const int32_t *lens, *cu; // cu: nullptr for one query token per sequence
+  int64_t T;
+  int32_t N, Hq, Hkv, D, max_q;
+  float sm_scale;
+  kda_dtype dt;
+  void* o;
+  float* lse;
+  int32_t* dev_err;
+};
+size_t attention_workspace(int32_t Hq, int32_t Hkv, int32_t D, int32_t max_q, kda_dtype dt);
+cudaError_t launch_attention(const AttnProblem& p, void* workspace, cudaStream_t stream);
+
 }  // namespace kv4
 }  // namespace kda

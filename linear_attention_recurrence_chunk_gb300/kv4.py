@@ -9,7 +9,9 @@ cache, the rounding and the errors are stated there):
 * ``kda_kv4_cache(num_pages, num_kv_heads, page_size, head_dim)`` -> an empty cache,
   uint8 ``[pages, kv heads, page_size / 16, 17 * head_dim]``;
 * ``kda_kv4_append(k, v, slot_map, cache)``: new tokens into the cache;
-* ``kda_kv4_gather(cache, slot_map, dtype)`` -> ``(k, v)``: tokens read back.
+* ``kda_kv4_gather(cache, slot_map, dtype)`` -> ``(k, v)``: tokens read back;
+* ``kda_kv4_attention(q, cache, block_table, seq_lens, ...)`` -> ``o`` or ``(o, lse)``:
+  softmax attention of each sequence's newest tokens over its cached ones.
 
 Tensors are CUDA tensors of one device; a ``stream`` (default: the current one) is
 a ``torch.cuda.Stream`` or a raw handle, and what a function allocates itself
@@ -23,7 +25,8 @@ from typing import Optional, Tuple
 
 import torch
 
-__all__ = ["kda_page_map", "kda_kv4_cache", "kda_kv4_append", "kda_kv4_gather"]
+__all__ = ["kda_page_map", "kda_kv4_cache", "kda_kv4_append", "kda_kv4_gather", "kda_kv4_attention",
+           "kda_kv4_attention_workspace_size"]
 
 _UNIT = 16          # tokens of a unit of the cache
 _UNIT_BYTES = 17    # bytes of a unit per channel
@@ -45,6 +48,11 @@ def _lib():
         lib.kda_kv4_append.restype = c
         lib.kda_kv4_gather.argtypes = [vp, i64, i32, vp, i64, i32, i32, c, vp, vp, vp]
         lib.kda_kv4_gather.restype = c
+        lib.kda_kv4_attention_workspace_size.argtypes = [i64, i32, i32, i32, i32, i32, c]
+        lib.kda_kv4_attention_workspace_size.restype = sz
+        lib.kda_kv4_attention.argtypes = [vp, i64, i64, vp, i64, i32, vp, i32, vp, vp, i64, i32, i32, i32, i32, i32,
+                                          ctypes.c_float, c, vp, vp, vp, sz, vp]
+        lib.kda_kv4_attention.restype = c
         _fns = lib
     return _fns
 
@@ -195,3 +203,56 @@ def kda_kv4_gather(cache: torch.Tensor, slot_map: torch.Tensor, dtype: torch.dty
         _check(lib.kda_kv4_gather(cache.data_ptr(), pages, ps, sl, T, H, D, dt, k.data_ptr(), v.data_ptr(), st),
                "kda_kv4_gather")
     return k, v
+
+
+def kda_kv4_attention_workspace_size(num_tokens: int, num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                                     max_q_len: int, dtype: torch.dtype) -> int:
+    """Bytes of workspace for ``kda_kv4_attention`` with these sizes."""
+    n = _lib().kda_kv4_attention_workspace_size(num_tokens, num_seqs, num_heads, num_kv_heads, head_dim, max_q_len,
+                                                _dtype(dtype))
+    if n == (1 << 64) - 1:
+        _check(1, "kda_kv4_attention_workspace_size")
+    return int(n)
+
+
+def kda_kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                      cu_seqlens: Optional[torch.Tensor] = None, max_q_len: int = 1,
+                      sm_scale: Optional[float] = None, return_lse: bool = False, o: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of the newest tokens of N sequences over their cached tokens.
+
+    q ``[T, heads, head dim]`` (token and head strides of 16-byte steps), block_table
+    ``[N, max_pages]``, seq_lens ``[N]`` (cached tokens, the new ones among them),
+    cu_seqlens ``[N + 1]`` (int32; None: one query token per sequence), at most
+    ``max_q_len`` query tokens per sequence; ``sm_scale`` defaults to head_dim^-1/2.
+    Returns o ``[T, heads, head dim]``, and with ``return_lse`` the log of each row's
+    sum of exponentials, fp32 ``[T, heads]``."""
+    lib = _lib()
+    pages, H, ps, D = _dims(cache)
+    if q.dim() != 3 or q.shape[2] != D:
+        raise ValueError(f"q: [tokens, heads, {D}] expected, got {tuple(q.shape)}")
+    T, Hq = q.shape[0], q.shape[1]
+    if block_table.dim() != 2:
+        raise ValueError("block_table: [N, max_pages] is expected")
+    N, max_pages = block_table.shape
+    qt, qh = _strided("q", q, Hq, D)
+    dt = _dtype(q.dtype)
+    bt, ln = _i32("block_table", block_table), _i32("seq_lens", seq_lens, (N,))
+    cu = None if cu_seqlens is None else _i32("cu_seqlens", cu_seqlens, (N + 1,))
+    dev = _same_device(q, cache, block_table, seq_lens, cu_seqlens, o, workspace)
+    if o is not None and (o.dtype is not q.dtype or o.shape != q.shape or not o.is_contiguous()):
+        raise ValueError("o: a contiguous tensor of q's type and shape is expected")
+    need = lib.kda_kv4_attention_workspace_size(T, N, Hq, H, D, max_q_len, dt)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor is expected")
+    with _on(dev, stream) as st:
+        if o is None:
+            o = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if return_lse else None
+        if workspace is None:
+            workspace = torch.empty(256 if need == (1 << 64) - 1 else need, dtype=torch.uint8, device=dev)
+        _check(lib.kda_kv4_attention(q.data_ptr(), qt, qh, cache.data_ptr(), pages, ps, bt, max_pages, ln, cu, T, N, Hq, H,
+                                     D, max_q_len, D ** -0.5 if sm_scale is None else sm_scale, dt, o.data_ptr(),
+                                     None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), st), "kda_kv4_attention")
+    return (o, lse) if return_lse else o

@@ -102,3 +102,34 @@ def attention(q, k, v, scale, n_new=None):
                 o[i, h] = p @ v[:m, h // (Hq // Hkv)] / p.sum()
             lse[i, h] = np.log(p.sum()) + top
     return o, lse
+
+
+def attention_bound(q, k, v, scale, n_new, parts):
+    """How far an fp32 evaluation may be from attention(): arrays (o [n, Hq, D] without
+    the rounding of the output itself, lse [n, Hq]).
+
+    A score is off by at most ds = 2^-20 sum_d |q_d k_d| |scale|: two fp16 parts of q or an
+    exact q (2^-22), the products' sums and the three factors in fp32.  A weight is off by
+    2 ds (its own score, and the sum's), its rounding to fp16 (2^-11, or 2^-21 in two
+    parts), and e^x (2^-21); the tokens' sums in fp32 add 2^-23 per 16 tokens.  A weight
+    times its value scale, relative to the row's largest weight and the largest scale
+    2^E, is held in fp16 below 2^16: where that is subnormal, half a step is 2^-40 2^E,
+    on each token's code of 6 at most.  2^E is below max|v| / 3, and counts as 2^-27 at
+    least."""
+    n, Hq, D = q.shape
+    L, Hkv = k.shape[0], k.shape[1]
+    to, tl = np.zeros((n, Hq, D)), np.zeros((n, Hq))
+    for i in range(n):
+        m = L - n + i + 1
+        if m <= 0:
+            continue
+        for h in range(Hq):
+            kk, vv = k[:m, h // (Hq // Hkv)], v[:m, h // (Hq // Hkv)]
+            z = (kk @ q[i, h]) * scale
+            w = np.exp(z - z.max())
+            ds = 2.0 ** -20 * (np.abs(kk) @ np.abs(q[i, h])).max() * abs(scale)
+            run = (m / 16 + 1) * 2.0 ** -23
+            small = 6 * m * 2.0 ** -40 * max(np.abs(vv[np.isfinite(vv)]).max(initial=0) / 3, 2.0 ** -27)
+            to[i, h] = small / w.sum() + (2 * ds + (2.0 ** -11 if parts == 1 else 2.0 ** -21) + 2.0 ** -21 + 2 * run) * (w @ np.abs(vv)) / w.sum()
+            tl[i, h] = ds + 2.0 ** -21 + run + 2.0 ** -22 * abs(np.log(w.sum()) + z.max())
+    return to, tl

@@ -134,3 +134,34 @@ def test_page_map_reference():
     assert slots.tolist()[:2] == [-1, -1] and pos.tolist()[:2] == [3, 4]
     assert t[1].tolist() == [6, 7, -1] and slots.tolist()[2:] == [6 * 16 + i for i in range(16)] + [7 * 16] + [-1]
     assert cu.tolist() == [0, 2, 19, 19] and lens.tolist() == [5, 17, 16] and nxt == 3
+
+
+def _attn(lib, **kw):
+    a = dict(q=FAKE, qt=1024, qh=128, cache=FAKE + 8 * G, pages=10, ps=64, table=FAKE + 9 * G, mp=4, lens=FAKE + 10 * G,
+             cu=None, T=3, N=3, Hq=8, Hkv=2, D=128, mq=1, scale=0.1, dt=1, o=FAKE + 11 * G, lse=None, ws=FAKE + 12 * G,
+             wsb=1 << 33)
+    a.update(kw)
+    return lib.kda_kv4_attention(a["q"], a["qt"], a["qh"], a["cache"], a["pages"], a["ps"], a["table"], a["mp"], a["lens"],
+                                 a["cu"], a["T"], a["N"], a["Hq"], a["Hkv"], a["D"], a["mq"], a["scale"], a["dt"], a["o"],
+                                 a["lse"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(q=None), 1), (dict(cache=None), 1), (dict(table=None), 1), (dict(lens=None), 1), (dict(o=None), 1),
+    (dict(ws=None), 1), (dict(wsb=100), 1), (dict(ws=FAKE + 12 * G + 128), 1), (dict(dt=3), 1), (dict(D=96), 2),
+    (dict(Hq=7), 1), (dict(Hq=258), 2), (dict(Hq=0), 1), (dict(T=4), 1), (dict(mq=2), 1), (dict(mq=0), 1),
+    (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(ps=20), 1), (dict(mp=-1), 1),
+    (dict(N=65536, T=65536), 2), (dict(q=FAKE + 2), 1), (dict(qt=1025), 1), (dict(o=FAKE), 1),
+    (dict(lse=FAKE + 11 * G + 16), 1), (dict(o=FAKE + 8 * G + 64), 1), (dict(lens=FAKE + 10 * G + 1), 1),
+    (dict(cu=FAKE + 13 * G + 2, mq=3), 1), (dict(N=-1), 1), (dict(T=-1), 1)])
+def test_attention_refusals(lib, kw, want):
+    assert _attn(lib, **kw) == want
+    assert _attn(lib, T=0, N=0, q=None) == 0
+
+
+def test_attention_workspace(lib):
+    f = lib.kda_kv4_attention_workspace_size
+    assert 0 < f(3, 3, 8, 2, 128, 1, 1) < f(3, 3, 32, 2, 128, 1, 1) < 1 << 30
+    for args in [(3, 3, 7, 2, 128, 1, 1), (3, 3, 8, 2, 100, 1, 1), (3, 3, 8, 2, 128, 0, 1), (-1, 3, 8, 2, 128, 1, 1),
+                 (3, 3, 8, 2, 128, 1, 9)]:
+        assert f(*args) == (1 << 64) - 1, args
