@@ -19,7 +19,6 @@ belongs to that stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional, Tuple
 
@@ -70,54 +69,53 @@ def _dtype(dt: torch.dtype) -> int:
     return _DT[dt]
 
 
-def _i32(name: str, t: torch.Tensor, shape: Optional[tuple] = None) -> int:
-    """Data pointer of a dense int32 CUDA tensor (of the given shape)."""
+def _i32(name: str, t: torch.Tensor, dev: int, n: Optional[int] = None, dim: int = 1) -> int:
+    """Data pointer of a dense int32 tensor of device ``dev`` with ``dim`` dimensions
+    (and n entries)."""
     if t.dtype is not torch.int32:
         raise TypeError(f"{name}: int32 expected, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: a CUDA tensor is expected")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous tensor is expected")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name}: shape {shape} expected, got {tuple(t.shape)}")
+    if t.get_device() != dev or not t.is_contiguous() or t.dim() != dim or (n is not None and t.numel() != n):
+        raise ValueError(f"{name}: a contiguous {dim}-dimensional tensor{'' if n is None else f' of {n} entries'} on "
+                         f"cuda:{dev} expected, got {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _same_device(*ts: Optional[torch.Tensor]):
-    dev = None
-    for t in ts:
-        if t is None:
-            continue
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
+def _device(name: str, t: torch.Tensor, dtype: Optional[torch.dtype] = None) -> int:
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name}: {dtype} expected, got {t.dtype}")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: a CUDA tensor is expected")
     return dev
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """The device made current, and the caller's stream for what is allocated
-    inside; yields the stream's handle."""
-    with contextlib.ExitStack() as st:
-        if device.index is not None and device.index != torch.cuda.current_device():
-            st.enter_context(torch.cuda.device(device))
-        if stream is not None:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            st.enter_context(torch.cuda.stream(stream))
-            yield stream.cuda_stream
-        else:
-            yield torch.cuda.current_stream().cuda_stream
+_current_raw_stream = torch._C._cuda_getCurrentRawStream   # the handle alone: no Stream object per call
+
+
+def _run(dev: int, stream, f):
+    """f(handle of the stream) with device ``dev`` current, and the caller's stream for
+    what f allocates."""
+    if stream is None and dev == torch.cuda.current_device():
+        return f(_current_raw_stream(dev))
+    with torch.cuda.device(dev):
+        if stream is None:
+            return f(_current_raw_stream(dev))
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", dev))
+        with torch.cuda.stream(stream):
+            return f(stream.cuda_stream)
 
 
 def _dims(cache: torch.Tensor) -> Tuple[int, int, int, int]:
     """(pages, kv heads, page size, head dim) of a cache."""
-    if cache.dtype is not torch.uint8 or cache.dim() != 4 or cache.shape[3] % _UNIT_BYTES != 0:
+    if cache.dtype is not torch.uint8 or cache.dim() != 4:
+        raise ValueError("cache: uint8 [pages, kv heads, page_size / 16, 17 * head_dim] is expected")
+    pages, heads, units, width = cache.shape
+    if width % _UNIT_BYTES != 0:
         raise ValueError("cache: uint8 [pages, kv heads, page_size / 16, 17 * head_dim] is expected")
     if not cache.is_cuda or not cache.is_contiguous():
         raise ValueError("cache: a contiguous CUDA tensor is expected")
-    return cache.shape[0], cache.shape[1], cache.shape[2] * _UNIT, cache.shape[3] // _UNIT_BYTES
+    return pages, heads, units * _UNIT, width // _UNIT_BYTES
 
 
 def kda_kv4_cache(num_pages: int, num_kv_heads: int, page_size: int, head_dim: int, device="cuda") -> torch.Tensor:
@@ -137,35 +135,39 @@ def kda_page_map(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table:
     ``(cu_seqlens [N + 1], seq_lens [N], slot_map [num_tokens], positions
     [num_tokens], free_next [1])``."""
     lib = _lib()
-    if cached_lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
-        raise ValueError("cached_lens [N], block_table [N, max_pages], free_pages [F] are expected")
-    N, max_pages = cached_lens.shape[0], block_table.shape[1]
-    args = (_i32("cached_lens", cached_lens), _i32("new_lens", new_lens, (N,)), N,
-            _i32("block_table", block_table, (N, max_pages)), max_pages, _i32("free_pages", free_pages),
-            free_pages.shape[0], _i32("free_start", free_start, (1,)), page_size, num_tokens)
-    dev = _same_device(cached_lens, new_lens, block_table, free_pages, free_start)
+    dev = _device("cached_lens", cached_lens, torch.int32)
+    N = cached_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != N:
+        raise ValueError(f"block_table: [{N}, max_pages] expected, got {tuple(block_table.shape)}")
     if num_tokens < 0:
         raise ValueError("num_tokens < 0")
-    with _on(dev, stream) as st:
-        # one allocation; slot_map and positions begin on 16-byte boundaries
-        room = (num_tokens + 3) & ~3
-        buf = torch.empty(2 * room + 2 * N + 2, dtype=torch.int32, device=dev)
-        slots, pos, cu, lens, nxt, _ = buf.split_with_sizes([room, room, N + 1, N, 1, 0])
+    max_pages = block_table.shape[1]
+    args = (_i32("cached_lens", cached_lens, dev), _i32("new_lens", new_lens, dev, N), N,
+            _i32("block_table", block_table, dev, dim=2), max_pages, _i32("free_pages", free_pages, dev),
+            free_pages.numel(), _i32("free_start", free_start, dev, 1), page_size, num_tokens)
+    pad = -num_tokens & 3   # one allocation; slot_map and positions begin on 16-byte boundaries
+    room = num_tokens + pad
+
+    def call(st):
+        buf = torch.empty(2 * room + 2 * N + 2, dtype=torch.int32, device=cached_lens.device)
         p = buf.data_ptr()
         _check(lib.kda_page_map(*args, p + 8 * room, p + 4 * (2 * room + N + 1), p, p + 4 * room,
                                 p + 4 * (2 * room + 2 * N + 1), st), "kda_page_map")
-    if room != num_tokens:
-        slots, pos = slots[:num_tokens], pos[:num_tokens]
-    return cu, lens, slots, pos, nxt
+        slots, _, pos, _, cu, lens, nxt = buf.split_with_sizes((num_tokens, pad, num_tokens, pad, N + 1, N, 1))
+        return cu, lens, slots, pos, nxt
+
+    return _run(dev, stream, call)
 
 
-def _strided(name: str, t: torch.Tensor, heads: int, dim: int):
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name}: [tokens, {heads}, {dim}] expected, got {tuple(t.shape)}")
-    if not t.is_cuda or (t.stride(2) != 1 and dim > 1):
-        raise ValueError(f"{name}: a CUDA tensor with contiguous channels is expected")
-    # a stride over one entry has no meaning
-    return t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if heads > 1 else 0
+def _strided(name: str, t: torch.Tensor, heads: int, dim: int, dev: int) -> Tuple[int, int]:
+    """Token and head strides of [tokens, heads, dim] with contiguous channels."""
+    if t.dim() != 3 or t.get_device() != dev:
+        raise ValueError(f"{name}: [tokens, {heads}, {dim}] on cuda:{dev} expected, got {tuple(t.shape)} on {t.device}")
+    T, H, D = t.shape
+    ts, hs, cs = t.stride()
+    if H != heads or D != dim or cs != 1:
+        raise ValueError(f"{name}: [tokens, {heads}, {dim}] with contiguous channels expected, got {tuple(t.shape)}")
+    return ts if T > 1 else 0, hs if H > 1 else 0   # a stride over one entry has no meaning
 
 
 def kda_kv4_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, cache: torch.Tensor,
@@ -174,16 +176,15 @@ def kda_kv4_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, cac
     steps, such as parts of a fused projection) into the cache at slot_map ``[T]``
     int32; tokens with a negative slot are left out."""
     lib = _lib()
+    dev = _device("k", k)
     pages, H, ps, D = _dims(cache)
+    (kt, kh), (vt, vh) = _strided("k", k, H, D, dev), _strided("v", v, H, D, dev)
     T = k.shape[0]
-    (kt, kh), (vt, vh) = _strided("k", k, H, D), _strided("v", v, H, D)
-    if v.dtype is not k.dtype or v.shape[0] != T:
-        raise ValueError("k and v differ in type or length")
-    dev = _same_device(k, v, slot_map, cache)
-    dt, sl = _dtype(k.dtype), _i32("slot_map", slot_map, (T,))
-    with _on(dev, stream) as st:
-        _check(lib.kda_kv4_append(k.data_ptr(), v.data_ptr(), sl, T, H, D, kt, kh, vt, vh, dt, cache.data_ptr(),
-                                  pages, ps, st), "kda_kv4_append")
+    if v.dtype is not k.dtype or v.shape[0] != T or cache.get_device() != dev:
+        raise ValueError("k, v and the cache differ in type, length or device")
+    args = (k.data_ptr(), v.data_ptr(), _i32("slot_map", slot_map, dev, T), T, H, D, kt, kh, vt, vh, _dtype(k.dtype),
+            cache.data_ptr(), pages, ps)
+    _run(dev, stream, lambda st: _check(lib.kda_kv4_append(*args, st), "kda_kv4_append"))
 
 
 def kda_kv4_gather(cache: torch.Tensor, slot_map: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
@@ -192,17 +193,16 @@ def kda_kv4_gather(cache: torch.Tensor, slot_map: torch.Tensor, dtype: torch.dty
     of ``dtype``, zeros at negative slots."""
     lib = _lib()
     pages, H, ps, D = _dims(cache)
-    if slot_map.dim() != 1:
-        raise ValueError("slot_map: [T] is expected")
-    T = slot_map.shape[0]
-    dev = _same_device(cache, slot_map)
-    dt, sl = _dtype(dtype), _i32("slot_map", slot_map)
-    with _on(dev, stream) as st:
-        k = torch.empty((T, H, D), dtype=dtype, device=dev)
-        v = torch.empty((T, H, D), dtype=dtype, device=dev)
+    dev = cache.get_device()
+    dt, sl, T = _dtype(dtype), _i32("slot_map", slot_map, dev), slot_map.numel()
+
+    def call(st):
+        k, v = torch.empty((2, T, H, D), dtype=dtype, device=cache.device).unbind(0)
         _check(lib.kda_kv4_gather(cache.data_ptr(), pages, ps, sl, T, H, D, dt, k.data_ptr(), v.data_ptr(), st),
                "kda_kv4_gather")
-    return k, v
+        return k, v
+
+    return _run(dev, stream, call)
 
 
 def kda_kv4_attention_workspace_size(num_tokens: int, num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
@@ -228,31 +228,33 @@ def kda_kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.T
     Returns o ``[T, heads, head dim]``, and with ``return_lse`` the log of each row's
     sum of exponentials, fp32 ``[T, heads]``."""
     lib = _lib()
+    dev = _device("q", q)
     pages, H, ps, D = _dims(cache)
-    if q.dim() != 3 or q.shape[2] != D:
-        raise ValueError(f"q: [tokens, heads, {D}] expected, got {tuple(q.shape)}")
     T, Hq = q.shape[0], q.shape[1]
-    if block_table.dim() != 2:
-        raise ValueError("block_table: [N, max_pages] is expected")
+    qt, qh = _strided("q", q, Hq, D, dev)
+    if block_table.dim() != 2 or cache.get_device() != dev:
+        raise ValueError(f"block_table [N, max_pages] and the cache are expected on cuda:{dev}")
     N, max_pages = block_table.shape
-    qt, qh = _strided("q", q, Hq, D)
     dt = _dtype(q.dtype)
-    bt, ln = _i32("block_table", block_table), _i32("seq_lens", seq_lens, (N,))
-    cu = None if cu_seqlens is None else _i32("cu_seqlens", cu_seqlens, (N + 1,))
-    dev = _same_device(q, cache, block_table, seq_lens, cu_seqlens, o, workspace)
-    if o is not None and (o.dtype is not q.dtype or o.shape != q.shape or not o.is_contiguous()):
-        raise ValueError("o: a contiguous tensor of q's type and shape is expected")
-    need = lib.kda_kv4_attention_workspace_size(T, N, Hq, H, D, max_q_len, dt)
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace: a contiguous tensor is expected")
-    with _on(dev, stream) as st:
-        if o is None:
-            o = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if return_lse else None
+    bt, ln = _i32("block_table", block_table, dev, dim=2), _i32("seq_lens", seq_lens, dev, N)
+    cu = None if cu_seqlens is None else _i32("cu_seqlens", cu_seqlens, dev, N + 1)
+    if o is not None and (o.dtype is not q.dtype or o.shape != q.shape or not o.is_contiguous() or o.get_device() != dev):
+        raise ValueError("o: a contiguous tensor of q's type, shape and device is expected")
+    if workspace is not None and (not workspace.is_contiguous() or workspace.get_device() != dev):
+        raise ValueError(f"workspace: a contiguous tensor on cuda:{dev} is expected")
+    scale = D ** -0.5 if sm_scale is None else sm_scale
+
+    def call(st):
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device) if o is None else o
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if return_lse else None
         if workspace is None:
-            workspace = torch.empty(256 if need == (1 << 64) - 1 else need, dtype=torch.uint8, device=dev)
+            n = lib.kda_kv4_attention_workspace_size(T, N, Hq, H, D, max_q_len, dt)
+            ws = torch.empty(256 if n == (1 << 64) - 1 else n, dtype=torch.uint8, device=q.device)
+        else:
+            ws, n = workspace, workspace.numel() * workspace.element_size()
         _check(lib.kda_kv4_attention(q.data_ptr(), qt, qh, cache.data_ptr(), pages, ps, bt, max_pages, ln, cu, T, N, Hq, H,
-                                     D, max_q_len, D ** -0.5 if sm_scale is None else sm_scale, dt, o.data_ptr(),
-                                     None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), st), "kda_kv4_attention")
-    return (o, lse) if return_lse else o
+                                     D, max_q_len, scale, dt, out.data_ptr(), lse.data_ptr() if return_lse else None,
+                                     ws.data_ptr(), n, st), "kda_kv4_attention")
+        return (out, lse) if return_lse else out
+
+    return _run(dev, stream, call)
