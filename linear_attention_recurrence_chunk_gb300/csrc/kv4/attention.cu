@@ -36,37 +36,14 @@
 // kernel joins the pieces of a segment in their order.  Lengths are read on the
 // device; the cut needs one sum over the sequences, which every CTA takes itself.
 // Each warp feeds itself through a ring of tiles filled by bulk copies.
-#include <cuda_fp16.h>
-
-#include "internal.cuh"
-#include "../tc_ptx.cuh"
+#include "attn_common.cuh"
 
 namespace kda {
 namespace kv4 {
 namespace {
 
-constexpr long long kWaitLimit = 2000000000LL;   // ~1 s of SM clocks per bounded wait
 constexpr int kCtas = 152;                       // one persistent CTA per SM
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kFewSegments = 64;                 // up to so many segments, a CTA is one worker
-
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-// The four bytes of w, each two E2M1 codes, as fp16 pairs.
-__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&r)[4]) {
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-      : "r"(w));
-}
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -81,10 +58,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t pack(float a, float b) {
-  const __half2 v = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 // what pack() left of (a, b), packed
 __device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi) {
   const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
@@ -131,28 +104,15 @@ struct Parts {
   float* o;      // [2 workers][R][D]
 };
 
-struct Seq {
-  int32_t L, q0, qn, tiles, rts;
+// A sequence's tiles and row blocks.
+struct Work : Seq {
+  int32_t tiles, rts;
 };
 
 template <class C>
-__device__ __forceinline__ Seq seq_of(const AttnProblem& p, int n, bool* bad) {
-  Seq s;
-  const int64_t cap = p.num_pages > 0 ? (int64_t)p.max_pages * p.page_size : 0;
-  s.L = p.lens[n];
-  if (s.L < 0 || s.L > cap) {
-    *bad = true;
-    s.L = s.L < 0 ? 0 : (int32_t)cap;
-  }
-  s.q0 = n;
-  s.qn = 1;
-  if (p.cu) {
-    s.q0 = p.cu[n];
-    const int64_t qn = (int64_t)p.cu[n + 1] - s.q0;
-    const bool ok = s.q0 >= 0 && qn >= 0 && qn <= p.max_q && (int64_t)s.q0 + qn <= p.T;
-    if (!ok || (n == 0 && s.q0 != 0)) *bad = true;
-    s.qn = ok ? (int32_t)qn : 0;
-  }
+__device__ __forceinline__ Work work_of(const AttnProblem& p, int n, bool* bad) {
+  Work s;
+  static_cast<Seq&>(s) = seq_of(p, n, bad);
   s.tiles = s.L > 0 ? (s.L - 1) / C::TILE + 1 : 1;   // no token: one empty tile writes the zeros
   s.rts = (s.qn * (p.Hq / p.Hkv) + C::R - 1) / C::R;
   return s;
@@ -163,7 +123,7 @@ template <class C>
 struct Cursor {
   int n, seg, tile;   // sequence, its (head, row block) segment, first tile of the piece
   int64_t left;       // tiles of the worker's part from here on
-  Seq s;
+  Work s;
 
   __device__ __forceinline__ int count() const { return (int)min((int64_t)(s.tiles - tile), left); }
   __device__ __forceinline__ void next(const AttnProblem& p) {
@@ -173,7 +133,7 @@ struct Cursor {
     bool bad = false;
     if (++seg == p.Hkv * s.rts) {
       seg = 0;
-      do s = seq_of<C>(p, ++n, &bad);
+      do s = work_of<C>(p, ++n, &bad);
       while (s.rts == 0);   // tiles are left, so such a sequence follows
     }
   }
@@ -413,7 +373,7 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
   bool bad = false;
   int64_t mine = 0, segs = 0;
   for (int n = na + lane; n < nb; n += 32) {
-    const Seq s = seq_of<C>(p, n, &bad);
+    const Work s = work_of<C>(p, n, &bad);
     mine += (int64_t)s.tiles * s.rts;
     segs += s.rts;
   }
@@ -457,7 +417,7 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
       bool b = false;
       int64_t c = 0;
       if (n < p.N) {
-        const Seq s = seq_of<C>(p, n, &b);
+        const Work s = work_of<C>(p, n, &b);
         c = (int64_t)s.tiles * s.rts * p.Hkv;
       }
       int64_t inc = c;
@@ -472,7 +432,7 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
         const int64_t before = at + __shfl_sync(0xffffffffu, inc - c, src);
         cur.n = n0 + src;
         bool dummy = false;
-        cur.s = seq_of<C>(p, cur.n, &dummy);
+        cur.s = work_of<C>(p, cur.n, &dummy);
         cur.seg = (int)((x0 - before) / cur.s.tiles);
         cur.tile = (int)((x0 - before) % cur.s.tiles);
         break;
@@ -820,6 +780,12 @@ auto with_cfg(int32_t Hq, int32_t Hkv, int32_t D, int32_t max_q, kda_dtype dt, F
   return rows <= 8 ? f(Cfg<64, 1, 1>{}, z) : rows <= 16 ? f(Cfg<64, 2, 1>{}, z) : f(Cfg<64, 4, 1>{}, z);
 }
 
+// Whether the tiled kernel takes the call: bf16, and a sequence's rows fill at least one of
+// its blocks of 128 rows.
+bool extend_rows(const AttnProblem& p) {
+  const int64_t rows = (int64_t)p.max_q * (p.Hq / p.Hkv);
+  return p.dt == KDA_BF16 && rows >= 128 && (rows + 255) / 256 * p.N * p.Hkv <= INT32_MAX;
+}
 }  // namespace
 
 size_t attention_workspace(int32_t Hq, int32_t Hkv, int32_t D, int32_t max_q, kda_dtype dt) {
@@ -827,6 +793,7 @@ size_t attention_workspace(int32_t Hq, int32_t Hkv, int32_t D, int32_t max_q, kd
 }
 
 cudaError_t launch_attention(const AttnProblem& p, void* workspace, cudaStream_t stream) {
+  if (extend_rows(p)) return launch_extend(p, stream);
   return with_cfg(p.Hq, p.Hkv, p.D, p.max_q, p.dt,
                   [&](auto c, auto z) { return launch<decltype(c), decltype(z)>(p, workspace, stream); });
 }

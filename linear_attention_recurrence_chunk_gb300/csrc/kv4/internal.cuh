@@ -78,6 +78,7 @@ struct AttnProblem {
   int32_t* dev_err;
 };
 size_t attention_workspace(int32_t Hq, int32_t Hkv, int32_t D, int32_t max_q, kda_dtype dt);
+cudaError_t launch_extend(const AttnProblem& p, cudaStream_t stream);   // bf16 only
 cudaError_t launch_attention(const AttnProblem& p, void* workspace, cudaStream_t stream);
 
 }  // namespace kv4

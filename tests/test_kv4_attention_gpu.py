@@ -115,6 +115,34 @@ def test_several_query_tokens(dt, D, Hq, Hkv, qn):
     run_check(dt, D, Hq, Hkv, 32, qn, qn)          # a prompt from its beginning
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,ps,lens,qn", [
+    (4, 1, 64, [300], [130]),                       # rows of one and a part of a block, tiles before and on the edge
+    (8, 2, 16, [128, 257, 40], [128, 129, 40]),     # from the beginning of a prompt; tile-sized lengths
+    (3, 1, 48, [500, 90, 0, 7], [100, 86, 3, 20]),  # uneven row blocks, more query tokens than cached ones
+    (32, 2, 32, [201], [64]),                       # a token's heads fill a fraction of a block
+    (6, 6, 128, [260, 1000], [259, 1])])
+def test_query_chunks(D, Hq, Hkv, ps, lens, qn):
+    s = run_check(BF, D, Hq, Hkv, ps, lens, qn, spread=2.0)
+    a, b = s.run(), s.run()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_query_chunk_with_scales_that_grow_and_not_finite_tokens():
+    def grow(k, v, rng):
+        v *= np.ldexp(1.0, (np.arange(v.shape[0]) // 60))[:, None, None]
+        k *= np.ldexp(1.0, rng.integers(-3, 4, (k.shape[0], k.shape[1], 4)).repeat(32, -1))
+        k *= (1 + np.arange(k.shape[0]) / 100)[:, None, None]
+    run_check(BF, 128, 8, 2, 16, [400], [100], edit=grow)
+
+    def holes(k, v, rng):
+        k[350, 0, 3] = np.inf
+        v[330, 1, 100] = np.nan
+        v[20, 1, 5] = np.inf
+    s = run_check(BF, 128, 8, 2, 16, [400], [100], edit=holes)
+    assert torch.isnan(s.run()[0]).any() and not torch.isnan(s.run()[0]).all()
+
+
 def test_sequences_without_query_tokens():
     run_check(BF, 128, 8, 2, 16, [100, 50, 0, 20, 300], [1, 0, 0, 2, 0])
     run_check(BF, 128, 8, 2, 16, [100, 50, 0, 20, 300], [0, 0, 0, 0, 1])
