@@ -21,21 +21,23 @@
 // transposing move each (movmatrix), after a multiplication by the token's value
 // scale of the channel group.
 // Ranges.  A query row is scaled by a power of two to 2^14 <= max|q| < 2^15, which
-// is exact in fp16 but for channels 2^28 below the largest.  Weights are taken
-// relative to m_r and to the largest value scale 2^E seen: p 2^(15 - E) 2^e <= 2^15,
-// so a weight loses bits only when p 2^(e - E) is below 2^-29.  E below 2^-27 counts
-// as that.
+// is exact in fp16 but for channels 2^28 below the largest.  Weights are 2^15 at
+// most and multiplied, transposed, by the value scales relative to the largest one
+// seen, 2^(e - E), in fp16: exact where e - E >= -14 and a product is normal; a tile
+// with smaller ones multiplies in fp32 first.  So a weight loses bits only when
+// p 2^(e - E) is below 2^-29.  E below 2^-27 counts as that.  The output follows E.
 // fp32 inputs: q and the weights each as the sum of two fp16 numbers, two products
 // for one.
 //
-// Split.  The tiles of all (sequence, head, row block) segments form one line that
-// is cut into equal parts, one per worker, whatever the lengths; a worker is a
-// warp, or for few segments a whole CTA (its warps take the tiles of a segment in
-// turn and join in shared memory).  At most the first and the last piece of a
-// worker's part is not a whole segment: it goes to the workspace, and a second
-// kernel joins the pieces of a segment in their order.  Lengths are read on the
-// device; the cut needs one sum over the sequences, which every CTA takes itself.
-// Each warp feeds itself through a ring of tiles filled by bulk copies.
+// Split.  The tiles of all (sequence, head, row block) segments form one line, each
+// segment with a little room for its beginning and end, that is cut into equal
+// parts, one per worker, whatever the lengths; a worker is a warp, or for few
+// segments a whole CTA (its warps take the tiles of a segment in turn and join in
+// shared memory).  At most the first and the last piece of a worker's part is not a
+// whole segment: it goes to the workspace, and a second kernel joins the pieces of a
+// segment in their order.  Lengths are read on the device; the cut needs one sum over
+// the sequences, which every CTA takes itself.  Each warp feeds itself through a ring
+// of tiles filled by bulk copies.
 #include "attn_common.cuh"
 
 namespace kda {
@@ -52,6 +54,14 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// c = a b
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -62,6 +72,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 __device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi) {
   const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
   return pack(a - h.x, b - h.y);
+}
+
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -84,17 +99,22 @@ struct Cfg {
   static constexpr int R = 8 * NT;                  // query rows of a segment
   static constexpr int MT = NT == 1 ? 4 : 2;        // units of a tile
   static constexpr int TILE = kUnit * MT;
-  static constexpr int STAGES = NT == 1 ? 2 : 4;
-  static constexpr bool QREG = NT <= 2 && PARTS == 1;   // q operands in registers
-  static constexpr int W = QREG ? 12 : 8;           // warps of a CTA
+  static constexpr int STAGES = NT == 1 ? 2 : NT == 2 && PARTS == 1 ? 3 : 4;
+  static constexpr bool QREG = NT == 1 && PARTS == 1;   // q operands in registers
+  static constexpr int W = NT <= 2 && PARTS == 1 ? 12 : 8;   // warps of a CTA
+  static constexpr int HEAD = NT == 1 ? 1 : 2;      // room of a segment's beginning and end on the line, in tiles
   static constexpr int GR = D / 32, KS = D / 16;
   static constexpr int kStage = MT * Unit<D>::kBytes, kRing = STAGES * kStage;
   static constexpr int kQ = QREG ? 0 : KS * NT * PARTS * 256;
+  // a warp's tables: a tile's scales, of keys as fp32 [token][group], of values as fp16
+  // [token pair][group][2]; the rows' score factors and last tokens
+  static constexpr int tV = TILE * GR * 4, tRow = tV + TILE * GR * 2, kTab = tRow + R * 8;
   static constexpr int kPart = R * (D + 2) * 4;     // a warp's result in shared memory: O, then (m, l)
-  static constexpr int oQ = W * kRing, oBar = oQ + W * kQ, oSum = oBar + W * STAGES * 8, kSmem = oSum + (W + 1) * 8;
+  static constexpr int oQ = W * kRing, oTab = oQ + W * kQ, oBar = oTab + W * kTab, oSum = oBar + W * STAGES * 8,
+                       kSmem = oSum + (W + 3) * 8;
   static_assert(kPart <= kRing, "a warp's result fits its ring");
   static_assert(kSmem <= 232448, "shared memory");
-  static_assert(kStage % 16 == 0 && kRing % 128 == 0, "alignment");
+  static_assert(kStage % 16 == 0 && kRing % 128 == 0 && kTab % 16 == 0, "alignment");
 };
 
 // Pieces in the workspace: slot 2 w is the first piece of worker w, 2 w + 1 its last.
@@ -118,23 +138,25 @@ __device__ __forceinline__ Work work_of(const AttnProblem& p, int n, bool* bad) 
   return s;
 }
 
-// A worker's place on the line of tiles.
+// A worker's place on the line: a segment takes HEAD + tiles of it.
 template <class C>
 struct Cursor {
-  int n, seg, tile;   // sequence, its (head, row block) segment, first tile of the piece
-  int64_t left;       // tiles of the worker's part from here on
+  int n, seg, pos;    // sequence, its (head, row block) segment, place in the segment
+  int64_t left;       // what is left of the worker's part
   Work s;
 
-  __device__ __forceinline__ int count() const { return (int)min((int64_t)(s.tiles - tile), left); }
+  __device__ __forceinline__ int span() const { return (int)min((int64_t)(C::HEAD + s.tiles - pos), left); }
+  __device__ __forceinline__ int first() const { return max(pos - C::HEAD, 0); }             // tiles of the piece
+  __device__ __forceinline__ int last() const { return max(pos + span() - C::HEAD, 0); }     // (one behind)
   __device__ __forceinline__ void next(const AttnProblem& p) {
-    left -= count();
-    tile = 0;
+    left -= span();
+    pos = 0;
     if (left <= 0) return;
     bool bad = false;
     if (++seg == p.Hkv * s.rts) {
       seg = 0;
       do s = work_of<C>(p, ++n, &bad);
-      while (s.rts == 0);   // tiles are left, so such a sequence follows
+      while (s.rts == 0);   // something is left, so such a sequence follows
     }
   }
 };
@@ -142,32 +164,105 @@ struct Cursor {
 template <class C>
 struct Acc {
   float O[2 * C::GR][C::NT][4];
-  float m[C::NT][2], ref[C::NT][2], l[C::NT][2];   // running maximum (log2), reference m + E - 142, sum relative to it
+  float m[C::NT][2], l[C::NT][2];   // running maximum (log2) and sum of 2^(s - m + 15) of each column
 };
 
-// One tile.  kSlow: rows see only a part of it, or it holds a group that is not finite.
-template <class C, bool kSlow>
-__device__ __forceinline__ void tile_step(uint8_t* st, const uint32_t (&qr)[C::QREG ? C::NT : 1][C::QREG ? C::KS : 1][2],
-                                          const uint8_t* qs, const float (&cf)[C::NT][2], const int (&lim)[C::NT][2],
-                                          int tok0, int E, Acc<C>& a) {
+// A tile's scales into the warp's tables; E becomes the largest value scale so far.
+// Returns whether the tile needs the careful step: a group that is not finite, or a
+// value scale that is not a normal fp16 number relative to E.
+template <class C>
+__device__ __forceinline__ bool load_scales(const uint8_t* st, uint8_t* tab, int left, int& E) {
+  using U = Unit<C::D>;
+  const int lane = threadIdx.x & 31;
+  constexpr uint32_t kOnes = C::GR == 4 ? 0x01010101u : 0x0101u;
+  uint32_t k[2] = {0, 0}, v[2] = {0, 0};   // of tokens 2 lane, 2 lane + 1; a byte per group
+  const bool in = lane < C::TILE / 2;
+  if (in) {
+    const uint8_t* u = st + (lane / 8) * U::kBytes + U::kKs + (lane % 8) * 2 * C::GR;
+    if constexpr (C::GR == 4) {
+      const uint2 a = *reinterpret_cast<const uint2*>(u), b = *reinterpret_cast<const uint2*>(u + C::D / 2);
+      k[0] = a.x; k[1] = a.y; v[0] = b.x; v[1] = b.y;
+    } else {
+      const uint32_t a = *reinterpret_cast<const uint32_t*>(u), b = *reinterpret_cast<const uint32_t*>(u + C::D / 2);
+      k[0] = a & 0xffffu; k[1] = a >> 16; v[0] = b & 0xffffu; v[1] = b >> 16;
+    }
+  }
+  if (left < C::TILE) {   // tokens behind the last: 0, whatever the cache holds there
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (2 * lane + i >= left) k[i] = v[i] = 0;
+  }
+  const uint32_t kt = __vmaxu4(k[0], k[1]), vt = __vmaxu4(v[0], v[1]);
+  uint32_t vl = in ? __vminu4(v[0], v[1]) : 0xffffffffu;
+  if constexpr (C::GR == 2) vl |= 0xffff0000u;
+  auto top = [](uint32_t w) { return max(max(w & 0xffu, w >> 8 & 0xffu), max(w >> 16 & 0xffu, w >> 24)); };
+  auto low = [](uint32_t w) { return min(min(w & 0xffu, w >> 8 & 0xffu), min(w >> 16 & 0xffu, w >> 24)); };
+  uint32_t vm = __reduce_max_sync(0xffffffffu, top(vt));
+  const uint32_t lo = __reduce_min_sync(0xffffffffu, low(vl));
+  const bool nan = __any_sync(0xffffffffu, top(kt) == 255u) || vm == 255u;
+  if (nan) vm = __reduce_max_sync(0xffffffffu, max(top(v[0] & ~__vcmpeq4(v[0], ~0u)), top(v[1] & ~__vcmpeq4(v[1], ~0u))));
+  E = max(E, (int)vm);
+  const bool careful = nan || (int)lo < E - 14;
+  if (in) {
+    float* kf = reinterpret_cast<float*>(tab) + 2 * lane * C::GR;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float f[C::GR];
+#pragma unroll
+      for (int j = 0; j < C::GR; ++j) {
+        f[j] = scale_f32(k[i] >> (8 * j) & 0xffu);
+        if (nan) f[j] = f[j] == INFINITY ? __uint_as_float(0x7fffffffu) : f[j];
+      }
+      if constexpr (C::GR == 4) reinterpret_cast<float4*>(kf)[i] = make_float4(f[0], f[1], f[2], f[3]);
+      else reinterpret_cast<float2*>(kf)[i] = make_float2(f[0], f[1]);
+    }
+    if (!careful) {   // exponent fields between 1 and 15
+      const uint32_t base = (uint32_t)(E - 15) * kOnes, a = v[0] - base, b = v[1] - base;
+      uint32_t h[C::GR];
+#pragma unroll
+      for (int j = 0; j < C::GR; ++j) h[j] = (__byte_perm(a, b, j | (4 + j) << 8) & 0x001f001fu) << 10;
+      uint8_t* vf = tab + C::tV + lane * C::GR * 4;
+      if constexpr (C::GR == 4) *reinterpret_cast<uint4*>(vf) = make_uint4(h[0], h[1], h[2], h[3]);
+      else *reinterpret_cast<uint2*>(vf) = make_uint2(h[0], h[1]);
+    } else {          // the careful step takes the bytes: of tokens that are there
+      uint32_t* vw = reinterpret_cast<uint32_t*>(tab + C::tV) + 2 * lane;
+      vw[0] = v[0];
+      vw[1] = v[1];
+    }
+  }
+  __syncwarp();
+  return careful;
+}
+
+// One tile.  kCut: rows see only a part of it.  kCareful: see load_scales.
+template <class C, bool kCut, bool kCareful>
+__device__ __forceinline__ void tile_step(const uint8_t* st, const uint8_t* tab,
+                                          const uint32_t (&qr)[C::QREG ? C::NT : 1][C::QREG ? C::KS : 1][2],
+                                          const uint8_t* qs, int tok0, int E, float moved, Acc<C>& a) {
   using U = Unit<C::D>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const float2* cfs = reinterpret_cast<const float2*>(tab + C::tRow) + t;                 // of columns 2 t, 2 t + 1
+  const int2* lims = reinterpret_cast<const int2*>(tab + C::tRow + C::R * 4) + t;
   float S[C::MT][C::NT][4];
 #pragma unroll
   for (int mt = 0; mt < C::MT; ++mt) {
     const uint8_t* u = st + mt * U::kBytes;
-    uint32_t kw[2][C::GR], ks[2];
+    uint32_t kw[2][C::GR];
+    float ks[2][C::GR];
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       const uint8_t* row = u + U::key_word(g + 8 * hf, 0, t);
+      const float* sc = reinterpret_cast<const float*>(tab) + (mt * kUnit + g + 8 * hf) * C::GR;
       if constexpr (C::GR == 4) {
         const uint4 x = *reinterpret_cast<const uint4*>(row);
         kw[hf][0] = x.x; kw[hf][1] = x.y; kw[hf][2] = x.z; kw[hf][3] = x.w;
-        ks[hf] = *reinterpret_cast<const uint32_t*>(u + U::kKs + (g + 8 * hf) * 4);
+        const float4 f = *reinterpret_cast<const float4*>(sc);
+        ks[hf][0] = f.x; ks[hf][1] = f.y; ks[hf][2] = f.z; ks[hf][3] = f.w;
       } else {
         const uint2 x = *reinterpret_cast<const uint2*>(row);
         kw[hf][0] = x.x; kw[hf][1] = x.y;
-        ks[hf] = *reinterpret_cast<const uint16_t*>(u + U::kKs + (g + 8 * hf) * 2);
+        const float2 f = *reinterpret_cast<const float2*>(sc);
+        ks[hf][0] = f.x; ks[hf][1] = f.y;
       }
     }
 #pragma unroll
@@ -175,41 +270,53 @@ __device__ __forceinline__ void tile_step(uint8_t* st, const uint32_t (&qr)[C::Q
       uint32_t r0[4], r1[4];
       e2m1x8(kw[0][j], r0);
       e2m1x8(kw[1][j], r1);
-      const float s0 = scale_at<kSlow>(ks[0], j), s1 = scale_at<kSlow>(ks[1], j);
 #pragma unroll
       for (int nt = 0; nt < C::NT; ++nt) {
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        float c[4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if constexpr (C::QREG) {
-            mma16816(c, r0[2 * h], r1[2 * h], r0[2 * h + 1], r1[2 * h + 1], qr[nt][2 * j + h][0], qr[nt][2 * j + h][1]);
-          } else {
 #pragma unroll
-            for (int part = 0; part < C::PARTS; ++part) {
+          for (int part = 0; part < C::PARTS; ++part) {
+            uint32_t b0, b1;
+            if constexpr (C::QREG) {
+              b0 = qr[nt][2 * j + h][0];
+              b1 = qr[nt][2 * j + h][1];
+            } else {
               const uint2 b = *reinterpret_cast<const uint2*>(qs + ((part * C::KS + 2 * j + h) * C::NT + nt) * 256 + lane * 8);
-              mma16816(c, r0[2 * h], r1[2 * h], r0[2 * h + 1], r1[2 * h + 1], b.x, b.y);
+              b0 = b.x;
+              b1 = b.y;
             }
+            if (h == 0 && part == 0) mma16816_first(c, r0[2 * h], r1[2 * h], r0[2 * h + 1], r1[2 * h + 1], b0, b1);
+            else mma16816(c, r0[2 * h], r1[2 * h], r0[2 * h + 1], r1[2 * h + 1], b0, b1);
           }
         }
         float(&s)[4] = S[mt][nt];
-        s[0] = j ? fmaf(s0, c[0], s[0]) : s0 * c[0];
-        s[1] = j ? fmaf(s0, c[1], s[1]) : s0 * c[1];
-        s[2] = j ? fmaf(s1, c[2], s[2]) : s1 * c[2];
-        s[3] = j ? fmaf(s1, c[3], s[3]) : s1 * c[3];
+        s[0] = j ? fmaf(ks[0][j], c[0], s[0]) : ks[0][j] * c[0];
+        s[1] = j ? fmaf(ks[0][j], c[1], s[1]) : ks[0][j] * c[1];
+        s[2] = j ? fmaf(ks[1][j], c[2], s[2]) : ks[1][j] * c[2];
+        s[3] = j ? fmaf(ks[1][j], c[3], s[3]) : ks[1][j] * c[3];
       }
     }
-    if constexpr (kSlow) {
+    if constexpr (kCut) {
 #pragma unroll
-      for (int nt = 0; nt < C::NT; ++nt)
+      for (int nt = 0; nt < C::NT; ++nt) {
+        const int2 lim = lims[4 * nt];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (tok0 + mt * kUnit + g + 8 * (e >> 1) > lim[nt][e & 1]) S[mt][nt][e] = -INFINITY;
+          if (tok0 + mt * kUnit + g + 8 * (e >> 1) > (e & 1 ? lim.y : lim.x)) S[mt][nt][e] = -INFINITY;
+      }
     }
   }
 
-  // running maximum and reference of each column; the accumulators follow them
-  bool move = false;
-  float f[C::NT][2];
+  // running maximum of each column; the accumulators follow it, and E by `moved`
+  bool move = moved != 1.f;
+  float f[C::NT][2], ref[C::NT][2], cf[C::NT][2];
+#pragma unroll
+  for (int nt = 0; nt < C::NT; ++nt) {
+    const float2 x = cfs[4 * nt];
+    cf[nt][0] = x.x;
+    cf[nt][1] = x.y;
+  }
 #pragma unroll
   for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
@@ -221,22 +328,22 @@ __device__ __forceinline__ void tile_step(uint8_t* st, const uint32_t (&qr)[C::Q
       x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
       x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
       const float m = fmaxf(a.m[nt][e], x * cf[nt][e]);
-      const float ref = (m == -INFINITY ? 0.f : m) + (float)(E - 142);
       // a row that has seen nothing has nothing to follow
-      f[nt][e] = a.m[nt][e] == -INFINITY ? 1.f : ex2(a.ref[nt][e] - ref);
+      f[nt][e] = a.m[nt][e] == -INFINITY ? 1.f : ex2(a.m[nt][e] - m);
       move |= f[nt][e] != 1.f;
       a.m[nt][e] = m;
-      a.ref[nt][e] = ref;
+      ref[nt][e] = (m == -INFINITY ? 0.f : m) - 15.f;
     }
   if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
     for (int nt = 0; nt < C::NT; ++nt) {
       a.l[nt][0] *= f[nt][0];
       a.l[nt][1] *= f[nt][1];
+      const float fo[2] = {f[nt][0] * moved, f[nt][1] * moved};
 #pragma unroll
       for (int i = 0; i < 2 * C::GR; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) a.O[i][nt][e] *= f[nt][e & 1];
+        for (int e = 0; e < 4; ++e) a.O[i][nt][e] *= fo[e & 1];
     }
   }
 #pragma unroll
@@ -244,34 +351,52 @@ __device__ __forceinline__ void tile_step(uint8_t* st, const uint32_t (&qr)[C::Q
 #pragma unroll
     for (int nt = 0; nt < C::NT; ++nt) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) S[mt][nt][e] = ex2(fmaf(S[mt][nt][e], cf[nt][e & 1], -a.ref[nt][e & 1]));
+      for (int e = 0; e < 4; ++e) S[mt][nt][e] = ex2(fmaf(S[mt][nt][e], cf[nt][e & 1], -ref[nt][e & 1]));
       a.l[nt][0] += S[mt][nt][0] + S[mt][nt][2];
       a.l[nt][1] += S[mt][nt][1] + S[mt][nt][3];
     }
 
+  const float to_e = kCareful ? __uint_as_float(E < 254 ? (uint32_t)(254 - E) << 23 : 0x00400000u) : 1.f;   // 2^(127 - E)
 #pragma unroll
   for (int mt = 0; mt < C::MT; ++mt) {
     const uint8_t* u = st + mt * U::kBytes;
     uint32_t xy[2][2][C::GR / 2];   // [8-token block][even or odd channel]: bytes of token pairs
-    uint32_t vs[2];
+    uint32_t vs[2][C::GR];          // [8-token block]: scales of the tokens 2 t, 2 t + 1
+    uint32_t pk[2][C::NT][C::PARTS];   // transposed weights of a block
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const uint8_t* at = u + U::val_half(8 * b + 2 * t, 0, g);
       uint32_t w[C::GR];
+      const uint8_t* sc = tab + C::tV + (mt * 8 + 4 * b + t) * C::GR * 4;
       if constexpr (C::GR == 4) {
         const uint4 x = *reinterpret_cast<const uint4*>(at);
         w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-        vs[b] = *reinterpret_cast<const uint32_t*>(u + U::kVs + (g + 8 * b) * 4);
+        if constexpr (!kCareful) {
+          const uint4 f = *reinterpret_cast<const uint4*>(sc);
+          vs[b][0] = f.x; vs[b][1] = f.y; vs[b][2] = f.z; vs[b][3] = f.w;
+        }
       } else {
         const uint2 x = *reinterpret_cast<const uint2*>(at);
         w[0] = x.x; w[1] = x.y;
-        vs[b] = *reinterpret_cast<const uint16_t*>(u + U::kVs + (g + 8 * b) * 2);
+        if constexpr (!kCareful) {
+          const uint2 f = *reinterpret_cast<const uint2*>(sc);
+          vs[b][0] = f.x; vs[b][1] = f.y;
+        }
       }
 #pragma unroll
       for (int i = 0; i < C::GR / 2; ++i) {
         const uint32_t A = w[i], B = w[C::GR / 2 + i];
         xy[b][0][i] = (A & 0x0f0f0f0fu) | ((B << 4) & 0xf0f0f0f0u);
         xy[b][1][i] = ((A >> 4) & 0x0f0f0f0fu) | (B & 0xf0f0f0f0u);
+      }
+      if constexpr (!kCareful) {
+#pragma unroll
+        for (int nt = 0; nt < C::NT; ++nt) {
+          const float p0 = S[mt][nt][2 * b], p1 = S[mt][nt][2 * b + 1];
+          const uint32_t hi = pack(p0, p1);
+          pk[b][nt][0] = transpose8x8(hi);
+          if constexpr (C::PARTS == 2) pk[b][nt][C::PARTS - 1] = transpose8x8(pack_rest(p0, p1, hi));
+        }
       }
     }
 #pragma unroll
@@ -284,60 +409,36 @@ __device__ __forceinline__ void tile_step(uint8_t* st, const uint32_t (&qr)[C::Q
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int j = 2 * i + k;
-        const float s0 = scale_at<kSlow>(vs[0], j), s1 = scale_at<kSlow>(vs[1], j);
 #pragma unroll
         for (int nt = 0; nt < C::NT; ++nt) {
-          float(&s)[4] = S[mt][nt];
-          float w[4] = {s[0] * s0, s[1] * s0, s[2] * s1, s[3] * s1};
-          if constexpr (kSlow) {   // a token that a row does not see adds nothing to it, whatever its values are
+          uint32_t b[2][C::PARTS];
+          if constexpr (!kCareful) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (s[e] == 0.f) w[e] = 0.f;
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+              for (int part = 0; part < C::PARTS; ++part) b[hf][part] = mul2(pk[hf][nt][part], vs[hf][j]);
+          } else {
+            const uint32_t* vw = reinterpret_cast<const uint32_t*>(tab + C::tV) + mt * kUnit;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {   // the token of this lane's two weights
+              const float sc = scale_at<true>(vw[g + 8 * hf], j) * to_e;
+              const float p0 = S[mt][nt][2 * hf], p1 = S[mt][nt][2 * hf + 1];
+              // a token that a row does not see adds nothing to it, whatever its values are
+              const float w0 = p0 == 0.f ? 0.f : p0 * sc, w1 = p1 == 0.f ? 0.f : p1 * sc;
+              const uint32_t hi = pack(w0, w1);
+              b[hf][0] = transpose8x8(hi);
+              if constexpr (C::PARTS == 2) b[hf][C::PARTS - 1] = transpose8x8(pack_rest(w0, w1, hi));
+            }
           }
-          const uint32_t h0 = pack(w[0], w[1]), h1 = pack(w[2], w[3]);
-          const uint32_t b0 = transpose8x8(h0), b1 = transpose8x8(h1);
-          mma16816(a.O[2 * j][nt], x0[2 * k], y0[2 * k], x1[2 * k], y1[2 * k], b0, b1);
-          mma16816(a.O[2 * j + 1][nt], x0[2 * k + 1], y0[2 * k + 1], x1[2 * k + 1], y1[2 * k + 1], b0, b1);
-          if constexpr (C::PARTS == 2) {
-            const uint32_t c0 = transpose8x8(pack_rest(w[0], w[1], h0)), c1 = transpose8x8(pack_rest(w[2], w[3], h1));
-            mma16816(a.O[2 * j][nt], x0[2 * k], y0[2 * k], x1[2 * k], y1[2 * k], c0, c1);
-            mma16816(a.O[2 * j + 1][nt], x0[2 * k + 1], y0[2 * k + 1], x1[2 * k + 1], y1[2 * k + 1], c0, c1);
+#pragma unroll
+          for (int part = 0; part < C::PARTS; ++part) {
+            mma16816(a.O[2 * j][nt], x0[2 * k], y0[2 * k], x1[2 * k], y1[2 * k], b[0][part], b[1][part]);
+            mma16816(a.O[2 * j + 1][nt], x0[2 * k + 1], y0[2 * k + 1], x1[2 * k + 1], y1[2 * k + 1], b[0][part], b[1][part]);
           }
         }
       }
     }
   }
-}
-
-// The largest finite value-scale byte of a tile, and whether a key or value scale in it is 255.
-template <class C>
-__device__ __forceinline__ int tile_scales(const uint8_t* st, bool* special) {
-  using U = Unit<C::D>;
-  const int lane = threadIdx.x & 31;
-  constexpr int kWords = C::D / 8;   // 32-bit words of value scales per unit (as many of key scales)
-  uint32_t k4 = 0, v4 = 0;
-#pragma unroll
-  for (int i = 0; i < (C::MT * kWords + 31) / 32; ++i) {
-    const int w = lane + 32 * i;
-    if (w < C::MT * kWords) {
-      const uint8_t* u = st + (w / kWords) * U::kBytes + U::kKs + (w % kWords) * 4;
-      k4 = __vmaxu4(k4, *reinterpret_cast<const uint32_t*>(u));
-      v4 = __vmaxu4(v4, *reinterpret_cast<const uint32_t*>(u + C::D / 2));
-    }
-  }
-  uint32_t both = __vmaxu4(k4, v4);
-  both = __vmaxu4(both, both >> 16);
-  *special = __any_sync(0xffffffffu, (both & 0xffu) == 255u || (both >> 8 & 0xffu) == 255u);
-  if (*special) {
-    v4 = 0;
-    for (int w = lane; w < C::MT * kWords; w += 32) {
-      const uint32_t x = *reinterpret_cast<const uint32_t*>(st + (w / kWords) * U::kBytes + U::kVs + (w % kWords) * 4);
-      v4 = __vmaxu4(v4, x & ~__vcmpeq4(x, 0xffffffffu));
-    }
-  }
-  v4 = __vmaxu4(v4, v4 >> 16);
-  const uint32_t top = max(v4 & 0xffu, v4 >> 8 & 0xffu);
-  return (int)__reduce_max_sync(0xffffffffu, top);
 }
 
 // Result rows: o (of the type) and lse, or a piece for the join.
@@ -362,19 +463,20 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   uint8_t* ring = sm + warp * C::kRing;
   uint8_t* qs = sm + C::oQ + warp * C::kQ;
+  uint8_t* tab = sm + C::oTab + warp * C::kTab;
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::oBar) + warp * C::STAGES;
   int64_t* sums = reinterpret_cast<int64_t*>(sm + C::oSum);
   const int G = p.Hq / p.Hkv;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- the line: tiles and segments of every sequence, a range of sequences per warp
+  // ---- the line: the room of every sequence's segments, a range of sequences per warp
   const int per = (p.N + C::W - 1) / C::W;
   const int na = min(warp * per, p.N), nb = min(na + per, p.N);
   bool bad = false;
   int64_t mine = 0, segs = 0;
   for (int n = na + lane; n < nb; n += 32) {
     const Work s = work_of<C>(p, n, &bad);
-    mine += (int64_t)s.tiles * s.rts;
+    mine += (int64_t)(C::HEAD + s.tiles) * s.rts;
     segs += s.rts;
   }
   if (bad && blockIdx.x == 0) report_bad(p.dev_err);
@@ -404,7 +506,11 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
     if (lane == 0) *own_at = make_int4(0, 0, 0, 0);
     return;
   }
-  const int64_t x0 = me * total / workers, x1 = (me + 1) * total / workers;
+  const int64_t x0 = me * total / workers;
+  if (threadIdx.x == 0) {   // read again at the end of a part that a segment outlasts: fewer registers in the loop
+    sums[C::W + 1] = total;
+    sums[C::W + 2] = workers;
+  }
 
   Cursor<C> cur;   // find x0: the warp's range, then the sequence
   {
@@ -418,7 +524,7 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
       int64_t c = 0;
       if (n < p.N) {
         const Work s = work_of<C>(p, n, &b);
-        c = (int64_t)s.tiles * s.rts * p.Hkv;
+        c = (int64_t)(C::HEAD + s.tiles) * s.rts * p.Hkv;
       }
       int64_t inc = c;
 #pragma unroll
@@ -433,13 +539,13 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
         cur.n = n0 + src;
         bool dummy = false;
         cur.s = work_of<C>(p, cur.n, &dummy);
-        cur.seg = (int)((x0 - before) / cur.s.tiles);
-        cur.tile = (int)((x0 - before) % cur.s.tiles);
+        cur.seg = (int)((x0 - before) / (C::HEAD + cur.s.tiles));
+        cur.pos = (int)((x0 - before) % (C::HEAD + cur.s.tiles));
         break;
       }
       at += __shfl_sync(0xffffffffu, inc, 31);
     }
-    cur.left = x1 - x0;
+    cur.left = (me + 1) * total / workers - x0;
   }
   const int wi = wide ? warp : 0, step = wide ? C::W : 1;
 
@@ -448,41 +554,43 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
   int pk = wi;          // tile of its piece
   uint32_t issued = 0, used = 0;
   bool ok = true;
-  const int upp = p.page_size / kUnit;
+  const uint32_t upp = p.page_size / kUnit;
+  const bool in_page = upp % C::MT == 0;                    // a tile lies in one page
   auto produce = [&]() {
-    while (pc.left > 0 && pk >= pc.count()) {
+    while (pc.left > 0 && pc.first() + pk >= pc.last()) {
       if (wide) return;   // the next piece's tiles follow once this one's result is joined
       pc.next(p);
       pk = wi;
     }
     if (pc.left <= 0) return;
-    const int tile = pc.tile + pk;
+    const int tile = pc.first() + pk;
     pk += step;
     const int slot = issued % C::STAGES;
     ++issued;
     const int units = min(C::MT, (pc.s.L + kUnit - 1) / kUnit - tile * C::MT);   // 0 for an empty sequence
     if (lane == 0) tc::mbar_arrive_expect_tx(full + slot, units * U::kBytes);
     __syncwarp();
-    const bool whole = upp % C::MT == 0;   // a tile lies in one page
-    if (lane < (whole ? min(units, 1) : units)) {
-      const int unit = tile * C::MT + lane;
-      int64_t page = p.table[(int64_t)pc.n * p.max_pages + unit / upp];
+    if (lane < (in_page ? min(units, 1) : units)) {
+      const uint32_t unit = tile * C::MT + lane, at = (uint32_t)(unit * p.upp_inv >> 40);
+      int64_t page = p.table[(int64_t)pc.n * p.max_pages + at];
       if (page < 0 || page >= p.num_pages) {
         report_bad(p.dev_err);
         page = 0;
       }
       const int h = pc.seg / pc.s.rts;
       bulk_g2s(tc::smem_u32(ring + slot * C::kStage + lane * U::kBytes),
-               p.cache + ((page * p.Hkv + h) * upp + unit % upp) * U::kBytes, (whole ? units : 1) * U::kBytes, full + slot);
+               p.cache + ((page * p.Hkv + h) * upp + (unit - at * upp)) * U::kBytes, (in_page ? units : 1) * U::kBytes, full + slot);
     }
   };
   for (int i = 0; i < C::STAGES; ++i) produce();
 
   int4 owner = make_int4(0, 0, 0, 0);
+  bool joined = false;
   for (; cur.left > 0; cur.next(p)) {
-    const int cnt = cur.count(), rt = cur.seg % cur.s.rts, h = cur.seg / cur.s.rts;
+    const int first = cur.first(), last = cur.last(), rt = cur.seg % cur.s.rts, h = cur.seg / cur.s.rts;
+    if (first == last) continue;   // the part ends in the room before the segment's first tile
     const int rows = min(C::R, cur.s.qn * G - rt * C::R);
-    if (wide && cur.left != x1 - x0) {   // the ring was used to join the last piece
+    if (wide && joined) {   // the ring was used to join the last piece
       pc = cur;
       pk = wi;
       for (int i = 0; i < C::STAGES; ++i) produce();
@@ -490,8 +598,6 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
 
     // q rows as operands, each scaled by a power of two
     uint32_t qr[C::QREG ? C::NT : 1][C::QREG ? C::KS : 1][2];
-    float cf[C::NT][2];
-    int lim[C::NT][2];
     __syncwarp();   // the last piece's operands have been read
 #pragma unroll
     for (int nt = 0; nt < C::NT; ++nt) {
@@ -502,7 +608,7 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
       for (int j = 0; j < C::GR; ++j) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[j][i] = 0.f;
-        if (r < rows) {
+        if (r < rows && cur.s.L > 0) {
           const int rr = rt * C::R + r;
           const T* src = static_cast<const T*>(p.q) + ((int64_t)cur.s.q0 + rr / G) * p.qt + (int64_t)(h * G + rr % G) * p.qh +
                          32 * j + 8 * t;
@@ -529,12 +635,9 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
       // the sign of sm_scale goes with q, so that the factor of a score is positive
       const float up = copysignf(__uint_as_float((268u - ex) << 23), p.sm_scale);
       const float down = fmaxf(__uint_as_float((ex - 14u) << 23) * fabsf(p.sm_scale) * kLog2e, 1.17549435e-38f);
-      cf[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);
-      cf[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int c = nt * 8 + 2 * t + e;
-        lim[nt][e] = c < rows ? cur.s.L - cur.s.qn + (rt * C::R + c) / G : -1;
+      if (t == 0) {
+        reinterpret_cast<float*>(tab + C::tRow)[r] = down;
+        reinterpret_cast<int*>(tab + C::tRow + C::R * 4)[r] = r < rows ? cur.s.L - cur.s.qn + (rt * C::R + r) / G : -1;
       }
 #pragma unroll
       for (int ks = 0; ks < C::KS; ++ks) {
@@ -561,41 +664,30 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         a.m[nt][e] = -INFINITY;
-        a.ref[nt][e] = a.l[nt][e] = 0.f;
+        a.l[nt][e] = 0.f;
 #pragma unroll
         for (int i = 0; i < 2 * C::GR; ++i) a.O[i][nt][e] = a.O[i][nt][e + 2] = 0.f;
       }
     int E = 100;
-    for (int k = wi; k < cnt; k += step) {
-      const int tile = cur.tile + k, slot = used % C::STAGES, tok0 = tile * C::TILE;
-      uint8_t* st = ring + slot * C::kStage;
+    for (int tile = first + wi; tile < last; tile += step) {
+      const int slot = used % C::STAGES, tok0 = tile * C::TILE;
+      const uint8_t* st = ring + slot * C::kStage;
       if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(full + slot, (used / C::STAGES) & 1, kWaitLimit));
       ++used;
-      if (ok) {
-        const bool cut = tok0 + C::TILE - 1 > lim_all;
-        if (tok0 + C::TILE > cur.s.L) {   // scales behind the last token: 0, whatever the cache holds there
-          for (int i = lane; i < C::TILE; i += 32)
-            if (tok0 + i >= cur.s.L) {
-              uint8_t* u = st + (i / kUnit) * U::kBytes + (i % kUnit) * C::GR;
-              if constexpr (C::GR == 4) {
-                *reinterpret_cast<uint32_t*>(u + U::kKs) = 0;
-                *reinterpret_cast<uint32_t*>(u + U::kVs) = 0;
-              } else {
-                *reinterpret_cast<uint16_t*>(u + U::kKs) = 0;
-                *reinterpret_cast<uint16_t*>(u + U::kVs) = 0;
-              }
-            }
-          tc::fence_proxy_async_smem();   // before the ring's next copy into these bytes
-          __syncwarp();
-        }
-        bool special;
-        E = max(E, tile_scales<C>(st, &special));
-        if (cut || special) tile_step<C, true>(st, qr, qs, cf, lim, tok0, E, a);
-        else tile_step<C, false>(st, qr, qs, cf, lim, tok0, E, a);
+      if (ok && cur.s.L > 0) {
+        const int was = E;
+        const bool careful = load_scales<C>(st, tab, cur.s.L - tok0, E);
+        const float moved = E == was ? 1.f : __uint_as_float((uint32_t)max(127 + was - E, 0) << 23);
+        if (careful) tile_step<C, true, true>(st, tab, qr, qs, tok0, E, moved, a);
+        else if (tok0 + C::TILE - 1 > lim_all) tile_step<C, true, false>(st, tab, qr, qs, tok0, E, moved, a);
+        else tile_step<C, false, false>(st, tab, qr, qs, tok0, E, moved, a);
       }
       __syncwarp();
       if (ok) produce();
     }
+    // each column's sum, and both it and the reference on the scale of O: O / l is the output
+    float ref[C::NT][2];
+    const float to_o = __uint_as_float(E < 254 ? (uint32_t)(254 - E) << 23 : 0x00400000u);   // 2^(127 - E)
 #pragma unroll
     for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
@@ -604,14 +696,18 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
         l += __shfl_xor_sync(0xffffffffu, l, 4);
         l += __shfl_xor_sync(0xffffffffu, l, 8);
         l += __shfl_xor_sync(0xffffffffu, l, 16);
+        l *= to_o;
+        ref[nt][e] = (a.m[nt][e] == -INFINITY ? 0.f : a.m[nt][e]) + (float)(E - 142);
       }
 
     // ---- the piece's result
-    const bool starts = cur.tile == 0, whole = starts && cnt == cur.s.tiles;
+    const bool starts = first == 0, whole = starts && last == cur.s.tiles;
     const int64_t slot = 2 * me + (starts ? 1 : 0);
     if (starts && !whole) {   // this worker's last piece; who has the rest of the segment?
-      const int64_t y = x1 + (cur.s.tiles - cnt) - 1;
-      owner = make_int4(cur.n, h, rt, (int)(((y + 1) * workers - 1) / total - me));
+      const volatile int64_t* v = sums + C::W + 1;
+      const int64_t all = v[0], cut = v[1];
+      const int64_t y = (me + 1) * all / cut - cur.left - cur.pos + C::HEAD + cur.s.tiles - 1;   // its last tile on the line
+      owner = make_int4(cur.n, h, rt, (int)(((y + 1) * cut - 1) / all - me));
     }
     const int64_t row0 = (int64_t)cur.s.q0 * p.Hq;   // row r: token r / G, head h G + r % G
     if (!wide) {
@@ -623,8 +719,8 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
           if (c >= rows) continue;
           const int64_t row = row0 + (int64_t)(rr / G) * p.Hq + h * G + rr % G;
           if (g == 0) {
-            if (!whole) parts.ml[slot * C::R + c] = make_float2(a.ref[nt][e], a.l[nt][e]);
-            else if (p.lse) p.lse[row] = lse_of(a.ref[nt][e], a.l[nt][e]);
+            if (!whole) parts.ml[slot * C::R + c] = make_float2(ref[nt][e], a.l[nt][e]);
+            else if (p.lse) p.lse[row] = lse_of(ref[nt][e], a.l[nt][e]);
           }
 #pragma unroll
           for (int j = 0; j < C::GR; ++j) {
@@ -643,7 +739,7 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int c = nt * 8 + 2 * t + e;
-          if (g == 0) mml[c] = make_float2(a.ref[nt][e], a.l[nt][e]);
+          if (g == 0) mml[c] = make_float2(ref[nt][e], a.l[nt][e]);
 #pragma unroll
           for (int j = 0; j < C::GR; ++j)
             *reinterpret_cast<float4*>(mo + c * C::D + 32 * j + 4 * g) =
@@ -680,6 +776,7 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
       }
       tc::fence_proxy_async_smem();   // before the next piece's copies into the rings
       __syncthreads();
+      joined = true;
     }
   }
   if (lane == 0) *own_at = wide && warp != 0 ? make_int4(0, 0, 0, 0) : owner;
@@ -776,8 +873,15 @@ auto with_cfg(int32_t Hq, int32_t Hkv, int32_t D, int32_t max_q, kda_dtype dt, F
     return rows <= 8 ? f(Cfg<64, 1, 2>{}, float{}) : f(Cfg<64, 2, 2>{}, float{});
   }
   const __nv_bfloat16 z{};
-  if (D == 128) return rows <= 8 ? f(Cfg<128, 1, 1>{}, z) : rows <= 16 ? f(Cfg<128, 2, 1>{}, z) : f(Cfg<128, 4, 1>{}, z);
-  return rows <= 8 ? f(Cfg<64, 1, 1>{}, z) : rows <= 16 ? f(Cfg<64, 2, 1>{}, z) : f(Cfg<64, 4, 1>{}, z);
+  if (D == 128)
+    return rows <= 8    ? f(Cfg<128, 1, 1>{}, z)
+           : rows <= 16 ? f(Cfg<128, 2, 1>{}, z)
+           : rows <= 24 ? f(Cfg<128, 3, 1>{}, z)
+                        : f(Cfg<128, 4, 1>{}, z);
+  return rows <= 8    ? f(Cfg<64, 1, 1>{}, z)
+         : rows <= 16 ? f(Cfg<64, 2, 1>{}, z)
+         : rows <= 24 ? f(Cfg<64, 3, 1>{}, z)
+                      : f(Cfg<64, 4, 1>{}, z);
 }
 
 // Whether the tiled kernel takes the call: bf16, and a sequence's rows fill at least one of
