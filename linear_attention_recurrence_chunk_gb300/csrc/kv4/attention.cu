@@ -21,11 +21,12 @@
 // transposing move each (movmatrix), after a multiplication by the token's value
 // scale of the channel group.
 // Ranges.  A query row is scaled by a power of two to 2^14 <= max|q| < 2^15, which
-// is exact in fp16 but for channels 2^28 below the largest.  Weights are 2^15 at
-// most and multiplied, transposed, by the value scales relative to the largest one
-// seen, 2^(e - E), in fp16: exact where e - E >= -14 and a product is normal; a tile
-// with smaller ones multiplies in fp32 first.  So a weight loses bits only when
-// p 2^(e - E) is below 2^-29.  E below 2^-27 counts as that.  The output follows E.
+// is exact in fp16 but for channels 2^28 below the largest.  Weights are 2^14 at
+// most and multiplied, transposed, by the value scales relative to a reference,
+// 2^(e - E) <= 2, in fp16: exact where e - E >= -14 and a product is normal; a tile
+// with smaller ones multiplies in fp32 first.  E is the largest e seen, or one below
+// it, and at least 2^-27; the output follows it.  So a weight loses bits only when
+// p 2^(e - E) is below 2^-28.
 // fp32 inputs: q and the weights each as the sum of two fp16 numbers, two products
 // for one.
 //
@@ -164,14 +165,15 @@ struct Cursor {
 template <class C>
 struct Acc {
   float O[2 * C::GR][C::NT][4];
-  float m[C::NT][2], l[C::NT][2];   // running maximum (log2) and sum of 2^(s - m + 15) of each column
+  float m[C::NT][2], l[C::NT][2];   // running maximum (log2) and sum of 2^(s - m + 14) of each column
 };
 
-// A tile's scales into the warp's tables; E becomes the largest value scale so far.
-// Returns whether the tile needs the careful step: a group that is not finite, or a
-// value scale that is not a normal fp16 number relative to E.
+// A tile's scales into the warp's tables.  E, the reference of the value scales, is the
+// largest of a piece's first tile (fresh), raised when one is above 2^(E + 1) later.  Returns whether the tile
+// needs the careful step: a group that is not finite, or a value scale outside
+// 2^(E - 14) .. 2^(E + 1), whose fp16 relative to E is not a normal number.
 template <class C>
-__device__ __forceinline__ bool load_scales(const uint8_t* st, uint8_t* tab, int left, int& E) {
+__device__ __forceinline__ bool load_scales(const uint8_t* st, uint8_t* tab, int left, bool fresh, int& E) {
   using U = Unit<C::D>;
   const int lane = threadIdx.x & 31;
   constexpr uint32_t kOnes = C::GR == 4 ? 0x01010101u : 0x0101u;
@@ -187,44 +189,56 @@ __device__ __forceinline__ bool load_scales(const uint8_t* st, uint8_t* tab, int
       k[0] = a & 0xffffu; k[1] = a >> 16; v[0] = b & 0xffffu; v[1] = b >> 16;
     }
   }
-  if (left < C::TILE) {   // tokens behind the last: 0, whatever the cache holds there
+  const int have = min(left - 2 * lane, in ? 2 : 0);   // of the two tokens; the cache may hold anything behind the last
+  auto largest = [&]() -> int {                        // value scale but 255
+    uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (2 * lane + i >= left) k[i] = v[i] = 0;
+#pragma unroll
+      for (int j = 0; j < C::GR; ++j) m = max(m, i < have ? (v[i] >> (8 * j) & 0xffu) % 255u : 0u);
+    return (int)__reduce_max_sync(0xffffffffu, m);
+  };
+  if (fresh) E = max(100, largest());
+  if (have < 2) {   // tokens that are not there: nothing that a weight of 0 would not cancel
+    if (have < 1) k[0] = 0, v[0] = (uint32_t)E * kOnes;
+    k[1] = 0;
+    v[1] = (uint32_t)E * kOnes;
   }
-  const uint32_t kt = __vmaxu4(k[0], k[1]), vt = __vmaxu4(v[0], v[1]);
-  uint32_t vl = in ? __vminu4(v[0], v[1]) : 0xffffffffu;
-  if constexpr (C::GR == 2) vl |= 0xffff0000u;
-  auto top = [](uint32_t w) { return max(max(w & 0xffu, w >> 8 & 0xffu), max(w >> 16 & 0xffu, w >> 24)); };
-  auto low = [](uint32_t w) { return min(min(w & 0xffu, w >> 8 & 0xffu), min(w >> 16 & 0xffu, w >> 24)); };
-  uint32_t vm = __reduce_max_sync(0xffffffffu, top(vt));
-  const uint32_t lo = __reduce_min_sync(0xffffffffu, low(vl));
-  const bool nan = __any_sync(0xffffffffu, top(kt) == 255u) || vm == 255u;
-  if (nan) vm = __reduce_max_sync(0xffffffffu, max(top(v[0] & ~__vcmpeq4(v[0], ~0u)), top(v[1] & ~__vcmpeq4(v[1], ~0u))));
-  E = max(E, (int)vm);
-  const bool careful = nan || (int)lo < E - 14;
+  // exponent fields of the value scales less one: a byte outside 0 .. 15 (or a borrow, which leaves one) shows in
+  // the high nibbles, for E <= 239; a key byte of 255 by a carry
+  uint32_t d0 = v[0] - (uint32_t)(E - 14) * kOnes, d1 = v[1] - (uint32_t)(E - 14) * kOnes;
+  uint32_t odd = (d0 | d1) & (C::GR == 4 ? 0xf0f0f0f0u : 0xfffff0f0u);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) odd |= ((k[i] & 0x7f7f7f7fu) + 0x01010101u) & k[i] & 0x80808080u;
+  const bool careful = __any_sync(0xffffffffu, odd != 0) || E > 239;
+  if (careful) {
+    const int vm = largest();
+    if (vm > E + 1) E = vm;
+  }
   if (in) {
     float* kf = reinterpret_cast<float*>(tab) + 2 * lane * C::GR;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float f[C::GR];
 #pragma unroll
-      for (int j = 0; j < C::GR; ++j) {
-        f[j] = scale_f32(k[i] >> (8 * j) & 0xffu);
-        if (nan) f[j] = f[j] == INFINITY ? __uint_as_float(0x7fffffffu) : f[j];
+      for (int j = 0; j < C::GR; ++j) f[j] = scale_f32(k[i] >> (8 * j) & 0xffu);
+      if (careful) {
+#pragma unroll
+        for (int j = 0; j < C::GR; ++j) f[j] = f[j] == INFINITY ? __uint_as_float(0x7fffffffu) : f[j];
       }
       if constexpr (C::GR == 4) reinterpret_cast<float4*>(kf)[i] = make_float4(f[0], f[1], f[2], f[3]);
       else reinterpret_cast<float2*>(kf)[i] = make_float2(f[0], f[1]);
     }
-    if (!careful) {   // exponent fields between 1 and 15
-      const uint32_t base = (uint32_t)(E - 15) * kOnes, a = v[0] - base, b = v[1] - base;
+    if (!careful) {
+      d0 += kOnes;   // exponent fields 1 .. 16
+      d1 += kOnes;
       uint32_t h[C::GR];
 #pragma unroll
-      for (int j = 0; j < C::GR; ++j) h[j] = (__byte_perm(a, b, j | (4 + j) << 8) & 0x001f001fu) << 10;
+      for (int j = 0; j < C::GR; ++j) h[j] = (__byte_perm(d0, d1, j | (4 + j) << 8) & 0x001f001fu) << 10;
       uint8_t* vf = tab + C::tV + lane * C::GR * 4;
       if constexpr (C::GR == 4) *reinterpret_cast<uint4*>(vf) = make_uint4(h[0], h[1], h[2], h[3]);
       else *reinterpret_cast<uint2*>(vf) = make_uint2(h[0], h[1]);
-    } else {          // the careful step takes the bytes: of tokens that are there
+    } else {          // the careful step takes the bytes
       uint32_t* vw = reinterpret_cast<uint32_t*>(tab + C::tV) + 2 * lane;
       vw[0] = v[0];
       vw[1] = v[1];
@@ -332,7 +346,7 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint8_t* tab,
       f[nt][e] = a.m[nt][e] == -INFINITY ? 1.f : ex2(a.m[nt][e] - m);
       move |= f[nt][e] != 1.f;
       a.m[nt][e] = m;
-      ref[nt][e] = (m == -INFINITY ? 0.f : m) - 15.f;
+      ref[nt][e] = (m == -INFINITY ? 0.f : m) - 14.f;
     }
   if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -676,8 +690,9 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
       ++used;
       if (ok && cur.s.L > 0) {
         const int was = E;
-        const bool careful = load_scales<C>(st, tab, cur.s.L - tok0, E);
-        const float moved = E == was ? 1.f : __uint_as_float((uint32_t)max(127 + was - E, 0) << 23);
+        const bool fresh = tile == first + wi;
+        const bool careful = load_scales<C>(st, tab, cur.s.L - tok0, fresh, E);
+        const float moved = E == was || fresh ? 1.f : __uint_as_float((uint32_t)max(127 + was - E, 0) << 23);
         if (careful) tile_step<C, true, true>(st, tab, qr, qs, tok0, E, moved, a);
         else if (tok0 + C::TILE - 1 > lim_all) tile_step<C, true, false>(st, tab, qr, qs, tok0, E, moved, a);
         else tile_step<C, false, false>(st, tab, qr, qs, tok0, E, moved, a);
@@ -697,7 +712,7 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
         l += __shfl_xor_sync(0xffffffffu, l, 8);
         l += __shfl_xor_sync(0xffffffffu, l, 16);
         l *= to_o;
-        ref[nt][e] = (a.m[nt][e] == -INFINITY ? 0.f : a.m[nt][e]) + (float)(E - 142);
+        ref[nt][e] = (a.m[nt][e] == -INFINITY ? 0.f : a.m[nt][e]) + (float)(E - 141);
       }
 
     // ---- the piece's result
