@@ -120,7 +120,7 @@ struct Cfg {
 
 // Pieces in the workspace: slot 2 w is the first piece of worker w, 2 w + 1 its last.
 struct Parts {
-  int4* owner;   // [workers] (sequence, head, row block, pieces that follow in workers w + 1 ..); .w = 0: none
+  int4* owner;   // [workers] (first query token, head * 64 + rows, first row, pieces that follow in workers w + 1 ..); .w = 0: none
   float2* ml;    // [2 workers][R] reference exponent and sum
   float* o;      // [2 workers][R][D]
 };
@@ -722,7 +722,7 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
       const volatile int64_t* v = sums + C::W + 1;
       const int64_t all = v[0], cut = v[1];
       const int64_t y = (me + 1) * all / cut - cur.left - cur.pos + C::HEAD + cur.s.tiles - 1;   // its last tile on the line
-      owner = make_int4(cur.n, h, rt, (int)(((y + 1) * cut - 1) / all - me));
+      owner = make_int4(cur.s.q0, h * 64 + rows, rt * C::R, (int)(((y + 1) * cut - 1) / all - me));
     }
     const int64_t row0 = (int64_t)cur.s.q0 * p.Hq;   // row r: token r / G, head h G + r % G
     if (!wide) {
@@ -803,38 +803,51 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
 }
 
 // Joins the pieces of the segments that a worker boundary cuts: block w those of the
-// segment that begins in worker w and goes on in the next ones, a thread per row and
-// four channels, in the order of the pieces.
+// segment that begins in worker w and goes on in the next ones, a warp per row (half
+// a warp for D = 64), in the order of the pieces, eight of them on their way at once.
+constexpr int kJoinWarps = 8;
 template <class C, typename T>
-__global__ void __launch_bounds__(C::R * C::D / 4) kv4_join_kernel(const __grid_constant__ AttnProblem p, const Parts parts) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+__global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const __grid_constant__ AttnProblem p, const Parts parts) {
+  constexpr int kLanes = C::D / 4, kAtOnce = 8;   // lanes of a row; pieces
   const int64_t w = blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 own = parts.owner[w];
   if (own.w == 0) return;
-  const int c = threadIdx.x / (C::D / 4), ch = (threadIdx.x % (C::D / 4)) * 4;
-  const int G = p.Hq / p.Hkv, rr = own.z * C::R + c;
-  const int q0 = p.cu ? p.cu[own.x] : own.x, qn = p.cu ? p.cu[own.x + 1] - q0 : 1;
-  if (rr >= qn * G) return;
-  auto slot = [&](int i) { return i == 0 ? 2 * w + 1 : 2 * (w + i); };
-  float ref = -INFINITY;
-#pragma unroll 4
-  for (int i = 0; i <= own.w; ++i) {
-    const float2 x = parts.ml[slot(i) * C::R + c];
-    if (x.y != 0.f) ref = fmaxf(ref, x.x);
+  const int G = p.Hq / p.Hkv, h = own.y >> 6, rows = own.y & 63, ch = (threadIdx.x % kLanes) * 4;
+  for (int c = threadIdx.x / kLanes; c < rows; c += kJoinWarps * 32 / kLanes) {
+    float ref = -INFINITY, l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int i0 = 0; i0 <= own.w; i0 += kAtOnce) {
+      float2 y[kAtOnce];
+      float4 v[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int64_t slot = (i0 + i == 0 ? 2 * w + 1 : 2 * (w + i0 + i)) * C::R + c;
+        const bool in = i0 + i <= own.w;
+        y[i] = in ? __ldcg(parts.ml + slot) : make_float2(0.f, 0.f);
+        v[i] = in ? __ldcg(reinterpret_cast<const float4*>(parts.o + slot * C::D + ch)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float top = ref;
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        if (y[i].y != 0.f) top = fmaxf(top, y[i].x);
+      const float back = ref == -INFINITY ? 1.f : ex2(ref - top);   // nothing to bring along from before the first weight
+      ref = top;
+      l *= back;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] *= back;
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        if (y[i].y == 0.f) continue;   // (a NaN is not)
+        const float f = ex2(y[i].x - ref);
+        l = fmaf(y[i].y, f, l);
+        x[0] = fmaf(v[i].x, f, x[0]); x[1] = fmaf(v[i].y, f, x[1]); x[2] = fmaf(v[i].z, f, x[2]); x[3] = fmaf(v[i].w, f, x[3]);
+      }
+    }
+    const int rr = own.z + c;
+    const int64_t row = ((int64_t)own.x + rr / G) * p.Hq + h * G + rr % G;
+    if (ch == 0 && p.lse) p.lse[row] = lse_of(ref, l);
+    write_row4<C, T>(p, row, ch, l, x);
   }
-  float l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int i = 0; i <= own.w; ++i) {
-    const float2 y = parts.ml[slot(i) * C::R + c];
-    const float4 v = *reinterpret_cast<const float4*>(parts.o + (slot(i) * C::R + c) * C::D + ch);
-    const float f = y.y != 0.f ? ex2(y.x - ref) : 0.f;
-    if (f == 0.f) continue;
-    l = fmaf(y.y, f, l);
-    x[0] = fmaf(v.x, f, x[0]); x[1] = fmaf(v.y, f, x[1]); x[2] = fmaf(v.z, f, x[2]); x[3] = fmaf(v.w, f, x[3]);
-  }
-  const int64_t row = ((int64_t)q0 + rr / G) * p.Hq + own.y * G + rr % G;
-  if (ch == 0 && p.lse) p.lse[row] = lse_of(ref, l);
-  write_row4<C, T>(p, row, ch, l, x);
 }
 
 template <class C>
@@ -864,7 +877,7 @@ cudaError_t launch(const AttnProblem& p, void* workspace, cudaStream_t stream) {
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid * C::W, 1, 1);
-  cfg.blockDim = dim3(C::R * C::D / 4, 1, 1);
+  cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];   // its blocks may come up while the first kernel ends; they wait for its results
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
