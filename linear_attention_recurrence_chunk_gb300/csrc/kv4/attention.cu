@@ -248,11 +248,12 @@ __device__ __forceinline__ bool load_scales(const uint8_t* st, uint8_t* tab, int
   return careful;
 }
 
-// One tile.  kCut: rows see only a part of it.  kCareful: see load_scales.
-template <class C, bool kCut, bool kCareful>
+// One tile.  cut: rows see only a part of it (a flag and not another instance, which would
+// crowd the instruction cache).  kCareful: see load_scales.
+template <class C, bool kCareful>
 __device__ __forceinline__ void tile_step(const uint8_t* st, const uint8_t* tab,
                                           const uint32_t (&qr)[C::QREG ? C::NT : 1][C::QREG ? C::KS : 1][2],
-                                          const uint8_t* qs, int tok0, int E, float moved, Acc<C>& a) {
+                                          const uint8_t* qs, int tok0, bool cut, int E, float moved, Acc<C>& a) {
   using U = Unit<C::D>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const float2* cfs = reinterpret_cast<const float2*>(tab + C::tRow) + t;                 // of columns 2 t, 2 t + 1
@@ -311,7 +312,7 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint8_t* tab,
         s[3] = j ? fmaf(ks[1][j], c[3], s[3]) : ks[1][j] * c[3];
       }
     }
-    if constexpr (kCut) {
+    if (cut) {
 #pragma unroll
       for (int nt = 0; nt < C::NT; ++nt) {
         const int2 lim = lims[4 * nt];
@@ -693,9 +694,9 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
         const bool fresh = tile == first + wi;
         const bool careful = load_scales<C>(st, tab, cur.s.L - tok0, fresh, E);
         const float moved = E == was || fresh ? 1.f : __uint_as_float((uint32_t)max(127 + was - E, 0) << 23);
-        if (careful) tile_step<C, true, true>(st, tab, qr, qs, tok0, E, moved, a);
-        else if (tok0 + C::TILE - 1 > lim_all) tile_step<C, true, false>(st, tab, qr, qs, tok0, E, moved, a);
-        else tile_step<C, false, false>(st, tab, qr, qs, tok0, E, moved, a);
+        const bool cut = tok0 + C::TILE - 1 > lim_all;
+        if (careful) tile_step<C, true>(st, tab, qr, qs, tok0, cut, E, moved, a);
+        else tile_step<C, false>(st, tab, qr, qs, tok0, cut, E, moved, a);
       }
       __syncwarp();
       if (ok) produce();
