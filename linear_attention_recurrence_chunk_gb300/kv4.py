@@ -149,11 +149,14 @@ def kda_page_map(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table:
     room = num_tokens + pad
 
     def call(st):
-        buf = torch.empty(2 * room + 2 * N + 2, dtype=torch.int32, device=cached_lens.device)
+        buf = cached_lens.new_empty(2 * room + 2 * N + 2)
         p = buf.data_ptr()
         _check(lib.kda_page_map(*args, p + 8 * room, p + 4 * (2 * room + N + 1), p, p + 4 * room,
                                 p + 4 * (2 * room + 2 * N + 1), st), "kda_page_map")
-        slots, _, pos, _, cu, lens, nxt = buf.split_with_sizes((num_tokens, pad, num_tokens, pad, N + 1, N, 1))
+        if pad:
+            slots, _, pos, _, cu, lens, nxt = buf.split_with_sizes((num_tokens, pad, num_tokens, pad, N + 1, N, 1))
+        else:
+            slots, pos, cu, lens, nxt = buf.split_with_sizes((num_tokens, num_tokens, N + 1, N, 1))
         return cu, lens, slots, pos, nxt
 
     return _run(dev, stream, call)
@@ -197,7 +200,7 @@ def kda_kv4_gather(cache: torch.Tensor, slot_map: torch.Tensor, dtype: torch.dty
     dt, sl, T = _dtype(dtype), _i32("slot_map", slot_map, dev), slot_map.numel()
 
     def call(st):
-        k, v = torch.empty((2, T, H, D), dtype=dtype, device=cache.device).unbind(0)
+        k, v = cache.new_empty((2, T, H, D), dtype=dtype).unbind(0)
         _check(lib.kda_kv4_gather(cache.data_ptr(), pages, ps, sl, T, H, D, dt, k.data_ptr(), v.data_ptr(), st),
                "kda_kv4_gather")
         return k, v
@@ -245,11 +248,11 @@ def kda_kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.T
     scale = D ** -0.5 if sm_scale is None else sm_scale
 
     def call(st):
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device) if o is None else o
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if return_lse else None
+        out = q.new_empty((T, Hq, D)) if o is None else o
+        lse = q.new_empty((T, Hq), dtype=torch.float32) if return_lse else None
         if workspace is None:
             n = lib.kda_kv4_attention_workspace_size(T, N, Hq, H, D, max_q_len, dt)
-            ws = torch.empty(256 if n == (1 << 64) - 1 else n, dtype=torch.uint8, device=q.device)
+            ws = cache.new_empty(256 if n == (1 << 64) - 1 else n)
         else:
             ws, n = workspace, workspace.numel() * workspace.element_size()
         _check(lib.kda_kv4_attention(q.data_ptr(), qt, qh, cache.data_ptr(), pages, ps, bt, max_pages, ln, cu, T, N, Hq, H,
