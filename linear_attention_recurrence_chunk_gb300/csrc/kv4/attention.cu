@@ -98,18 +98,18 @@ template <int D_, int NT_, int PARTS_>
 struct Cfg {
   static constexpr int D = D_, NT = NT_, PARTS = PARTS_;
   static constexpr int R = 8 * NT;                  // query rows of a segment
-  static constexpr int MT = NT == 1 ? 4 : 2;        // units of a tile
-  static constexpr int TILE = kUnit * MT;
-  static constexpr int STAGES = NT == 1 ? 2 : NT == 2 && PARTS == 1 ? 3 : 4;
-  static constexpr bool QREG = NT == 1 && PARTS == 1;   // q operands in registers
-  static constexpr int W = NT <= 2 && PARTS == 1 ? 12 : 8;   // warps of a CTA
-  static constexpr int HEAD = NT == 1 ? 1 : 2;      // room of a segment's beginning and end on the line, in tiles
+  static constexpr int MT = 4, TILE = kUnit * MT;   // units and tokens of a tile
+  static constexpr int MH = NT == 1 ? 4 : 2;        // units of a softmax step: as many as the registers hold scores of
+  static constexpr int STAGES = 2;
+  static constexpr bool QREG = NT <= 2 && PARTS == 1;   // q operands in registers
+  static constexpr int W = NT == 1 && PARTS == 1 ? 12 : 8;   // warps of a CTA
+  static constexpr int HEAD = 1;                    // room of a segment's beginning and end on the line, in tiles
   static constexpr int GR = D / 32, KS = D / 16;
   static constexpr int kStage = MT * Unit<D>::kBytes, kRing = STAGES * kStage;
   static constexpr int kQ = QREG ? 0 : KS * NT * PARTS * 256;
   // a warp's tables: a tile's scales, of keys as fp32 [token][group], of values as fp16
   // [token pair][group][2]; the rows' score factors and last tokens
-  static constexpr int tV = TILE * GR * 4, tRow = tV + TILE * GR * 2, kTab = tRow + R * 8;
+  static constexpr int tV = TILE * GR * 4, tRow = tV + TILE * 8, kTab = tRow + R * 8;
   static constexpr int kPart = R * (D + 2) * 4;     // a warp's result in shared memory: O, then (m, l)
   static constexpr int oQ = W * kRing, oTab = oQ + W * kQ, oBar = oTab + W * kTab, oSum = oBar + W * STAGES * 8,
                        kSmem = oSum + (W + 3) * 8;
@@ -248,26 +248,26 @@ __device__ __forceinline__ bool load_scales(const uint8_t* st, uint8_t* tab, int
   return careful;
 }
 
-// One tile.  cut: rows see only a part of it (a flag and not another instance, which would
+// One step of MH units.  cut: rows see only a part of it (a flag and not another instance, which would
 // crowd the instruction cache).  kCareful: see load_scales.
 template <class C, bool kCareful>
-__device__ __forceinline__ void tile_step(const uint8_t* st, const uint8_t* tab,
+__device__ __forceinline__ void tile_step(const uint8_t* st, const float* ktab, const uint8_t* vtab, const uint8_t* rowtab,
                                           const uint32_t (&qr)[C::QREG ? C::NT : 1][C::QREG ? C::KS : 1][2],
                                           const uint8_t* qs, int tok0, bool cut, int E, float moved, Acc<C>& a) {
   using U = Unit<C::D>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const float2* cfs = reinterpret_cast<const float2*>(tab + C::tRow) + t;                 // of columns 2 t, 2 t + 1
-  const int2* lims = reinterpret_cast<const int2*>(tab + C::tRow + C::R * 4) + t;
-  float S[C::MT][C::NT][4];
+  const float2* cfs = reinterpret_cast<const float2*>(rowtab) + t;                 // of columns 2 t, 2 t + 1
+  const int2* lims = reinterpret_cast<const int2*>(rowtab + C::R * 4) + t;
+  float S[C::MH][C::NT][4];
 #pragma unroll
-  for (int mt = 0; mt < C::MT; ++mt) {
+  for (int mt = 0; mt < C::MH; ++mt) {
     const uint8_t* u = st + mt * U::kBytes;
     uint32_t kw[2][C::GR];
     float ks[2][C::GR];
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       const uint8_t* row = u + U::key_word(g + 8 * hf, 0, t);
-      const float* sc = reinterpret_cast<const float*>(tab) + (mt * kUnit + g + 8 * hf) * C::GR;
+      const float* sc = ktab + (mt * kUnit + g + 8 * hf) * C::GR;
       if constexpr (C::GR == 4) {
         const uint4 x = *reinterpret_cast<const uint4*>(row);
         kw[hf][0] = x.x; kw[hf][1] = x.y; kw[hf][2] = x.z; kw[hf][3] = x.w;
@@ -338,7 +338,7 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint8_t* tab,
     for (int e = 0; e < 2; ++e) {
       float x = fmaxf(S[0][nt][e], S[0][nt][e + 2]);
 #pragma unroll
-      for (int mt = 1; mt < C::MT; ++mt) x = fmaxf(x, fmaxf(S[mt][nt][e], S[mt][nt][e + 2]));
+      for (int mt = 1; mt < C::MH; ++mt) x = fmaxf(x, fmaxf(S[mt][nt][e], S[mt][nt][e + 2]));
       x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
       x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
       x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
@@ -362,7 +362,7 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint8_t* tab,
     }
   }
 #pragma unroll
-  for (int mt = 0; mt < C::MT; ++mt)
+  for (int mt = 0; mt < C::MH; ++mt)
 #pragma unroll
     for (int nt = 0; nt < C::NT; ++nt) {
 #pragma unroll
@@ -373,7 +373,7 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint8_t* tab,
 
   const float to_e = kCareful ? __uint_as_float(E < 254 ? (uint32_t)(254 - E) << 23 : 0x00400000u) : 1.f;   // 2^(127 - E)
 #pragma unroll
-  for (int mt = 0; mt < C::MT; ++mt) {
+  for (int mt = 0; mt < C::MH; ++mt) {
     const uint8_t* u = st + mt * U::kBytes;
     uint32_t xy[2][2][C::GR / 2];   // [8-token block][even or odd channel]: bytes of token pairs
     uint32_t vs[2][C::GR];          // [8-token block]: scales of the tokens 2 t, 2 t + 1
@@ -382,7 +382,7 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint8_t* tab,
     for (int b = 0; b < 2; ++b) {
       const uint8_t* at = u + U::val_half(8 * b + 2 * t, 0, g);
       uint32_t w[C::GR];
-      const uint8_t* sc = tab + C::tV + (mt * 8 + 4 * b + t) * C::GR * 4;
+      const uint8_t* sc = vtab + (mt * 8 + 4 * b + t) * C::GR * 4;
       if constexpr (C::GR == 4) {
         const uint4 x = *reinterpret_cast<const uint4*>(at);
         w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
@@ -433,7 +433,7 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint8_t* tab,
 #pragma unroll
               for (int part = 0; part < C::PARTS; ++part) b[hf][part] = mul2(pk[hf][nt][part], vs[hf][j]);
           } else {
-            const uint32_t* vw = reinterpret_cast<const uint32_t*>(tab + C::tV) + mt * kUnit;
+            const uint32_t* vw = reinterpret_cast<const uint32_t*>(vtab) + mt * kUnit;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {   // the token of this lane's two weights
               const float sc = scale_at<true>(vw[g + 8 * hf], j) * to_e;
@@ -694,9 +694,18 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
         const bool fresh = tile == first + wi;
         const bool careful = load_scales<C>(st, tab, cur.s.L - tok0, fresh, E);
         const float moved = E == was || fresh ? 1.f : __uint_as_float((uint32_t)max(127 + was - E, 0) << 23);
-        const bool cut = tok0 + C::TILE - 1 > lim_all;
-        if (careful) tile_step<C, true>(st, tab, qr, qs, tok0, cut, E, moved, a);
-        else tile_step<C, false>(st, tab, qr, qs, tok0, cut, E, moved, a);
+#pragma unroll 1
+        for (int u = 0; u < C::MT && tok0 + u * kUnit < cur.s.L; u += C::MH) {
+          const uint8_t* su = st + u * U::kBytes;
+          const float* ktab = reinterpret_cast<const float*>(tab) + u * kUnit * C::GR;
+          // (bytes of two tokens as one word each in the careful step, a pair of fp16 per group else)
+          const uint8_t* vtab = tab + C::tV + u * (careful ? kUnit * 4 : 8 * C::GR * 4);
+          const int tok = tok0 + u * kUnit;
+          const bool cut = tok + C::MH * kUnit - 1 > lim_all;
+          const float follow = u == 0 ? moved : 1.f;
+          if (careful) tile_step<C, true>(su, ktab, vtab, tab + C::tRow, qr, qs, tok, cut, E, follow, a);
+          else tile_step<C, false>(su, ktab, vtab, tab + C::tRow, qr, qs, tok, cut, E, follow, a);
+        }
       }
       __syncwarp();
       if (ok) produce();
