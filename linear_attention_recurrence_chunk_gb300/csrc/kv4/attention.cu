@@ -39,6 +39,9 @@
 // segment in their order.  Lengths are read on the device; the cut needs one sum over
 // the sequences, which every CTA takes itself.  Each warp feeds itself through a ring
 // of tiles filled by bulk copies.
+#include <algorithm>
+#include <cstdlib>
+
 #include "attn_common.cuh"
 
 namespace kda {
@@ -922,12 +925,24 @@ auto with_cfg(int32_t Hq, int32_t Hkv, int32_t D, int32_t max_q, kda_dtype dt, F
                       : f(Cfg<64, 4, 1>{}, z);
 }
 
-// Whether the tiled kernel takes the call: bf16, and a sequence's rows fill at least one of
-// its blocks of 128 rows.
+// Whether the tiled kernel takes the call (bf16).  Both kernels' times grow with the cached
+// tokens, so the rule needs no lengths.  Per 1,024 cached tokens the cut line takes about
+// 0.098 us for each 32 rows of a key/value head, on the whole GPU; the tiled kernel 18 us
+// a wave of 152 CTAs of up to 128 rows, 22 us of up to 256.  Measured over 16,384 cached tokens
+// (line / tiled, us): 8 sequences of 8 heads with 64 rows 243 / 285, 128 rows 416 / 289,
+// 512 rows 1,457 / 361; one sequence of 8 heads with 256 rows 125 / 349; 8 of 2 heads with
+// 256 rows 212 / 348, 512 rows 374 / 355.  Up to 24 rows the line's cost per row is that of
+// smaller instances (16 rows: 66 / 280).  KDA_KV4_TILED=0 or =1 forces a kernel for bf16 calls.
 bool extend_rows(const AttnProblem& p) {
-  const int64_t rows = (int64_t)p.max_q * (p.Hq / p.Hkv);
-  return p.dt == KDA_BF16 && rows >= 128 && (rows + 255) / 256 * p.N * p.Hkv <= INT32_MAX;
+  const int64_t G = p.Hq / p.Hkv, rows = (int64_t)p.max_q * G;
+  if (p.dt != KDA_BF16 || (rows + 255) / 256 * p.N * p.Hkv > INT32_MAX) return false;
+  const int64_t work = p.Hkv * std::max<int64_t>(p.N, (p.T * G + 31) / 32);
+  const int64_t waves = (p.Hkv * std::max<int64_t>(p.N, (p.T * G + 255) / 256) + kCtas - 1) / kCtas;
+  bool tiled = rows > 24 && work > (rows > 128 ? 220 : 183) * waves;
+  if (const char* env = std::getenv("KDA_KV4_TILED")) tiled = std::atoi(env) != 0;
+  return tiled;
 }
+
 }  // namespace
 
 size_t attention_workspace(int32_t Hq, int32_t Hkv, int32_t D, int32_t max_q, kda_dtype dt) {

@@ -100,7 +100,7 @@ def test_decode(D, dt, Hq, Hkv):
 
 
 @pytest.mark.parametrize("ps", [16, 32, 48, 64, 80, 128, 4096])
-def test_page_sizes(ps):
+def test_page_sizes(ps, kernel):
     """Pages that end inside a tile, and tiles inside a page."""
     run_check(BF, 128, 8, 2, ps, [1, 47, 333, 100], [1] * 4)
     run_check(F32, 64, 4, 2, ps, [5, 161], [1] * 2)
@@ -109,10 +109,17 @@ def test_page_sizes(ps):
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("D,Hq,Hkv,qn", [(128, 8, 8, [1, 2, 3]), (128, 8, 2, [5, 1, 4]), (64, 12, 2, [3, 3, 8]),
                                          (128, 32, 8, [9, 2, 33]), (64, 5, 1, [70, 1, 17])])
-def test_several_query_tokens(dt, D, Hq, Hkv, qn):
+def test_several_query_tokens(dt, D, Hq, Hkv, qn, kernel):
     """The causal edge inside a tile and over tiles; more tokens than are cached leave rows empty."""
     run_check(dt, D, Hq, Hkv, 32, [70, 2, 150], qn)
     run_check(dt, D, Hq, Hkv, 32, qn, qn)          # a prompt from its beginning
+
+
+@pytest.fixture(params=["0", "1"], ids=["line", "tiled"])
+def kernel(request, monkeypatch):
+    """Both kernels of bf16 calls, whichever the sizes would choose."""
+    monkeypatch.setenv("KDA_KV4_TILED", request.param)
+    return request.param
 
 
 @pytest.mark.parametrize("D", [64, 128])
@@ -122,13 +129,13 @@ def test_several_query_tokens(dt, D, Hq, Hkv, qn):
     (3, 1, 48, [500, 90, 0, 7], [100, 86, 3, 20]),  # uneven row blocks, more query tokens than cached ones
     (32, 2, 32, [201], [64]),                       # a token's heads fill a fraction of a block
     (6, 6, 128, [260, 1000], [259, 1])])
-def test_query_chunks(D, Hq, Hkv, ps, lens, qn):
+def test_query_chunks(D, Hq, Hkv, ps, lens, qn, kernel):
     s = run_check(BF, D, Hq, Hkv, ps, lens, qn, spread=2.0)
     a, b = s.run(), s.run()
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
-def test_query_chunk_with_scales_that_grow_and_not_finite_tokens():
+def test_query_chunk_with_scales_that_grow_and_not_finite_tokens(kernel):
     def grow(k, v, rng):
         v *= np.ldexp(1.0, (np.arange(v.shape[0]) // 60))[:, None, None]
         k *= np.ldexp(1.0, rng.integers(-3, 4, (k.shape[0], k.shape[1], 4)).repeat(32, -1))
@@ -143,7 +150,13 @@ def test_query_chunk_with_scales_that_grow_and_not_finite_tokens():
     assert torch.isnan(s.run()[0]).any() and not torch.isnan(s.run()[0]).all()
 
 
-def test_sequences_without_query_tokens():
+def test_chunks_that_choose_the_tiled_kernel():
+    """Sizes on both sides of the rule, without a forced kernel, agree with the reference."""
+    run_check(BF, 64, 32, 8, 32, [300] * 4, [80] * 4)       # 8 heads x 4 sequences x 10 blocks of 32 rows: 320
+    run_check(BF, 64, 32, 8, 32, [300] * 4, [40] * 4)       # 160
+
+
+def test_sequences_without_query_tokens(kernel):
     run_check(BF, 128, 8, 2, 16, [100, 50, 0, 20, 300], [1, 0, 0, 2, 0])
     run_check(BF, 128, 8, 2, 16, [100, 50, 0, 20, 300], [0, 0, 0, 0, 1])
 
@@ -179,12 +192,12 @@ def test_scale_arguments():
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("spread,kscale,vscale", [(1.0, 2.0 ** 20, 2.0 ** -60), (2.0 ** -20, 2.0 ** 20, 2.0 ** 40),
                                                   (2.0 ** 60, 2.0 ** -60, 1.0), (0.0, 1.0, 2.0 ** -20)])
-def test_magnitudes(dt, spread, kscale, vscale):
+def test_magnitudes(dt, spread, kscale, vscale, kernel):
     """Keys, values and queries far from 1, up to scores that pick one token."""
     run_check(dt, 128, 8, 1, 16, [300, 40], [1, 2], spread=spread, kscale=kscale, vscale=vscale)
 
 
-def test_value_scales_that_grow_and_differ():
+def test_value_scales_that_grow_and_differ(kernel):
     """The weights' reference follows the largest value scale; small ones keep their precision."""
     def edit(k, v, rng):
         v *= np.ldexp(1.0, rng.integers(-9, 10, (v.shape[0], v.shape[1], 4)).repeat(32, -1))
@@ -194,7 +207,7 @@ def test_value_scales_that_grow_and_differ():
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
-def test_not_finite_tokens_reach_only_the_rows_that_see_them(dt):
+def test_not_finite_tokens_reach_only_the_rows_that_see_them(dt, kernel):
     def edit(k, v, rng):
         k[60, 0, 3] = np.inf       # seen by the last two query tokens only
         v[59, 1, 100] = np.nan     # its group of channels, for the last three
@@ -206,7 +219,7 @@ def test_not_finite_tokens_reach_only_the_rows_that_see_them(dt):
     assert nan[3:, 4:, 96:].all() and not nan[:, 4:, :96].any() and not nan[:4, :4].any() and nan[4:, :4].all()
 
 
-def test_not_finite_queries():
+def test_not_finite_queries(kernel):
     s = Setup(BF, 128, 8, 2, 16, [62, 9], [1, 1])
     want = s.run()[0]
     q = s.q.clone()
@@ -219,7 +232,7 @@ def test_not_finite_queries():
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
-def test_strided_queries(dt):
+def test_strided_queries(dt, kernel):
     s = Setup(dt, 64, 6, 2, 16, [40, 99], [2, 3])
     want = s.run()
     wide = torch.zeros((5, 3, 6, 64), dtype=dt, device=DEV)
@@ -297,7 +310,7 @@ def test_captured_into_a_graph():
     no_error()
 
 
-def test_far_pages():
+def test_far_pages(kernel):
     """A sequence whose pages lie beyond 2^32 bytes."""
     D, Hq, Hkv, ps = 128, 8, 8, 64
     pages = 1 << 16                                  # 4.6 GB
@@ -316,7 +329,7 @@ def test_far_pages():
 
 
 @pytest.mark.parametrize("what", ["page", "page_high", "len", "len_negative", "cu_start", "cu_down", "cu_beyond", "many"])
-def test_bad_device_arguments_are_reported(what):
+def test_bad_device_arguments_are_reported(what, kernel):
     """The other sequences' results are those of a good call."""
     s = Setup(BF, 128, 8, 2, 16, [50, 70, 33], [1, 2, 1])
     want = s.run()[0].clone()
