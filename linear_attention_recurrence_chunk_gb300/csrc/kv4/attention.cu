@@ -106,13 +106,15 @@ struct Cfg {
   static constexpr int STAGES = 2;
   static constexpr bool QREG = NT <= 2 && PARTS == 1;   // q operands in registers
   static constexpr int W = NT == 1 && PARTS == 1 ? 12 : 8;   // warps of a CTA
-  static constexpr int HEAD = 1;                    // room of a segment's beginning and end on the line, in tiles
+  // room of a segment's beginning and end on the line, in tiles (256 sequences up to 2,048 tokens, 96 query on
+  // 8 key heads: 107 us with 1, 98 with 2, 94 with 3, 98 with 4)
+  static constexpr int HEAD = 3;
   static constexpr int GR = D / 32, KS = D / 16;
   static constexpr int kStage = MT * Unit<D>::kBytes, kRing = STAGES * kStage;
   static constexpr int kQ = QREG ? 0 : KS * NT * PARTS * 256;
   // a warp's tables: a tile's scales, of keys as fp32 [token][group], of values as fp16
-  // [token pair][group][2]; the rows' score factors and last tokens
-  static constexpr int tV = TILE * GR * 4, tRow = tV + TILE * 8, kTab = tRow + R * 8;
+  // [token pair][group][2]; the rows' score factors, last tokens and places in the output
+  static constexpr int tV = TILE * GR * 4, tRow = tV + TILE * 8, kTab = tRow + R * 16;
   static constexpr int kPart = R * (D + 2) * 4;     // a warp's result in shared memory: O, then (m, l)
   static constexpr int oQ = W * kRing, oTab = oQ + W * kQ, oBar = oTab + W * kTab, oSum = oBar + W * STAGES * 8,
                        kSmem = oSum + (W + 3) * 8;
@@ -655,7 +657,9 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
       const float down = fmaxf(__uint_as_float((ex - 14u) << 23) * fabsf(p.sm_scale) * kLog2e, 1.17549435e-38f);
       if (t == 0) {
         reinterpret_cast<float*>(tab + C::tRow)[r] = down;
-        reinterpret_cast<int*>(tab + C::tRow + C::R * 4)[r] = r < rows ? cur.s.L - cur.s.qn + (rt * C::R + r) / G : -1;
+        const int rr = rt * C::R + r, tok = rr / G;
+        reinterpret_cast<int*>(tab + C::tRow + C::R * 4)[r] = r < rows ? cur.s.L - cur.s.qn + tok : -1;
+        reinterpret_cast<int*>(tab + C::tRow + C::R * 8)[r] = (cur.s.q0 + tok) * p.Hq + h * G + (rr - tok * G);   // below T Hq
       }
 #pragma unroll
       for (int ks = 0; ks < C::KS; ++ks) {
@@ -737,15 +741,14 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
       const int64_t y = (me + 1) * all / cut - cur.left - cur.pos + C::HEAD + cur.s.tiles - 1;   // its last tile on the line
       owner = make_int4(cur.s.q0, h * 64 + rows, rt * C::R, (int)(((y + 1) * cut - 1) / all - me));
     }
-    const int64_t row0 = (int64_t)cur.s.q0 * p.Hq;   // row r: token r / G, head h G + r % G
     if (!wide) {
 #pragma unroll
       for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int c = nt * 8 + 2 * t + e, rr = rt * C::R + c;
+          const int c = nt * 8 + 2 * t + e;
           if (c >= rows) continue;
-          const int64_t row = row0 + (int64_t)(rr / G) * p.Hq + h * G + rr % G;
+          const int64_t row = reinterpret_cast<const int*>(tab + C::tRow + C::R * 8)[c];
           if (g == 0) {
             if (!whole) parts.ml[slot * C::R + c] = make_float2(ref[nt][e], a.l[nt][e]);
             else if (p.lse) p.lse[row] = lse_of(ref[nt][e], a.l[nt][e]);
@@ -775,7 +778,7 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
         }
       __syncthreads();
       for (int i = threadIdx.x; i < rows * (C::D / 4); i += C::W * 32) {
-        const int c = i / (C::D / 4), ch = (i % (C::D / 4)) * 4, rr = rt * C::R + c;
+        const int c = i / (C::D / 4), ch = (i % (C::D / 4)) * 4;
         auto ml_of = [&](int w) {
           return reinterpret_cast<const float2*>(sm + w * C::kRing + C::R * C::D * 4)[c];
         };
@@ -794,7 +797,7 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
           x[0] = fmaf(v.x, f, x[0]); x[1] = fmaf(v.y, f, x[1]); x[2] = fmaf(v.z, f, x[2]); x[3] = fmaf(v.w, f, x[3]);
         }
         if (l == 0.f) ref = 0.f;
-        const int64_t row = row0 + (int64_t)(rr / G) * p.Hq + h * G + rr % G;
+        const int64_t row = reinterpret_cast<const int*>(tab + C::tRow + C::R * 8)[c];   // (every warp's table has them)
         if (ch == 0) {
           if (!whole) parts.ml[slot * C::R + c] = make_float2(ref, l);
           else if (p.lse) p.lse[row] = lse_of(ref, l);
@@ -904,41 +907,35 @@ cudaError_t launch(const AttnProblem& p, void* workspace, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// Calls f with the instance for these sizes: as many blocks of eight rows as a
-// sequence's rows fill, up to four (two for fp32).
+// Calls f with the instance for these sizes: one block of eight rows, or two, of which a
+// segment with more rows takes several.  (Three and four blocks at once were built: their
+// accumulators leave too few registers, 20 rows over 8,191 tokens 66 us against 50.)
 template <typename F>
 auto with_cfg(int32_t Hq, int32_t Hkv, int32_t D, int32_t max_q, kda_dtype dt, F f) {
-  const int64_t rows = (int64_t)max_q * (Hq / Hkv);
+  const bool one = (int64_t)max_q * (Hq / Hkv) <= 8;
   if (dt == KDA_F32) {
-    if (D == 128) return rows <= 8 ? f(Cfg<128, 1, 2>{}, float{}) : f(Cfg<128, 2, 2>{}, float{});
-    return rows <= 8 ? f(Cfg<64, 1, 2>{}, float{}) : f(Cfg<64, 2, 2>{}, float{});
+    if (D == 128) return one ? f(Cfg<128, 1, 2>{}, float{}) : f(Cfg<128, 2, 2>{}, float{});
+    return one ? f(Cfg<64, 1, 2>{}, float{}) : f(Cfg<64, 2, 2>{}, float{});
   }
   const __nv_bfloat16 z{};
-  if (D == 128)
-    return rows <= 8    ? f(Cfg<128, 1, 1>{}, z)
-           : rows <= 16 ? f(Cfg<128, 2, 1>{}, z)
-           : rows <= 24 ? f(Cfg<128, 3, 1>{}, z)
-                        : f(Cfg<128, 4, 1>{}, z);
-  return rows <= 8    ? f(Cfg<64, 1, 1>{}, z)
-         : rows <= 16 ? f(Cfg<64, 2, 1>{}, z)
-         : rows <= 24 ? f(Cfg<64, 3, 1>{}, z)
-                      : f(Cfg<64, 4, 1>{}, z);
+  if (D == 128) return one ? f(Cfg<128, 1, 1>{}, z) : f(Cfg<128, 2, 1>{}, z);
+  return one ? f(Cfg<64, 1, 1>{}, z) : f(Cfg<64, 2, 1>{}, z);
 }
 
 // Whether the tiled kernel takes the call (bf16).  Both kernels' times grow with the cached
 // tokens, so the rule needs no lengths.  Per 1,024 cached tokens the cut line takes about
-// 0.098 us for each 32 rows of a key/value head, on the whole GPU; the tiled kernel 18 us
+// 0.074 us for each 32 rows of a key/value head, on the whole GPU; the tiled kernel 18 us
 // a wave of 152 CTAs of up to 128 rows, 22 us of up to 256.  Measured over 16,384 cached tokens
-// (line / tiled, us): 8 sequences of 8 heads with 64 rows 243 / 285, 128 rows 416 / 289,
-// 512 rows 1,457 / 361; one sequence of 8 heads with 256 rows 125 / 349; 8 of 2 heads with
-// 256 rows 212 / 348, 512 rows 374 / 355.  Up to 24 rows the line's cost per row is that of
-// smaller instances (16 rows: 66 / 280).  KDA_KV4_TILED=0 or =1 forces a kernel for bf16 calls.
+// (line / tiled, us): 8 sequences of 8 heads with 64 rows 171 / 285, 128 rows 319 / 288,
+// 512 rows 1,216 / 360; one sequence of 8 heads with 256 rows 99 / 346; 8 of 2 heads with
+// 512 rows 316 / 353, 1,024 rows 616 / 354.  Up to 24 rows the line is far ahead (16 rows:
+// 66 / 279).  KDA_KV4_TILED=0 or =1 forces a kernel for bf16 calls.
 bool extend_rows(const AttnProblem& p) {
   const int64_t G = p.Hq / p.Hkv, rows = (int64_t)p.max_q * G;
   if (p.dt != KDA_BF16 || (rows + 255) / 256 * p.N * p.Hkv > INT32_MAX) return false;
   const int64_t work = p.Hkv * std::max<int64_t>(p.N, (p.T * G + 31) / 32);
   const int64_t waves = (p.Hkv * std::max<int64_t>(p.N, (p.T * G + 255) / 256) + kCtas - 1) / kCtas;
-  bool tiled = rows > 24 && work > (rows > 128 ? 220 : 183) * waves;
+  bool tiled = rows > 24 && work > (rows > 128 ? 297 : 243) * waves;
   if (const char* env = std::getenv("KDA_KV4_TILED")) tiled = std::atoi(env) != 0;
   return tiled;
 }
