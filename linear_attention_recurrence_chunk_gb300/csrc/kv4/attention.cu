@@ -451,9 +451,18 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const float* ktab, 
             }
           }
 #pragma unroll
-          for (int part = 0; part < C::PARTS; ++part) {
-            mma16816(a.O[2 * j][nt], x0[2 * k], y0[2 * k], x1[2 * k], y1[2 * k], b[0][part], b[1][part]);
-            mma16816(a.O[2 * j + 1][nt], x0[2 * k + 1], y0[2 * k + 1], x1[2 * k + 1], y1[2 * k + 1], b[0][part], b[1][part]);
+          for (int d = 0; d < 2; ++d) {
+            const uint32_t a0 = x0[2 * k + d], a1 = y0[2 * k + d], a2 = x1[2 * k + d], a3 = y1[2 * k + d];
+            float(&o)[4] = a.O[2 * j + d][nt];
+            if constexpr (C::PARTS == 1) {
+              mma16816(o, a0, a1, a2, a3, b[0][0], b[1][0]);
+            } else {   // the instruction's sum cuts off: over thousands of units that would show in fp32
+              float c[4];
+              mma16816_first(c, a0, a1, a2, a3, b[0][C::PARTS - 1], b[1][C::PARTS - 1]);
+              mma16816(c, a0, a1, a2, a3, b[0][0], b[1][0]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[e] += c[e];
+            }
           }
         }
       }
