@@ -39,6 +39,11 @@
 // segment in their order.  Lengths are read on the device; the cut needs one sum over
 // the sequences, which every CTA takes itself.  Each warp feeds itself through a ring
 // of tiles filled by bulk copies.
+//
+// Measured: one token of 48 sequences up to 32,000, 64 query on 8 key heads of 128: 111 us
+// with the join, 563 MB at 5.1 TB/s.  Counters: issue 56 % and ALU pipe 55 % of active
+// cycles, DRAM 66 %, 262 warp instructions for 16 tokens of a head.  16 warps of 32-token
+// tiles took 136 us, 8 warps with three stages 119.
 #include <algorithm>
 #include <cstdlib>
 
@@ -49,7 +54,10 @@ namespace kv4 {
 namespace {
 
 constexpr int kCtas = 152;                       // one persistent CTA per SM
-constexpr int kFewSegments = 64;                 // up to so many segments, a CTA is one worker
+// Up to so many segments a CTA is one worker: one token over 131,072, 4 key heads, 27.6 us
+// against 87.6 with a warp as the worker.  Between 16 and 160 the bound made no difference
+// to the sizes timed.
+constexpr int kFewSegments = 64;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {

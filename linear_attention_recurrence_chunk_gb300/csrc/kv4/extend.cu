@@ -10,8 +10,9 @@
 // both K-major with 128-byte swizzle, a tile ahead of the products; warps 8-11 and
 // 12-15 are the softmax of the two blocks, a thread per row, and the first of each four
 // issues its block's products.
-// While one block's softmax runs, the other's products do: per tile and block two
-// products of 128 x 128 x D against 128 exponentials per thread.
+// Nothing orders the blocks against each other, so that one's products may run under the
+// other's softmax: per tile and block two products of 128 x 128 x D against 128
+// exponentials per thread.
 //
 // Ranges.  A query row is scaled by a power of two to 2^14 <= max|q| < 2^15 (bf16 is exact
 // in fp16 then, but for channels 2^28 below the largest).  A tile's keys are held relative
@@ -25,8 +26,14 @@
 // reach rows that do not see the token, each row notes the groups of the tokens
 // that it gives a weight, and its output becomes NaN there.
 //
-// Bound: the tensor pipe and the exponentials (about 512 + 512 and 1,024 / 2 cycles a
-// tile and block).
+// Measured: 3 sequences, 3,394 tokens over 16,860 cached, 32 query on 8 key heads of 128,
+// 402 us, 38 % of the bf16 matrix rate for the causal work.  Counters: tensor pipe 34 % of
+// active cycles, ALU 37 %, issue 46 %, no unit full; the longest stall is the wait for
+// memory and TMEM loads.  With one part left out (results wrong, for timing only): the
+// weights' arithmetic 288 us, most of the products 327, the conversions 360.  Slower or
+// equal: scores in two buffers of 64 tokens 452, blocks in strict turns 452, two threads
+// per row on 24 warps 442, one pass with maxima by chunks 443, a row's scores kept in
+// registers 402 to 406.
 #include "attn_common.cuh"
 
 namespace kda {
