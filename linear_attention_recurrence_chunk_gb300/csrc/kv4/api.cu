@@ -188,8 +188,7 @@ kda_status kda_kv4_attention(const void* q, int64_t q_token_stride, int64_t q_he
   kda::kv4::AttnProblem p{q, q_token_stride, q_head_stride, static_cast<const uint8_t*>(cache), num_pages, page_size,
                           block_table, max_pages, seq_lens, cu_seqlens, T, N, Hq, Hkv, D, max_q_len, sm_scale, dt, o,
                           lse, nullptr, 0};
-  const uint64_t upp = (uint64_t)(page_size / kda::kv4::kUnit);
-  p.upp_inv = (((uint64_t)1 << 40) + upp - 1) / upp;
+  p.upp_inv = kda::kv4::page_inverse((uint32_t)(page_size / kda::kv4::kUnit));
   if (kda::device_error_ptr(&p.dev_err) != cudaSuccess) return KDA_ERR_CUDA;
   return kda::kv4::launch_attention(p, workspace, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
     if (lane == 0) tc::mbar_arrive_expect_tx(full + slot, units * U::kBytes);
     __syncwarp();
     if (lane < (in_page ? min(units, 1) : units)) {
-      const uint32_t unit = tile * C::MT + lane, at = (uint32_t)(unit * p.upp_inv >> 40);
+      const uint32_t unit = tile * C::MT + lane, at = page_of_unit(unit, p.upp_inv);
       int64_t page = p.table[(int64_t)pc.n * p.max_pages + at];
       if (page < 0 || page >= p.num_pages) {
         report_bad(p.dev_err);

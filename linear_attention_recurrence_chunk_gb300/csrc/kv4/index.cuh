@@ -1,0 +1,23 @@
+// Index arithmetic of the attention kernels over a paged cache, apart from the
+// kernels so that it can be compiled and checked on the host over its whole range.
+#pragma once
+
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#define KDA_INDEX_FN __host__ __device__ __forceinline__
+#else
+#define KDA_INDEX_FN inline
+#endif
+
+namespace kda {
+namespace kv4 {
+
+// unit / upp as a product, for unit < 2^27 (2^31 - 1 tokens) and upp <= 256 units of a page.
+// The inverse is above 2^36 / upp by less than 1, so the quotient by less than
+// 2^27 / 2^36 = 2^-9 <= 1 / (2 upp), which does not reach the next page; the product is at most 2^63.
+KDA_INDEX_FN uint64_t page_inverse(uint32_t upp) { return (((uint64_t)1 << 36) + upp - 1) / upp; }
+KDA_INDEX_FN uint32_t page_of_unit(uint32_t unit, uint64_t inverse) { return (uint32_t)(unit * inverse >> 36); }
+
+}  // namespace kv4
+}  // namespace kda

@@ -2,6 +2,7 @@
 // and the device helpers that its kernels share.
 #pragma once
 
+#include "index.cuh"
 #include "kda_internal.cuh"
 #include "kda_kv4.h"
 
@@ -76,7 +77,7 @@ struct AttnProblem {
   void* o;
   float* lse;
   int32_t* dev_err;
-  uint64_t upp_inv;         // 2^40 / (units of a page), rounded up: unit / units of a page by a product (exact, units < 2^28)
+  uint64_t upp_inv;         // page_inverse(units of a page)
 };
 size_t attention_workspace(int32_t Hq, int32_t Hkv, int32_t D, int32_t max_q, kda_dtype dt);
 cudaError_t launch_extend(const AttnProblem& p, cudaStream_t stream);   // bf16 only
