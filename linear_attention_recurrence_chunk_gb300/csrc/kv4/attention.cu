@@ -125,7 +125,7 @@ struct Cfg {
   static constexpr int tV = TILE * GR * 4, tRow = tV + TILE * 8, kTab = tRow + R * 16;
   static constexpr int kPart = R * (D + 2) * 4;     // a warp's result in shared memory: O, then (m, l)
   static constexpr int oQ = W * kRing, oTab = oQ + W * kQ, oBar = oTab + W * kTab, oSum = oBar + W * STAGES * 8,
-                       kSmem = oSum + (W + 3) * 8;
+                       kSmem = oSum + (W + 1) * 8;
   static_assert(kPart <= kRing, "a warp's result fits its ring");
   static_assert(kSmem <= 232448, "shared memory");
   static_assert(kStage % 16 == 0 && kRing % 128 == 0 && kTab % 16 == 0, "alignment");
@@ -531,11 +531,17 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
   __syncthreads();
   if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long*>(sums + C::W), (unsigned long long)(segs * p.Hkv));
   __syncthreads();
-  int64_t total = 0;
-  for (int w = 0; w < C::W; ++w) total += sums[w];
   const bool wide = sums[C::W] <= kFewSegments;   // a CTA is one worker
-  const int64_t most = wide ? gridDim.x : (int64_t)gridDim.x * C::W;
-  const int64_t workers = min(most, total);
+  // The line's length and its workers, from sums that no warp writes any more.  Called again where a segment outlasts
+  // the worker's part (hence volatile): fewer registers in the loop.
+  auto whole_line = [&](int64_t& total, int64_t& workers) {
+    const volatile int64_t* v = sums;
+    total = 0;
+    for (int w = 0; w < C::W; ++w) total += v[w];
+    workers = min(wide ? (int64_t)gridDim.x : (int64_t)gridDim.x * C::W, total);
+  };
+  int64_t total, workers;
+  whole_line(total, workers);
   const int64_t me = wide ? blockIdx.x : (int64_t)blockIdx.x * C::W + warp;
   // every entry of the owner table is written: a wide grid's workers have the first ones
   int4* own_at = parts.owner + (wide ? (int64_t)warp * gridDim.x + blockIdx.x : me);
@@ -544,10 +550,6 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
     return;
   }
   const int64_t x0 = me * total / workers;
-  if (threadIdx.x == 0) {   // read again at the end of a part that a segment outlasts: fewer registers in the loop
-    sums[C::W + 1] = total;
-    sums[C::W + 2] = workers;
-  }
 
   Cursor<C> cur;   // find x0: the warp's range, then the sequence
   {
@@ -753,8 +755,8 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
     const bool starts = first == 0, whole = starts && last == cur.s.tiles;
     const int64_t slot = 2 * me + (starts ? 1 : 0);
     if (starts && !whole) {   // this worker's last piece; who has the rest of the segment?
-      const volatile int64_t* v = sums + C::W + 1;
-      const int64_t all = v[0], cut = v[1];
+      int64_t all, cut;
+      whole_line(all, cut);
       const int64_t y = (me + 1) * all / cut - cur.left - cur.pos + C::HEAD + cur.s.tiles - 1;   // its last tile on the line
       owner = make_int4(cur.s.q0, h * 64 + rows, rt * C::R, (int)(((y + 1) * cut - 1) / all - me));
     }

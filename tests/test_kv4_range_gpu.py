@@ -47,3 +47,35 @@ def one_token_far_away(L, ps, at, D=64, dt=BF):
 def test_pages_beyond_two_to_the_24(ps):
     """More table entries than 24 bits count, and the token that matters behind them."""
     one_token_far_away(((1 << 24) + 9) * ps + 3, ps, ((1 << 24) + 5) * ps + 7)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("Hq,Hkv,lens", [(8, 2, [3000] * 40), (16, 8, [701, 0, 4000, 65] * 7), (4, 4, [20000])])
+def test_cut_segments_are_joined_alike_every_time(dt, Hq, Hkv, lens):
+    """Most workers' parts end inside a segment here, so that its pieces go through the workspace: which workers
+    have them depends on the lengths alone.  Between the calls others leave their own sums in shared memory."""
+    ps, D = 32, 128
+    gen = torch.Generator(device=DEV).manual_seed(len(lens))
+    T = max(lens)
+    cache = kda.kda_kv4_cache(-(-T // ps), Hkv, ps, D)
+    k, v = (torch.randn(T, Hkv, D, device=DEV, generator=gen).to(BF) for _ in range(2))
+    kda.kda_kv4_append(k, v, torch.arange(T, dtype=torch.int32, device=DEV), cache)
+    table = torch.arange(cache.shape[0], dtype=torch.int32, device=DEV).repeat(len(lens), 1)
+    q = torch.randn(len(lens), Hq, D, device=DEV, generator=gen).to(dt)
+    dl, other = i32(lens), i32([17 + 31 * i for i in range(len(lens))])
+    want = kda.kda_kv4_attention(q, cache, table, dl, return_lse=True)
+    for _ in range(20):
+        kda.kda_kv4_attention(q, cache, table, other)
+        got = kda.kda_kv4_attention(q, cache, table, dl, return_lse=True)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # the same rows in calls of their own, cut at other places, agree to the output's rounding
+    for n in range(0, len(lens), 9):
+        o, lse = kda.kda_kv4_attention(q[n:n + 1], cache, table[n:n + 1], dl[n:n + 1], return_lse=True)
+        if lens[n] == 0:
+            assert not o.any() and torch.isneginf(lse).all()
+            continue
+        # two evaluations, each off by half a step of its type and of its weights (fp16, or two parts) on values of at most 6
+        step = 2.0 ** -8 + 2.0 ** -11 if dt is BF else 2.0 ** -20
+        assert ((o - want[0][n:n + 1]).float().abs() <= 2 * step * 6).all()
+        assert ((lse - want[1][n:n + 1]).abs() <= 2.0 ** -18 * lse.abs().clamp(min=1.0)).all()
+    no_error()
