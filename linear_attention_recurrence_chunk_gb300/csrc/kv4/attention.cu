@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
     pk += step;
     const int slot = issued % C::STAGES;
     ++issued;
-    const int units = min(C::MT, (pc.s.L + kUnit - 1) / kUnit - tile * C::MT);   // 0 for an empty sequence
+    const int units = units_of_tile(pc.s.L, tile, C::MT);   // 0 for an empty sequence
     if (lane == 0) tc::mbar_arrive_expect_tx(full + slot, units * U::kBytes);
     __syncwarp();
     if (lane < (in_page ? min(units, 1) : units)) {

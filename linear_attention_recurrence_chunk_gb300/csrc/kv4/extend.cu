@@ -145,9 +145,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_extend_kernel(const __grid_co
     // Loads run ahead of their use: page pointers two tiles, scales and codes one.  A
     // warp finds the tile's largest scale by itself, from all tokens' scales.
     const int upp = p.page_size / kUnit;
-    auto unit_ptr = [&](int tok) -> const uint8_t* {   // null behind the last token
+    auto unit_ptr = [&](int64_t tok) -> const uint8_t* {   // null behind the last token
       if (tok >= s.L) return nullptr;
-      const int unit = tok / kUnit;
+      const int unit = (int)tok / kUnit;
       int64_t page = p.table[(int64_t)n * p.max_pages + unit / upp];
       if (page < 0 || page >= p.num_pages) {
         report_bad(p.dev_err);
@@ -225,8 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_extend_kernel(const __grid_co
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(kfull + st);
-        ku = unit_ptr((i + 2) * kTok + tid);
-        au = unit_ptr((i + 2) * kTok + 4 * lane);
+        ku = unit_ptr(token_of_tile(i + 2, kTok, tid));
+        au = unit_ptr(token_of_tile(i + 2, kTok, 4 * lane));
       }
     } else {
       // thread: 8-token block vb of the tile, g
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_extend_kernel(const __grid_co
           const uint32_t* w = reinterpret_cast<const uint32_t*>(vs4);
           vs[t] = GR == 4 ? w[t] : w[t >> 1] >> (16 * (t & 1)) & 0xffffu;
         }
-        if (tv + 8 > s.L) {
+        if (s.L - tv < 8) {
 #pragma unroll
           for (int t = 0; t < 8; ++t)
             if (tv + t >= s.L) vs[t] = 0;
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_extend_kernel(const __grid_co
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(vfull + st);
-        vu = unit_ptr((i + 2) * kTok + 8 * vb);
+        vu = unit_ptr(token_of_tile(i + 2, kTok, 8 * vb));
       }
     }
   } else {

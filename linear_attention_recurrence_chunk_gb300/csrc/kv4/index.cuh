@@ -19,5 +19,16 @@ namespace kv4 {
 KDA_INDEX_FN uint64_t page_inverse(uint32_t upp) { return (((uint64_t)1 << 36) + upp - 1) / upp; }
 KDA_INDEX_FN uint32_t page_of_unit(uint32_t unit, uint64_t inverse) { return (uint32_t)(unit * inverse >> 36); }
 
+// Token `at` of tile i, tiles of `tokens`.  What is loaded ahead lies up to two tiles behind the
+// last, and a sequence may have 2^31 - 1 tokens: 64 bits.
+KDA_INDEX_FN int64_t token_of_tile(int64_t i, int32_t tokens, int32_t at) { return i * tokens + at; }
+
+// Units of 16 tokens, `most` at most, that tile i (tiles of `most` units) holds of a sequence of L.
+// (L + 15 passes 31 bits.)
+KDA_INDEX_FN int32_t units_of_tile(int32_t L, int32_t i, int32_t most) {
+  const int32_t n = (int32_t)(((uint32_t)L + 15) / 16) - i * most;
+  return n < most ? n : most;
+}
+
 }  // namespace kv4
 }  // namespace kda

@@ -25,6 +25,8 @@ int64_t first_wrong_page(uint32_t upp, int64_t n) {
   }
   return -1;
 }
+int64_t token(int64_t i, int32_t tokens, int32_t at) { return token_of_tile(i, tokens, at); }
+int32_t units(int32_t L, int32_t i, int32_t most) { return units_of_tile(L, i, most); }
 }
 """
 
@@ -37,6 +39,8 @@ def lib(tmp_path_factory):
                    check=True)
     lib = ctypes.CDLL(str(d / "index.so"))
     lib.first_wrong_page.argtypes, lib.first_wrong_page.restype = [ctypes.c_uint32, ctypes.c_int64], ctypes.c_int64
+    lib.token.argtypes, lib.token.restype = [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32], ctypes.c_int64
+    lib.units.argtypes, lib.units.restype = [ctypes.c_int32] * 3, ctypes.c_int32
     return lib
 
 
@@ -52,3 +56,23 @@ def test_page_of_a_unit_every_page_size(lib):
     """The other page sizes at their last pages, where an inverse that is cut off too early shows first."""
     for upp in range(1, 257):
         assert lib.first_wrong_page(upp, 1 << 20) == -1, upp
+
+
+MOST = (1 << 31) - 1
+
+
+@pytest.mark.parametrize("L", [1, 127, 128, 129, 1 << 28, MOST - 512, MOST - 127, MOST])
+def test_tokens_loaded_ahead(lib, L):
+    """The tiles of 128 tokens up to two behind the last: every token keeps its place, below L or not."""
+    last = (L - 1) // 128
+    for i in range(max(last - 3, 0), last + 3):
+        for at in (0, 1, 64, 127):
+            assert lib.token(i, 128, at) == 128 * i + at
+
+
+@pytest.mark.parametrize("L", [0, 1, 16, 17, 63, 64, 65, 1 << 28, MOST - 65, MOST - 16, MOST - 15, MOST])
+def test_units_of_a_tile(lib, L):
+    tiles = max(-(-L // 64), 1)
+    for i in range(max(tiles - 3, 0), tiles):
+        assert lib.units(L, i, 4) == min(4, -(-L // 16) - 4 * i)
+    assert L == 0 or 1 <= lib.units(L, tiles - 1, 4) <= 4

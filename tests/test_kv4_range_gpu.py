@@ -82,3 +82,9 @@ def test_cut_segments_are_joined_alike_every_time(dt, Hq, Hkv, lens):
         assert ((o - want[0][n:n + 1]).float().abs() <= 2 * step * 6).all()
         assert ((lse - want[1][n:n + 1]).abs() <= 2 * (ds + 2.0 ** -21 * lse.abs())).all()
     no_error()
+
+
+@pytest.mark.parametrize("at", [0, (1 << 31) - 2])
+def test_the_longest_sequence(at):
+    """2^31 - 1 tokens, the one that matters the first or the last of them."""
+    one_token_far_away((1 << 31) - 1, 4096, at)
