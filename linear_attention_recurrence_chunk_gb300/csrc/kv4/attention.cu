@@ -183,7 +183,8 @@ struct Acc {
 
 // A tile's scales into the warp's tables.  E, the reference of the value scales, is the
 // largest of a piece's first tile (fresh), raised when one is above 2^(E + 1) later.  Returns whether the tile
-// needs the careful step: a group that is not finite, or a value scale outside
+// needs the careful step: a group that is not finite, a key scale of 2^97 or more (the scores'
+// sums, up to 2^24.6 of it before the rows' factors, might pass fp32), or a value scale outside
 // 2^(E - 14) .. 2^(E + 1), whose fp16 relative to E is not a normal number.
 template <class C>
 __device__ __forceinline__ bool load_scales(const uint8_t* st, uint8_t* tab, int left, bool fresh, int& E) {
@@ -218,11 +219,11 @@ __device__ __forceinline__ bool load_scales(const uint8_t* st, uint8_t* tab, int
     v[1] = (uint32_t)E * kOnes;
   }
   // exponent fields of the value scales less one: a byte outside 0 .. 15 (or a borrow, which leaves one) shows in
-  // the high nibbles, for E <= 239; a key byte of 255 by a carry
+  // the high nibbles, for E <= 239; a key byte of 224 or more by a carry
   uint32_t d0 = v[0] - (uint32_t)(E - 14) * kOnes, d1 = v[1] - (uint32_t)(E - 14) * kOnes;
   uint32_t odd = (d0 | d1) & (C::GR == 4 ? 0xf0f0f0f0u : 0xfffff0f0u);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) odd |= ((k[i] & 0x7f7f7f7fu) + 0x01010101u) & k[i] & 0x80808080u;
+  for (int i = 0; i < 2; ++i) odd |= ((k[i] & 0x7f7f7f7fu) + 0x20202020u) & k[i] & 0x80808080u;
   const bool careful = __any_sync(0xffffffffu, odd != 0) || E > 239;
   if (careful) {
     const int vm = largest();
@@ -319,10 +320,15 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const float* ktab, 
           }
         }
         float(&s)[4] = S[mt][nt];
-        s[0] = j ? fmaf(ks[0][j], c[0], s[0]) : ks[0][j] * c[0];
-        s[1] = j ? fmaf(ks[0][j], c[1], s[1]) : ks[0][j] * c[1];
-        s[2] = j ? fmaf(ks[1][j], c[2], s[2]) : ks[1][j] * c[2];
-        s[3] = j ? fmaf(ks[1][j], c[3], s[3]) : ks[1][j] * c[3];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float f = ks[e >> 1][j];
+          if constexpr (kCareful) {   // the row's factor joins the scale before the sum; a product beyond fp32 only meets sums near 0
+            f *= e & 1 ? cfs[4 * nt].y : cfs[4 * nt].x;
+            if (f > 0x1p127f) f = 0x1p127f;   // (a NaN stays)
+          }
+          s[e] = j ? fmaf(f, c[e], s[e]) : f * c[e];
+        }
       }
     }
     if (cut) {
@@ -341,9 +347,9 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const float* ktab, 
   float f[C::NT][2], ref[C::NT][2], cf[C::NT][2];
 #pragma unroll
   for (int nt = 0; nt < C::NT; ++nt) {
-    const float2 x = cfs[4 * nt];
-    cf[nt][0] = x.x;
-    cf[nt][1] = x.y;
+    const float2 x = kCareful ? make_float2(1.f, 1.f) : cfs[4 * nt];
+    cf[nt][0] = fmaxf(x.x, 0x1p-149f);   // above 0, so that -inf keeps its sign
+    cf[nt][1] = fmaxf(x.y, 0x1p-149f);
   }
 #pragma unroll
   for (int nt = 0; nt < C::NT; ++nt)
@@ -673,7 +679,7 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
       const uint32_t ex = min(max(top >> 23, 27u), 254u);
       // the sign of sm_scale goes with q, so that the factor of a score is positive
       const float up = copysignf(__uint_as_float((268u - ex) << 23), p.sm_scale);
-      const float down = fmaxf(__uint_as_float((ex - 14u) << 23) * fabsf(p.sm_scale) * kLog2e, 1.17549435e-38f);
+      const float down = __uint_as_float((ex - 14u) << 23) * fabsf(p.sm_scale) * kLog2e;
       if (t == 0) {
         reinterpret_cast<float*>(tab + C::tRow)[r] = down;
         const int rr = rt * C::R + r, tok = rr / G;

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import linear_attention_recurrence_chunk_gb300 as kda
+from test_kv4_attention_gpu import Setup, kernel  # noqa: F401  (a fixture)
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -88,3 +89,18 @@ def test_cut_segments_are_joined_alike_every_time(dt, Hq, Hkv, lens):
 def test_the_longest_sequence(at):
     """2^31 - 1 tokens, the one that matters the first or the last of them."""
     one_token_far_away((1 << 31) - 1, 4096, at)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("D", [64, 128])
+def test_keys_far_above_and_queries_far_below_one(dt, D, kernel):
+    """Finite scores (of a few tens) whose sums pass 2^128 when a row of q is scaled to 2^14."""
+    s = Setup(dt, D, 8, 1, 16, [300, 40], [1, 2], spread=2.0 ** -98, kscale=2.0 ** 112)
+    s.check(*s.run(sm_scale=2.0 ** -15), scale=2.0 ** -15)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_scale_of_zero_with_the_largest_keys(dt, kernel):
+    """sm_scale = 0: every token the same weight, whatever its key."""
+    s = Setup(dt, 128, 8, 2, 16, [300, 40], [1, 2], kscale=2.0 ** 122)
+    s.check(*s.run(sm_scale=0.0), scale=0.0)
