@@ -457,8 +457,11 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const float* ktab, 
             for (int hf = 0; hf < 2; ++hf) {   // the token of this lane's two weights
               const float sc = scale_at<true>(vw[g + 8 * hf], j) * to_e;
               const float p0 = S[mt][nt][2 * hf], p1 = S[mt][nt][2 * hf + 1];
-              // a token that a row does not see adds nothing to it, whatever its values are
-              const float w0 = p0 == 0.f ? 0.f : p0 * sc, w1 = p1 == 0.f ? 0.f : p1 * sc;
+              // a token that a row does not see adds nothing to it, whatever its values are; one that it sees makes it NaN
+              // where they are, also with a weight of 0
+              const int2 lim = lims[4 * nt];
+              const int tok = tok0 + mt * kUnit + g + 8 * hf;
+              const float w0 = tok > lim.x ? 0.f : p0 * sc, w1 = tok > lim.y ? 0.f : p1 * sc;
               const uint32_t hi = pack(w0, w1);
               b[hf][0] = transpose8x8(hi);
               if constexpr (C::PARTS == 2) b[hf][C::PARTS - 1] = transpose8x8(pack_rest(w0, w1, hi));

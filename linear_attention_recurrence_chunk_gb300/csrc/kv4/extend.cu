@@ -24,7 +24,7 @@
 // weights reach 2^15 and lose bits below 2^-23 of the largest.
 // Groups that are not finite: keys become NaN operands; for values, whose NaN would
 // reach rows that do not see the token, each row notes the groups of the tokens
-// that it gives a weight, and its output becomes NaN there.
+// that it sees, and its output becomes NaN there.
 //
 // Measured: 3 sequences, 3,394 tokens over 16,860 cached, 32 query on 8 key heads of 128,
 // 402 us, 38 % of the bf16 matrix rate for the causal work.  Counters: tensor pipe 34 % of
@@ -486,12 +486,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_extend_kernel(const __grid_co
           sum[e & 1] = __fadd2_rn(sum[e & 1], make_float2(v[2 * e], v[2 * e + 1]));
         }
         tc::tmem_st16(tc::tmem_addr(tmem, tl, cS + 16 * c), w);   // over scores that have been read
-        if (mt.w) {   // groups that are not finite, of the tokens that this row gives a weight
-          uint32_t some = 0;
-#pragma unroll
-          for (int e = 0; e < 32; ++e) some |= (v[e] != 0.f ? 1u : 0u) << e;
+        if (mt.w) {   // groups that are not finite, of the tokens that this row sees (with a weight of 0 too)
 #pragma unroll 1
-          for (int e = 0; e < 32; ++e) nans |= some >> e & 1u ? sm[M::oFlags + st * kTok + 32 * c + e] : 0u;
+          for (int e = 0; e < 32; ++e) nans |= t0 + 32 * c + e <= lim ? sm[M::oFlags + st * kTok + 32 * c + e] : 0u;
         }
       };
 #pragma unroll 1

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import linear_attention_recurrence_chunk_gb300 as kda
-from test_kv4_attention_gpu import Setup, kernel  # noqa: F401  (a fixture)
+from test_kv4_attention_gpu import Setup, kernel, run_check  # noqa: F401  (a fixture)
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -104,3 +104,14 @@ def test_scale_of_zero_with_the_largest_keys(dt, kernel):
     """sm_scale = 0: every token the same weight, whatever its key."""
     s = Setup(dt, 128, 8, 2, 16, [300, 40], [1, 2], kscale=2.0 ** 122)
     s.check(*s.run(sm_scale=0.0), scale=0.0)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("spread", [1.0, 64.0])
+def test_not_finite_values_of_tokens_whose_weight_is_far_below_the_largest(dt, spread, kernel):
+    """A query sees them wherever they lie, also where fp32 has no weight as small (spread 64: most weights here)."""
+    def edit(k, v, rng):
+        for tok, head, ch in [(5, 0, 40), (63, 1, 3), (200, 0, 100), (395, 1, 70), (397, 0, 5)]:
+            v[tok, head, ch] = np.inf if tok % 2 else np.nan
+    run_check(dt, 128, 8, 2, 16, [400, 30], [6, 1], edit=edit, spread=spread)
+    run_check(dt, 64, 4, 4, 32, [400], [3], edit=lambda k, v, rng: edit(k, np.concatenate([v, v], -1), rng), spread=spread)
