@@ -89,7 +89,8 @@ def _device(name: str, t: torch.Tensor, dtype: Optional[torch.dtype] = None) -> 
     return dev
 
 
-_current_raw_stream = torch._C._cuda_getCurrentRawStream   # the handle alone: no Stream object per call
+# The handle alone: no Stream object per call.  A PyTorch without CUDA does not have it, and has no tensor that gets as far.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _run(dev: int, stream, f):
