@@ -63,8 +63,11 @@ KDA_API size_t kda_kv4_cache_bytes(int64_t num_pages, int32_t Hkv, int32_t page_
  * asks for: tokens whose page is not there (the free pages used up, the row too short, a
  * partly filled page with a negative entry) get slot -1, table entries without a free page
  * get -1; negative lengths count as 0; of more than num_tokens new tokens the first are
- * mapped.  Each of these is reported (kda_device_error).  The same inputs give the same
- * outputs, whatever the table's entries behind the cached pages hold.
+ * mapped, and pages that begin behind them get the entry -1.  Each of these is reported
+ * (kda_device_error).  seq_lens and free_next count every new token and its pages, those
+ * without a slot among them: after a report a caller goes on from its own lengths, table and
+ * free_start of before the call.  The same inputs give the same outputs, whatever the table's
+ * entries behind the cached pages hold.
  * N is at most 28672 (its prefix sums are held in shared memory), else KDA_ERR_UNSUPPORTED.
  * No output may overlap an input or another output.
  */

@@ -101,6 +101,16 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const PageMapProblem
   if (bad && lead) report_bad(p.dev_err);
   __syncthreads();
 
+  // More new tokens than there is room for (reported above): pages whose first token is not mapped get the entry -1,
+  // so that no entry of an earlier step stands for one.  (A capped cu[i] is beyond num_tokens all the same.)
+  if (total > p.num_tokens) {
+    for (int i = blockIdx.x * kThreads + tid; i < p.N; i += gridDim.x * kThreads) {
+      const int64_t c = clamped(p.cached[i]), n = clamped(p.fresh[i]);
+      const int64_t full = min((c + n + ps - 1) / ps, (int64_t)p.max_pages), known = max(p.num_tokens - cu[i], (int64_t)0);
+      for (int64_t j = (c + known + ps - 1) / ps; j < full; ++j) p.table[(int64_t)i * p.max_pages + j] = -1;
+    }
+  }
+
   const int32_t known = cu[p.N];
   bool lost = false;
   for (int32_t tile = blockIdx.x; tile < n_tiles; tile += gridDim.x) {
