@@ -126,10 +126,11 @@ KDA_API size_t kda_kv4_attention_workspace_size(int64_t T, int32_t N, int32_t Hq
  * see it NaN (of a value group: its 32 channels).
  * Scores, softmax statistics and sums are fp32.  bf16 inputs multiply exactly (a row of q is
  * scaled by a power of two into fp16's range), the softmax weights enter the second product
- * as fp16, relative to the largest; fp32 inputs take both products in two fp16 parts.  bf16
- * calls with many query rows per key/value head (max_q_len Hq / Hkv) run a kernel that also
- * holds keys and values in fp16, relative to the largest scale of a tile and of the sequence
- * so far: exact for groups down to 2^-21 of it.
+ * as fp16, relative to the largest and to the largest scale of their 32 value channels so far;
+ * fp32 inputs take both products in two fp16 parts.  bf16 calls with many query rows per
+ * key/value head (max_q_len Hq / Hkv) run a kernel that also holds keys and values in fp16,
+ * keys relative to the largest scale of 128 tokens, values to that of their 32 channels so far:
+ * exact for groups down to 2^-21 of it.
  * A length beyond the table, a page beyond the cache, a cu_seqlens that decreases, does not
  * begin at 0 or passes T, and a sequence of more than max_q_len tokens are reported; the
  * outputs of such a sequence are unspecified, no access leaves the arrays.

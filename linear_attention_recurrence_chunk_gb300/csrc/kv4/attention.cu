@@ -22,11 +22,12 @@
 // scale of the channel group.
 // Ranges.  A query row is scaled by a power of two to 2^14 <= max|q| < 2^15, which
 // is exact in fp16 but for channels 2^28 below the largest.  Weights are 2^14 at
-// most and multiplied, transposed, by the value scales relative to a reference,
-// 2^(e - E) <= 2, in fp16: exact where e - E >= -14 and a product is normal; a tile
-// with smaller ones multiplies in fp32 first.  E is the largest e seen, or one below
-// it, and at least 2^-27; the output follows it.  So a weight loses bits only when
-// p 2^(e - E) is below 2^-28.
+// most and multiplied, transposed, by the value scales relative to a reference of
+// their channel group, 2^(e - E) <= 2, in fp16: exact where e - E >= -14 and a product is
+// normal; a tile with smaller ones multiplies in fp32 first.  E is the largest e seen in
+// the group, or one below it, and at least 2^-107; the group's output follows it.  So a
+// weight loses bits only when p 2^(e - E) is below 2^-28.  The sum l takes the weights
+// before they are rounded.
 // fp32 inputs: q and the weights each as the sum of two fp16 numbers, two products
 // for one.
 //
@@ -181,16 +182,23 @@ struct Acc {
   float m[C::NT][2], l[C::NT][2];   // running maximum (log2) and sum of 2^(s - m + 14) of each column
 };
 
-// A tile's scales into the warp's tables.  E, the reference of the value scales, is the
+// 2^x, 0 below the smallest normal number; x <= 127
+__device__ __forceinline__ float pow2(int x) { return __uint_as_float((uint32_t)max(127 + x, 0) << 23); }
+__device__ __forceinline__ int byte_of(uint32_t w, int i) { return (int)(w >> (8 * i) & 0xffu); }
+
+template <class C>
+constexpr uint32_t kOnes = C::GR == 4 ? 0x01010101u : 0x0101u;   // a byte per group
+constexpr uint32_t kLeastE = 20;                                  // 2^-107
+
+// A tile's scales into the warp's tables.  E, a byte per channel group, the reference of its value scales, is the
 // largest of a piece's first tile (fresh), raised when one is above 2^(E + 1) later.  Returns whether the tile
 // needs the careful step: a group that is not finite, a key scale of 2^97 or more (the scores'
 // sums, up to 2^24.6 of it before the rows' factors, might pass fp32), or a value scale outside
 // 2^(E - 14) .. 2^(E + 1), whose fp16 relative to E is not a normal number.
 template <class C>
-__device__ __forceinline__ bool load_scales(const uint8_t* st, uint8_t* tab, int left, bool fresh, int& E) {
+__device__ __forceinline__ bool load_scales(const uint8_t* st, uint8_t* tab, int left, bool fresh, uint32_t& E) {
   using U = Unit<C::D>;
   const int lane = threadIdx.x & 31;
-  constexpr uint32_t kOnes = C::GR == 4 ? 0x01010101u : 0x0101u;
   uint32_t k[2] = {0, 0}, v[2] = {0, 0};   // of tokens 2 lane, 2 lane + 1; a byte per group
   const bool in = lane < C::TILE / 2;
   if (in) {
@@ -204,31 +212,34 @@ __device__ __forceinline__ bool load_scales(const uint8_t* st, uint8_t* tab, int
     }
   }
   const int have = min(left - 2 * lane, in ? 2 : 0);   // of the two tokens; the cache may hold anything behind the last
-  auto largest = [&]() -> int {                        // value scale but 255
-    uint32_t m = 0;
+  auto raise = [&](uint32_t room) {                    // E to a group's largest value scale but 255 where that is more than E + room
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < C::GR; ++j) {
+      uint32_t m = 0;
 #pragma unroll
-      for (int j = 0; j < C::GR; ++j) m = max(m, i < have ? (v[i] >> (8 * j) & 0xffu) % 255u : 0u);
-    return (int)__reduce_max_sync(0xffffffffu, m);
+      for (int i = 0; i < 2; ++i) m = max(m, i < have ? (v[i] >> (8 * j) & 0xffu) % 255u : 0u);
+      m = __reduce_max_sync(0xffffffffu, m);
+      if (m > (E >> (8 * j) & 0xffu) + room) E = (E & ~(0xffu << (8 * j))) | m << (8 * j);
+    }
   };
-  if (fresh) E = max(100, largest());
+  if (fresh) {
+    E = kLeastE * kOnes<C>;
+    raise(0);
+  }
   if (have < 2) {   // tokens that are not there: nothing that a weight of 0 would not cancel
-    if (have < 1) k[0] = 0, v[0] = (uint32_t)E * kOnes;
+    if (have < 1) k[0] = 0, v[0] = E;
     k[1] = 0;
-    v[1] = (uint32_t)E * kOnes;
+    v[1] = E;
   }
   // exponent fields of the value scales less one: a byte outside 0 .. 15 (or a borrow, which leaves one) shows in
   // the high nibbles, for E <= 239; a key byte of 224 or more by a carry
-  uint32_t d0 = v[0] - (uint32_t)(E - 14) * kOnes, d1 = v[1] - (uint32_t)(E - 14) * kOnes;
+  uint32_t d0 = v[0] - (E - 14 * kOnes<C>), d1 = v[1] - (E - 14 * kOnes<C>);
   uint32_t odd = (d0 | d1) & (C::GR == 4 ? 0xf0f0f0f0u : 0xfffff0f0u);
 #pragma unroll
   for (int i = 0; i < 2; ++i) odd |= ((k[i] & 0x7f7f7f7fu) + 0x20202020u) & k[i] & 0x80808080u;
-  const bool careful = __any_sync(0xffffffffu, odd != 0) || E > 239;
-  if (careful) {
-    const int vm = largest();
-    if (vm > E + 1) E = vm;
-  }
+  odd |= E & E << 1 & E << 2 & E << 3 & 0x80808080u;   // E > 239
+  const bool careful = __any_sync(0xffffffffu, odd != 0);
+  if (careful) raise(1);
   if (in) {
     float* kf = reinterpret_cast<float*>(tab) + 2 * lane * C::GR;
 #pragma unroll
@@ -244,8 +255,8 @@ __device__ __forceinline__ bool load_scales(const uint8_t* st, uint8_t* tab, int
       else reinterpret_cast<float2*>(kf)[i] = make_float2(f[0], f[1]);
     }
     if (!careful) {
-      d0 += kOnes;   // exponent fields 1 .. 16
-      d1 += kOnes;
+      d0 += kOnes<C>;   // exponent fields 1 .. 16
+      d1 += kOnes<C>;
       uint32_t h[C::GR];
 #pragma unroll
       for (int j = 0; j < C::GR; ++j) h[j] = (__byte_perm(d0, d1, j | (4 + j) << 8) & 0x001f001fu) << 10;
@@ -263,11 +274,11 @@ __device__ __forceinline__ bool load_scales(const uint8_t* st, uint8_t* tab, int
 }
 
 // One step of MH units.  cut: rows see only a part of it (a flag and not another instance, which would
-// crowd the instruction cache).  kCareful: see load_scales.
+// crowd the instruction cache).  was: E before this tile.  kCareful: see load_scales.
 template <class C, bool kCareful>
 __device__ __forceinline__ void tile_step(const uint8_t* st, const float* ktab, const uint8_t* vtab, const uint8_t* rowtab,
                                           const uint32_t (&qr)[C::QREG ? C::NT : 1][C::QREG ? C::KS : 1][2],
-                                          const uint8_t* qs, int tok0, bool cut, int E, float moved, Acc<C>& a) {
+                                          const uint8_t* qs, int tok0, bool cut, uint32_t E, uint32_t was, Acc<C>& a) {
   using U = Unit<C::D>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const float2* cfs = reinterpret_cast<const float2*>(rowtab) + t;                 // of columns 2 t, 2 t + 1
@@ -342,8 +353,8 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const float* ktab, 
     }
   }
 
-  // running maximum of each column; the accumulators follow it, and E by `moved`
-  bool move = moved != 1.f;
+  // running maximum of each column; the accumulators follow it, and E
+  bool move = was != E;
   float f[C::NT][2], ref[C::NT][2], cf[C::NT][2];
 #pragma unroll
   for (int nt = 0; nt < C::NT; ++nt) {
@@ -373,11 +384,12 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const float* ktab, 
     for (int nt = 0; nt < C::NT; ++nt) {
       a.l[nt][0] *= f[nt][0];
       a.l[nt][1] *= f[nt][1];
-      const float fo[2] = {f[nt][0] * moved, f[nt][1] * moved};
 #pragma unroll
-      for (int i = 0; i < 2 * C::GR; ++i)
+      for (int i = 0; i < 2 * C::GR; ++i) {
+        const float moved = pow2(byte_of(was, i / 2) - byte_of(E, i / 2));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) a.O[i][nt][e] *= fo[e & 1];
+        for (int e = 0; e < 4; ++e) a.O[i][nt][e] *= f[nt][e & 1] * moved;
+      }
     }
   }
 #pragma unroll
@@ -390,7 +402,6 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const float* ktab, 
       a.l[nt][1] += S[mt][nt][1] + S[mt][nt][3];
     }
 
-  const float to_e = kCareful ? __uint_as_float(E < 254 ? (uint32_t)(254 - E) << 23 : 0x00400000u) : 1.f;   // 2^(127 - E)
 #pragma unroll
   for (int mt = 0; mt < C::MH; ++mt) {
     const uint8_t* u = st + mt * U::kBytes;
@@ -453,6 +464,8 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const float* ktab, 
               for (int part = 0; part < C::PARTS; ++part) b[hf][part] = mul2(pk[hf][nt][part], vs[hf][j]);
           } else {
             const uint32_t* vw = reinterpret_cast<const uint32_t*>(vtab) + mt * kUnit;
+            const int ej = byte_of(E, j);
+            const float to_e = __uint_as_float(ej < 254 ? (uint32_t)(254 - ej) << 23 : 0x00400000u);   // 2^(127 - E)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {   // the token of this lane's two weights
               const float sc = scale_at<true>(vw[g + 8 * hf], j) * to_e;
@@ -718,17 +731,17 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
 #pragma unroll
         for (int i = 0; i < 2 * C::GR; ++i) a.O[i][nt][e] = a.O[i][nt][e + 2] = 0.f;
       }
-    int E = 100;
+    uint32_t E = kLeastE * kOnes<C>;
     for (int tile = first + wi; tile < last; tile += step) {
       const int slot = used % C::STAGES, tok0 = tile * C::TILE;
       const uint8_t* st = ring + slot * C::kStage;
       if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(full + slot, (used / C::STAGES) & 1, kWaitLimit));
       ++used;
       if (ok && cur.s.L > 0) {
-        const int was = E;
+        uint32_t was = E;
         const bool fresh = tile == first + wi;
         const bool careful = load_scales<C>(st, tab, cur.s.L - tok0, fresh, E);
-        const float moved = E == was || fresh ? 1.f : __uint_as_float((uint32_t)max(127 + was - E, 0) << 23);
+        if (fresh) was = E;
 #pragma unroll 1
         for (int u = 0; u < C::MT && tok0 + u * kUnit < cur.s.L; u += C::MH) {
           const uint8_t* su = st + u * U::kBytes;
@@ -737,17 +750,33 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
           const uint8_t* vtab = tab + C::tV + u * (careful ? kUnit * 4 : 8 * C::GR * 4);
           const int tok = tok0 + u * kUnit;
           const bool cut = tok + C::MH * kUnit - 1 > lim_all;
-          const float follow = u == 0 ? moved : 1.f;
-          if (careful) tile_step<C, true>(su, ktab, vtab, tab + C::tRow, qr, qs, tok, cut, E, follow, a);
-          else tile_step<C, false>(su, ktab, vtab, tab + C::tRow, qr, qs, tok, cut, E, follow, a);
+          if (careful) tile_step<C, true>(su, ktab, vtab, tab + C::tRow, qr, qs, tok, cut, E, was, a);
+          else tile_step<C, false>(su, ktab, vtab, tab + C::tRow, qr, qs, tok, cut, E, was, a);
+          was = E;
         }
       }
       __syncwarp();
       if (ok) produce();
     }
-    // each column's sum, and both it and the reference on the scale of O: O / l is the output
+    // The groups' outputs, and each column's sum and reference, on one scale 2^Eo: O / l is the output.  The largest
+    // group's, but at least 2^-27, where l 2^-Eo fits, and at most 2^63, where groups of 2^-63 keep their bits (the largest's
+    // sums, 2^49 at most, fit all the same).
+    int Eo = 0;
+#pragma unroll
+    for (int j = 0; j < C::GR; ++j) Eo = max(Eo, byte_of(E, j));
+    Eo = min(max(Eo, 100), 190);
+    if (E != Eo * kOnes<C>) {
+#pragma unroll
+      for (int i = 0; i < 2 * C::GR; ++i) {
+        const float to = pow2(byte_of(E, i / 2) - Eo);
+#pragma unroll
+        for (int nt = 0; nt < C::NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a.O[i][nt][e] *= to;
+      }
+    }
     float ref[C::NT][2];
-    const float to_o = __uint_as_float(E < 254 ? (uint32_t)(254 - E) << 23 : 0x00400000u);   // 2^(127 - E)
+    const float to_o = pow2(127 - Eo);
 #pragma unroll
     for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
@@ -757,7 +786,7 @@ __global__ void __launch_bounds__(C::W * 32, 1) kv4_attention_kernel(const __gri
         l += __shfl_xor_sync(0xffffffffu, l, 8);
         l += __shfl_xor_sync(0xffffffffu, l, 16);
         l *= to_o;
-        ref[nt][e] = (a.m[nt][e] == -INFINITY ? 0.f : a.m[nt][e]) + (float)(E - 141);
+        ref[nt][e] = (a.m[nt][e] == -INFINITY ? 0.f : a.m[nt][e]) + (float)(Eo - 141);
       }
 
     // ---- the piece's result

@@ -18,8 +18,8 @@
 // in fp16 then, but for channels 2^28 below the largest).  A tile's keys are held relative
 // to its largest key scale 2^EK, as code 2^(e - EK + 8), exact for groups down to
 // 2^-21 of it and off by 2^-33 of it at most; S is multiplied back in fp32.  Values
-// likewise relative to the largest value scale so far, 2^EV; the output follows it
-// when it grows.  The reference m of a row follows its maximum only when that has
+// likewise relative to the largest value scale of their channel group so far, 2^EV (2^-95 at
+// least); the group's output follows it when it grows.  The reference m of a row follows its maximum only when that has
 // grown by more than 2^6 (few tiles do, and each costs a pass over O in TMEM), so
 // weights reach 2^15 and lose bits below 2^-23 of the largest.
 // Groups that are not finite: keys become NaN operands; for values, whose NaN would
@@ -53,6 +53,7 @@ struct L {
   static constexpr uint32_t oMeta = oFlags + 2 * kTok, oBar = oMeta + 2 * 16;
   static constexpr uint32_t kBars = 12, oTmem = oBar + kBars * 8, kBytes = oTmem + 8, kAlloc = kBytes + 1024;
   static_assert(kAlloc <= 232448 && oK % 1024 == 0 && oV % 1024 == 0 && oBar % 8 == 0, "layout");
+  static constexpr uint32_t kOnes = D == 128 ? 0x01010101u : 0x0101u, kLeastEV = 32 * kOnes;   // a byte per channel group
   static constexpr uint32_t cS = 0, cO = 256;                 // TMEM: S (and P over it) of block b at 128 b, O at 256 + 128 b
 };
 
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_extend_kernel(const __grid_co
 
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + M::oBar);
   uint64_t *kfull = bar, *vfull = bar + 2, *kvempty = bar + 4, *sfull = bar + 6, *drain = bar + 8, *ready = bar + 10;
-  int4* meta = reinterpret_cast<int4*>(sm + M::oMeta);   // per stage: EK, -, EV, whether values are not finite
+  int4* meta = reinterpret_cast<int4*>(sm + M::oMeta);   // per stage: EK, -, EV (a byte per group), whether values are not finite
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + M::oTmem);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_extend_kernel(const __grid_co
       vu = unit_ptr(8 * vb);
       if (nt > 0) load();
       vu = unit_ptr(kTok + 8 * vb);
-      int EV = 100;
+      uint32_t EV = M::kLeastEV;
       for (int i = 0; i < nt; ++i) {
         const int st = i & 1, tv = i * kTok + 8 * vb;
         // the tokens' scales, a byte per group, tokens behind the last: 0, whatever the cache holds there
@@ -266,27 +267,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_extend_kernel(const __grid_co
           hi = __vmaxu4(hi, vs[t]);
           lo = __vminu4(lo, vs[t]);
         }
-        uint32_t vm = 0, vl = 255u;
+        bool nan = false;
+        if (__any_sync(0xffffffffu, __vmaxu4(hi, EV) != EV)) {   // a warp holds all 16 blocks
 #pragma unroll
-        for (int j = 0; j < GR; ++j) {
-          vm = max(vm, (uint32_t)byte_at(hi, j));
-          vl = min(vl, (uint32_t)byte_at(lo, j));
+          for (int j = 0; j < GR; ++j) {
+            uint32_t vm = __reduce_max_sync(0xffffffffu, (uint32_t)byte_at(hi, j));
+            if (vm == 255u) {   // the largest of the others
+              nan = true;
+              vm = 0;
+#pragma unroll
+              for (int t = 0; t < 8; ++t) vm = max(vm, byte_at(vs[t], j) == 255 ? 0u : (uint32_t)byte_at(vs[t], j));
+              vm = __reduce_max_sync(0xffffffffu, vm);
+            }
+            EV = (EV & ~(0xffu << (8 * j))) | max((uint32_t)byte_at(EV, j), vm) << (8 * j);
+          }
         }
-        vm = __reduce_max_sync(0xffffffffu, vm);   // a warp holds all 16 blocks
-        vl = __reduce_min_sync(0xffffffffu, vl);
-        const bool nan = vm == 255u;
-        if (nan) {   // the largest of the others
-          vm = 0;
-#pragma unroll
-          for (int t = 0; t < 8; ++t)
-#pragma unroll
-            for (int j = 0; j < GR; ++j) vm = max(vm, byte_at(vs[t], j) == 255 ? 0u : (uint32_t)byte_at(vs[t], j));
-          vm = __reduce_max_sync(0xffffffffu, vm);
-        }
-        EV = max(EV, (int)vm);
         uint32_t sp[4][GR];   // scale pairs of tokens 2 m, 2 m + 1
-        if (!nan && (int)vl > EV - 23) {   // exponent fields by bytes: all between 1 and 23
-          const uint32_t base = (uint32_t)(EV - 23) * (GR == 4 ? 0x01010101u : 0x0101u);
+        const uint32_t low = EV - 22 * M::kOnes;
+        if (!nan && !__any_sync(0xffffffffu, __vminu4(lo, low) != low)) {   // exponent fields by bytes: all between 1 and 23
+          const uint32_t base = EV - 23 * M::kOnes;
 #pragma unroll
           for (int m = 0; m < 4; ++m)
 #pragma unroll
@@ -297,13 +296,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_extend_kernel(const __grid_co
           for (int m = 0; m < 4; ++m)
 #pragma unroll
             for (int j = 0; j < GR; ++j) {
-              const int a = byte_at(vs[2 * m], j), b = byte_at(vs[2 * m + 1], j);
-              sp[m][j] = (a == 0 || a == 255 ? 0u : pow2_h(a - EV + 23)) | (b == 0 || b == 255 ? 0u : pow2_h(b - EV + 23)) << 16;
+              const int a = byte_at(vs[2 * m], j), b = byte_at(vs[2 * m + 1], j), up = 23 - byte_at(EV, j);
+              sp[m][j] = (a == 0 || a == 255 ? 0u : pow2_h(a + up)) | (b == 0 || b == 255 ? 0u : pow2_h(b + up)) << 16;
             }
         }
         if (i >= 2) ok = wait_all(kvempty + st, ((i >> 1) - 1) & 1);
         if (!ok) break;
-        if (tid == 128) *reinterpret_cast<int2*>(&meta[st].z) = make_int2(EV, nan ? 1 : 0);
+        if (tid == 128) *reinterpret_cast<int2*>(&meta[st].z) = make_int2((int)EV, nan ? 1 : 0);
         if (nan && vg == 0) {   // which tokens have which groups
 #pragma unroll
           for (int t = 0; t < 8; ++t) {
@@ -379,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_extend_kernel(const __grid_co
     const int lim = live ? s.L - s.qn + rr / G : -1;
     const uint32_t cS = M::cS + 128 * b, cO = M::cO + 128 * b;
     float m = -INFINITY, l = 0.f;
-    int EV = 100;
+    uint32_t EV = M::kLeastEV;
     uint32_t nans = 0;
     const bool run = b == 0 || two;
     const int steps = run ? nt : 0;
@@ -443,25 +442,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_extend_kernel(const __grid_co
       }
       float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
       top *= cf;
-      // the reference and the output's scale; both only move up
+      // the reference and the output's scales; all only move up
       float f = 1.f;
       if (top > m + kLazy || m == -INFINITY) {
         if (m != -INFINITY) f = ex2(m - top);
         m = top;
       }
       l *= f;
-      if (mt.z != EV) {
-        if (i > 0) f *= __uint_as_float((uint32_t)max(127 + EV - mt.z, 0) << 23);
-        EV = mt.z;
-      }
-      if (__any_sync(0xffffffffu, f != 1.f) && i > 0) {   // the products into O so far have completed (before S was committed)
+      const uint32_t was = EV;
+      EV = (uint32_t)mt.z;
+      if (i > 0 && __any_sync(0xffffffffu, f != 1.f || EV != was)) {   // the products into O so far have completed (before S was committed)
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
           float v[16];
           uint32_t w[16];
+          const float fo = f * __uint_as_float((uint32_t)max(127 + byte_at(was, c >> 1) - byte_at(EV, c >> 1), 0) << 23);
           tc::tmem_ld16(tc::tmem_addr(tmem, tl, cO + 16 * c), v);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(v[e] * f);
+          for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(v[e] * fo);
           tc::tmem_st16(tc::tmem_addr(tmem, tl, cO + 16 * c), w);
         }
       }
@@ -529,13 +527,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_extend_kernel(const __grid_co
       }
       if (ok) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const float back = __uint_as_float((uint32_t)(EV - 8) << 23);   // 2^(EV - 135)
         __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + orow * D;
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
           float v[16];
           if (nt > 0) tc::tmem_ld16(tc::tmem_addr(tmem, tl, cO + 16 * c), v);
           uint32_t w[8];
+          const float back = __uint_as_float((uint32_t)(byte_at(EV, c >> 1) - 8) << 23);   // 2^(EV - 135)
           const bool none = nt == 0 || l == 0.f, gone = (nans >> (c >> 1) & 1u) != 0;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {

@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import kv4_testutil as ref
 import linear_attention_recurrence_chunk_gb300 as kda
 from test_kv4_attention_gpu import Setup, kernel, run_check  # noqa: F401  (a fixture)
 
@@ -115,3 +116,32 @@ def test_not_finite_values_of_tokens_whose_weight_is_far_below_the_largest(dt, s
             v[tok, head, ch] = np.inf if tok % 2 else np.nan
     run_check(dt, 128, 8, 2, 16, [400, 30], [6, 1], edit=edit, spread=spread)
     run_check(dt, 64, 4, 4, 32, [400], [3], edit=lambda k, v, rng: edit(k, np.concatenate([v, v], -1), rng), spread=spread)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("exps,grow", [((0, -15, -30, -45), 0), ((-60, 10, -20, 40), 0), ((-90, -40, 0, -65), 30), ((0, -30, 0, -30), -9)])
+def test_channel_groups_of_far_apart_sizes(dt, exps, grow, kernel):
+    """Each group of 32 channels has the precision of its own values, however large another group's are (grow: by
+    2^grow every 60 tokens)."""
+    def edit(k, v, rng):
+        v *= np.ldexp(1.0, np.array(exps).repeat(32))
+        v *= np.ldexp(1.0, grow * (np.arange(v.shape[0]) // 60))[:, None, None]
+    s = Setup(dt, 128, 8, 2, 16, [300, 45], [3, 1], edit=edit)
+    o, lse = s.run()
+    s.check(o, lse)
+    q, got, step = s.q.double().cpu().numpy(), o.double().cpu().numpy(), torch.finfo(dt).eps / 2
+    a = b = 0
+    for L, n in zip(s.lens, s.qn):
+        k, v, x = s.k[a:a + L], s.v[a:a + L], q[b:b + n]
+        want, _ = ref.attention(x, k, v, s.scale)
+        for j in range(4):
+            if np.isnan(want[..., 32 * j:32 * j + 32]).all():   # values that grew beyond the type; check() has seen them
+                continue
+            own = np.zeros_like(v)   # the bound counts the largest value of the group alone
+            own[..., 32 * j:32 * j + 32] = v[..., 32 * j:32 * j + 32]
+            unit = 2.0 ** np.floor(np.log2(np.abs(own).max()))
+            to, _ = ref.attention_bound(x, k, own / unit, s.scale, n, 1 if dt is BF else 2)
+            c = slice(32 * j, 32 * j + 32)
+            tol = to[..., c] * unit + step * np.abs(want[..., c]) + 2.0 ** -133
+            assert (np.abs(got[b:b + n][..., c] - want[..., c]) <= tol).all(), j
+        a, b = a + L, b + n
