@@ -91,8 +91,9 @@ KDA_API kda_status kda_kv4_append(const void* k, const void* v, const int32_t* s
 
 /*
  * Reads tokens back: k, v [T][Hkv][D] dtype dt, dense, get the values that the cache holds at
- * the slots (exact in either type); zeros for a negative slot, and for one beyond the cache,
- * which is reported.  k, v 16-byte aligned.
+ * the slots; zeros for a negative slot, and for one beyond the cache, which is reported.  They
+ * are exact in either type, but for 4 * 2^126 = 2^128, to which |x| from 3.5 * 2^126 on is rounded
+ * and which reads back as inf.  k, v 16-byte aligned.
  */
 KDA_API kda_status kda_kv4_gather(const void* cache, int64_t num_pages, int32_t page_size, const int32_t* slot_map,
                                   int64_t T, int32_t Hkv, int32_t D, kda_dtype dt, void* k, void* v,

@@ -53,3 +53,18 @@ def test_page_map_without_room_many_requests():
         x0 += new[i]
     assert np.array_equal(t.cpu().numpy(), want)
     assert kda.kda_device_error()[0] == 1
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_the_largest_values_read_back_as_infinite(dt):
+    """From 3.5 * 2^126 on a value rounds to 4 * 2^126 = 2^128, which neither type holds; below, to finite ones."""
+    x = torch.zeros((4, 1, 64), dtype=torch.float32, device=DEV)
+    x[0, 0, 3], x[1, 0, 3], x[2, 0, 3], x[3, 0, 3] = 3.5 * 2.0 ** 126, -torch.finfo(torch.bfloat16).max, 3.484375 * 2.0 ** 126, 2.0 ** 127
+    x = x.to(dt)
+    cache = kda.kda_kv4_cache(1, 1, 16, 64)
+    slots = i32(range(4))
+    kda.kda_kv4_append(x, x, slots, cache)
+    for got in kda.kda_kv4_gather(cache, slots, dt):
+        got = got[:, 0, 3].double().tolist()
+        assert got == [float("inf"), -float("inf"), 3.0 * 2.0 ** 126, 2.0 ** 127]
+    assert kda.kda_device_error() == (0, 0)
