@@ -149,7 +149,7 @@ __device__ __forceinline__ Work work_of(const AttnProblem& p, int n, bool* bad) 
   Work s;
   static_cast<Seq&>(s) = seq_of(p, n, bad);
   s.tiles = s.L > 0 ? (s.L - 1) / C::TILE + 1 : 1;   // no token: one empty tile writes the zeros
-  s.rts = (s.qn * (p.Hq / p.Hkv) + C::R - 1) / C::R;
+  s.rts = row_blocks(s.qn, p.Hq / p.Hkv, C::R);
   return s;
 }
 

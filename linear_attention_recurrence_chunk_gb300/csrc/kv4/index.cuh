@@ -30,5 +30,8 @@ KDA_INDEX_FN int32_t units_of_tile(int32_t L, int32_t i, int32_t most) {
   return n < most ? n : most;
 }
 
+// Blocks of R query rows that qn query tokens of G heads fill; qn G is at most 2^31 - 1.
+KDA_INDEX_FN int32_t row_blocks(int32_t qn, int32_t G, int32_t R) { return (int32_t)(((uint32_t)(qn * G) + R - 1) / R); }
+
 }  // namespace kv4
 }  // namespace kda

@@ -26,6 +26,7 @@ int64_t first_wrong_page(uint32_t upp, int64_t n) {
   return -1;
 }
 int64_t token(int64_t i, int32_t tokens, int32_t at) { return token_of_tile(i, tokens, at); }
+int32_t blocks(int32_t qn, int32_t G, int32_t R) { return row_blocks(qn, G, R); }
 int32_t units(int32_t L, int32_t i, int32_t most) { return units_of_tile(L, i, most); }
 }
 """
@@ -41,6 +42,7 @@ def lib(tmp_path_factory):
     lib.first_wrong_page.argtypes, lib.first_wrong_page.restype = [ctypes.c_uint32, ctypes.c_int64], ctypes.c_int64
     lib.token.argtypes, lib.token.restype = [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32], ctypes.c_int64
     lib.units.argtypes, lib.units.restype = [ctypes.c_int32] * 3, ctypes.c_int32
+    lib.blocks.argtypes, lib.blocks.restype = [ctypes.c_int32] * 3, ctypes.c_int32
     return lib
 
 
@@ -76,3 +78,9 @@ def test_units_of_a_tile(lib, L):
     for i in range(max(tiles - 3, 0), tiles):
         assert lib.units(L, i, 4) == min(4, -(-L // 16) - 4 * i)
     assert L == 0 or 1 <= lib.units(L, tiles - 1, 4) <= 4
+
+
+@pytest.mark.parametrize("qn,G", [(0, 1), (0, 128), (1, 1), (8, 1), (3, 12), (2048, 4), (MOST, 1), (MOST - 7, 1), (MOST // 12, 12), (MOST // 128, 128)])
+def test_row_blocks(lib, qn, G):
+    for R in (8, 16):
+        assert lib.blocks(qn, G, R) == -(-qn * G // R)
