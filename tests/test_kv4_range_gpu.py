@@ -145,3 +145,14 @@ def test_channel_groups_of_far_apart_sizes(dt, exps, grow, kernel):
             tol = to[..., c] * unit + step * np.abs(want[..., c]) + 2.0 ** -133
             assert (np.abs(got[b:b + n][..., c] - want[..., c]) <= tol).all(), j
         a, b = a + L, b + n
+
+
+@pytest.mark.parametrize("dt,Hq,Hkv,ps,lens,qn", [(BF, 8, 1, 64, [131072], [1]), (F32, 2, 1, 16, [60000], [1]),
+                                                  (BF, 4, 2, 32, [30001, 17], [5, 2]), (F32, 3, 1, 64, [20000], [7])])
+def test_long_sequences(dt, Hq, Hkv, ps, lens, qn):
+    run_check(dt, 128, Hq, Hkv, ps, lens, qn, spread=2.0)
+
+
+def test_long_sequences_of_chunks(kernel):
+    run_check(BF, 128, 2, 1, 16, [20011], [35], spread=2.0)
+    run_check(BF, 64, 1, 1, 64, [30000, 200], [33, 129])
