@@ -41,10 +41,11 @@
 // the sequences, which every CTA takes itself.  Each warp feeds itself through a ring
 // of tiles filled by bulk copies.
 //
-// Measured: one token of 48 sequences up to 32,000, 64 query on 8 key heads of 128: 111 us
-// with the join, 563 MB at 5.1 TB/s.  Counters: issue 56 % and ALU pipe 55 % of active
-// cycles, DRAM 66 %, 262 warp instructions for 16 tokens of a head.  16 warps of 32-token
-// tiles took 136 us, 8 warps with three stages 119.
+// Measured: one token of 48 sequences up to 32,000, 64 query on 8 key heads of 128: 107 us
+// with the join, 563 MB at 5.2 TB/s (fp32: 150 us for 497 K tokens).  Counters: issue 57 %
+// and ALU pipe 56 % of active cycles, DRAM 68 %, 260 warp instructions for 16 tokens of a
+// head.  Before later steps, which took 111 to 107 us, 16 warps of 32-token tiles took 136 us
+// and 8 warps with three stages 119.
 #include <algorithm>
 #include <cstdlib>
 
@@ -115,8 +116,10 @@ struct Cfg {
   static constexpr int STAGES = 2;
   static constexpr bool QREG = NT <= 2 && PARTS == 1;   // q operands in registers
   static constexpr int W = NT == 1 && PARTS == 1 ? 12 : 8;   // warps of a CTA
-  // room of a segment's beginning and end on the line, in tiles (256 sequences up to 2,048 tokens, 96 query on
-  // 8 key heads: 107 us with 1, 98 with 2, 94 with 3, 98 with 4)
+  // room of a segment's beginning and end on the line, in tiles.  With 1, 2, 3, 4 (us): 256 sequences up to 2,048 tokens,
+  // 96 query on 8 key heads 108.6, 97.3, 91.7, 95.5; 48 up to 32,000, 64 on 8, 108.4, 108.2, 107.4, 108.8; 32 up to 8,191 with
+  // 5 tokens, 32 on 8, 67.9, 65.9, 67.2, 67.9; 256 up to 500, 8 on 8, 26.3, 26.5, 27.9, 29.8; 128 up to 1,000 with heads of
+  // 64, 16 on 4, 15.0, 15.8, 16.2, 16.4; 40 fp32 up to 3,000, 32 on 8, 24.4, 25.9, 25.5, 26.3.
   static constexpr int HEAD = 3;
   static constexpr int GR = D / 32, KS = D / 16;
   static constexpr int kStage = MT * Unit<D>::kBytes, kRing = STAGES * kStage;
@@ -979,14 +982,20 @@ auto with_cfg(int32_t Hq, int32_t Hkv, int32_t D, int32_t max_q, kda_dtype dt, F
   return one ? f(Cfg<64, 1, 1>{}, z) : f(Cfg<64, 2, 1>{}, z);
 }
 
-// Whether the tiled kernel takes the call (bf16).  Both kernels' times grow with the cached
-// tokens, so the rule needs no lengths.  Per 1,024 cached tokens the cut line takes about
+// Whether the tiled kernel takes the call (bf16).  The host does not know the lengths, so the
+// rule takes the sequences to be alike in cached and in query tokens: both kernels' times then
+// grow with the cached tokens alike.  Per 1,024 cached tokens the cut line takes about
 // 0.074 us for each 32 rows of a key/value head, on the whole GPU; the tiled kernel 18 us
 // a wave of 152 CTAs of up to 128 rows, 22 us of up to 256.  Measured over 16,384 cached tokens
 // (line / tiled, us): 8 sequences of 8 heads with 64 rows 171 / 285, 128 rows 319 / 288,
 // 512 rows 1,216 / 360; one sequence of 8 heads with 256 rows 99 / 346; 8 of 2 heads with
 // 512 rows 316 / 353, 1,024 rows 616 / 354.  Up to 24 rows the line is far ahead (16 rows:
-// 66 / 279).  KDA_KV4_TILED=0 or =1 forces a kernel for bf16 calls.
+// 66 / 279).  Where the sequences are not alike it may choose the slower one, and either kernel
+// may be slower than two calls (32 query on 8 key heads, line / tiled): 2,048 tokens over 4,096 beside
+// 31 single ones over up to 32,000 729 / 709, chosen tiled, and apart 152 (tiled) + 76 (line); beside
+// 255 single ones 1,425 / 3,471, chosen line, and apart 152 + 488; 64 sequences of 16 tokens of
+// 64 on 8 heads, one over 131,072 and the others over 2,048, 639 / 2,175, chosen tiled (all over 4,064:
+// 634 / 320).  KDA_KV4_TILED=0 or =1 forces a kernel for bf16 calls.
 bool extend_rows(const AttnProblem& p) {
   const int64_t G = p.Hq / p.Hkv, rows = (int64_t)p.max_q * G;
   if (p.dt != KDA_BF16 || (rows + 255) / 256 * p.N * p.Hkv > INT32_MAX) return false;

@@ -13,8 +13,9 @@
 // codes pass through shared memory, so that the lanes of eight tokens write the eight
 // bytes that a unit keeps of each token next to one another.  Each token's place comes
 // from its own slot; consecutive slots make whole lines of these stores.
-// Measured for 65,536 tokens, 8 heads of 128, bf16 (340 MB each way, times between events
-// around the launch): write 71.6 us, 4.7 TB/s; read-back 51.2 us, 6.6 TB/s.
+// Measured for 65,536 tokens, 8 heads of 128 (replayed from a graph): bf16, 340 MB each way,
+// write 67.9 us, 5.0 TB/s, read-back 52.3 us, 6.5 TB/s; fp32, 608 MB, write 98.2 us, 6.2 TB/s,
+// read-back 93.7 us, 6.5 TB/s.  What keeps the bf16 write below the others has not been profiled.
 #include "internal.cuh"
 
 namespace kda {

@@ -27,11 +27,11 @@
 // that it sees, and its output becomes NaN there.
 //
 // Measured: 3 sequences, 3,394 tokens over 16,860 cached, 32 query on 8 key heads of 128,
-// 402 us, 38 % of the bf16 matrix rate for the causal work.  Counters: tensor pipe 34 % of
-// active cycles, ALU 37 %, issue 46 %, no unit full; the longest stall is the wait for
-// memory and TMEM loads.  With one part left out (results wrong, for timing only): the
-// weights' arithmetic 288 us, most of the products 327, the conversions 360.  Slower or
-// equal: scores in two buffers of 64 tokens 452, blocks in strict turns 452, two threads
+// 398 us, 37 % of the bf16 matrix rate for the causal work.  Counters: tensor pipe 35 % of
+// active cycles, ALU 39 %, issue 47 %, no unit full; the longest stall is the wait for
+// memory and TMEM loads.  Against 402 us, with one part left out (results wrong, for timing
+// only): the weights' arithmetic 288 us, most of the products 327, the conversions 360.
+// Slower or equal: scores in two buffers of 64 tokens 452, blocks in strict turns 452, two threads
 // per row on 24 warps 442, one pass with maxima by chunks 443, a row's scores kept in
 // registers 402 to 406.
 #include "attn_common.cuh"
