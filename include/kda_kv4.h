@@ -133,7 +133,7 @@ KDA_API size_t kda_kv4_attention_workspace_size(int64_t T, int32_t N, int32_t Hq
  * keys relative to the largest scale of 128 tokens, values to that of their 32 channels so far:
  * exact for groups down to 2^-21 of it.
  * One kernel runs the whole call, chosen by the numbers of tokens, heads and sequences; a step with
- * long chunks beside many single tokens is faster as a call for each kind.
+ * long chunks beside many single tokens may be faster as a call for each kind.
  * A length beyond the table, a page beyond the cache, a cu_seqlens that decreases, does not
  * begin at 0 or passes T, and a sequence of more than max_q_len tokens are reported; the
  * outputs of such a sequence are unspecified, no access leaves the arrays.
