@@ -33,6 +33,9 @@ Functions keep the C names:
 * from ``kv4.py``, the paged 4-bit key/value cache of the attention layers beside
   the recurrent ones: ``kda_page_map``, ``kda_kv4_cache``, ``kda_kv4_append``,
   ``kda_kv4_gather``, ``kda_kv4_attention``, ``kda_kv4_attention_workspace_size``.
+* from ``dense.py``, the dense half of a decoder layer: ``kda_add_rmsnorm``,
+  ``kda_add_rmsnorm_fp8``, ``kda_fp8_quant``, ``kda_fp8_values``, ``kda_fp8_matmul``,
+  ``kda_rotary``, ``kda_rotary_freqs``.
 """
 from __future__ import annotations
 
@@ -48,7 +51,8 @@ __all__ = ["kda_chunk_fwd", "kda_chunk_fwd_snapshots", "kda_chunk_fwd_gated", "k
            "DECAY_BOUNDED", "DECAY_SOFTPLUS", "kda_decode_step", "kda_decode_layer_step", "kda_chunk_fwd_workspace_size", "kda_device_error",
            "kda_check_wait_timeout", "KdaError", "library_path", "load_library", "STATUS",
            "kda_page_map", "kda_kv4_cache", "kda_kv4_append", "kda_kv4_gather", "kda_kv4_attention",
-           "kda_kv4_attention_workspace_size"]
+           "kda_kv4_attention_workspace_size", "kda_add_rmsnorm", "kda_add_rmsnorm_fp8", "kda_fp8_quant", "kda_fp8_values",
+           "kda_fp8_matmul", "kda_rotary", "kda_rotary_freqs"]
 
 DECAY_BOUNDED, DECAY_SOFTPLUS = 0, 1   # kda_decay_map
 STATUS = {0: "KDA_OK", 1: "KDA_ERR_INVALID_ARG", 2: "KDA_ERR_UNSUPPORTED", 3: "KDA_ERR_CUDA",
@@ -323,3 +327,5 @@ def kda_check_wait_timeout(limit_cycles: int, stream=None) -> None:
 
 from .kv4 import (kda_kv4_append, kda_kv4_attention, kda_kv4_attention_workspace_size, kda_kv4_cache,  # noqa: E402
                   kda_kv4_gather, kda_page_map)
+from .dense import (kda_add_rmsnorm, kda_add_rmsnorm_fp8, kda_fp8_matmul, kda_fp8_quant, kda_fp8_values,  # noqa: E402
+                    kda_rotary, kda_rotary_freqs)

@@ -1,0 +1,168 @@
+// C ABI of the dense half of a decoder layer: argument validation and dispatch.
+#include <limits.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "internal.cuh"
+
+namespace {
+
+using kda::dense::kBlock;
+
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+struct Range {
+  const void* p;
+  size_t n;
+};
+bool overlaps(const Range& a, const Range& b) {
+  if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y + b.n && y < x + a.n;
+}
+
+// Every output apart from every input and from the other outputs.
+template <size_t NI, size_t NO>
+bool apart(const Range (&in)[NI], const Range (&out)[NO]) {
+  for (size_t i = 0; i < NO; ++i) {
+    for (const Range& r : in)
+      if (overlaps(out[i], r)) return false;
+    for (size_t j = i + 1; j < NO; ++j)
+      if (overlaps(out[i], out[j])) return false;
+  }
+  return true;
+}
+
+size_t elem(kda_dtype dt) { return dt == KDA_F32 ? 4 : 2; }
+bool dtype_ok(kda_dtype dt) { return dt == KDA_F32 || dt == KDA_BF16; }
+int64_t blocks_of(int64_t n) { return (n + kBlock - 1) / kBlock; }
+
+constexpr int64_t kMost = (int64_t)INT32_MAX - 511;   // rows or columns
+constexpr int64_t kMostStride = (int64_t)1 << 40;     // elements
+
+// Rows of a strided [rows][C] matrix (rows, C at least 1), its bytes from first to last.
+Range span(const void* p, int64_t rows, int64_t C, int64_t stride, size_t eb) {
+  return {p, (size_t)((rows - 1) * stride + C) * eb};
+}
+bool shape_ok(int64_t rows, int64_t C) {
+  return rows >= 0 && C >= 0 && rows <= kMost && C <= kMost && (rows == 0 || C <= ((int64_t)1 << 42) / rows);
+}
+bool stride_ok(int64_t stride, int64_t C) { return stride >= C && stride <= kMostStride; }
+
+kda_status done(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
+
+}  // namespace
+
+extern "C" {
+
+kda_status kda_fp8_quant(const void* x, int64_t x_stride, int64_t T, int64_t C, int32_t block_rows, kda_dtype dt, uint8_t* codes,
+                         uint8_t* scales, cudaStream_t stream) {
+  if (!dtype_ok(dt) || !shape_ok(T, C) || (block_rows != 1 && block_rows != kBlock)) return KDA_ERR_INVALID_ARG;
+  if (T == 0 || C == 0) return KDA_OK;
+  if (T == 1) x_stride = C;   // a stride over one row has no meaning
+  if (!x || !codes || !scales || !aligned(x, elem(dt)) || !stride_ok(x_stride, C)) return KDA_ERR_INVALID_ARG;
+  const int64_t srows = block_rows == 1 ? T : blocks_of(T);
+  const Range in[] = {span(x, T, C, x_stride, elem(dt))};
+  const Range out[] = {{codes, (size_t)(T * C)}, {scales, (size_t)(srows * blocks_of(C))}};
+  if (!apart(in, out)) return KDA_ERR_INVALID_ARG;
+  return done(kda::dense::launch_quant({x, x_stride, T, C, block_rows, dt, codes, scales}, stream));
+}
+
+kda_status kda_fp8_values(const uint8_t* codes, const uint8_t* scales, int64_t T, int64_t C, int32_t block_rows, kda_dtype dt, void* y,
+                          cudaStream_t stream) {
+  if (!dtype_ok(dt) || !shape_ok(T, C) || (block_rows != 1 && block_rows != kBlock)) return KDA_ERR_INVALID_ARG;
+  if (T == 0 || C == 0) return KDA_OK;
+  if (!codes || !scales || !y || !aligned(y, elem(dt))) return KDA_ERR_INVALID_ARG;
+  const int64_t srows = block_rows == 1 ? T : blocks_of(T);
+  const Range in[] = {{codes, (size_t)(T * C)}, {scales, (size_t)(srows * blocks_of(C))}};
+  const Range out[] = {{y, (size_t)(T * C) * elem(dt)}};
+  if (!apart(in, out)) return KDA_ERR_INVALID_ARG;
+  return done(kda::dense::launch_values({codes, scales, T, C, block_rows, dt, y}, stream));
+}
+
+kda_status kda_add_rmsnorm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride, const float* weight, float eps,
+                           int64_t T, int64_t C, kda_dtype dt, void* h, void* y, uint8_t* codes, uint8_t* scales, cudaStream_t stream) {
+  if (!dtype_ok(dt) || !shape_ok(T, C) || !(eps >= 0.f) || isinf(eps)) return KDA_ERR_INVALID_ARG;
+  if (C > kda::dense::kNormMost) return KDA_ERR_UNSUPPORTED;
+  if (T == 0 || C == 0) return KDA_OK;
+  if (T == 1) x_stride = residual_stride = C;
+  const size_t eb = elem(dt);
+  if (!x || !aligned(x, eb) || !stride_ok(x_stride, C) || !aligned(weight, 4)) return KDA_ERR_INVALID_ARG;
+  if (residual && (!aligned(residual, eb) || !stride_ok(residual_stride, C))) return KDA_ERR_INVALID_ARG;
+  if ((residual != nullptr) != (h != nullptr) || !aligned(h, eb)) return KDA_ERR_INVALID_ARG;
+  if ((y != nullptr) == (codes != nullptr) || (codes != nullptr) != (scales != nullptr) || !aligned(y, eb)) return KDA_ERR_INVALID_ARG;
+  const size_t n = (size_t)(T * C);
+  const Range rx = span(x, T, C, x_stride, eb), rr = span(residual, T, C, residual_stride, eb), rw = {weight, (size_t)C * 4};
+  const Range rh = {h, n * eb}, ry = {y, n * eb}, rc = {codes, n}, rs = {scales, (size_t)(T * blocks_of(C))};
+  // h over x or the residual, y over x, row for row; else apart
+  const bool x_dense = x_stride == C, r_dense = residual_stride == C;
+  if (overlaps(rh, rx) && !(h == x && x_dense)) return KDA_ERR_INVALID_ARG;
+  if (residual && overlaps(rh, rr) && !(h == residual && r_dense)) return KDA_ERR_INVALID_ARG;
+  if (overlaps(ry, rx) && !(y == x && x_dense)) return KDA_ERR_INVALID_ARG;
+  if (overlaps(rh, ry) || (residual && overlaps(ry, rr)) || overlaps(rh, rw) || overlaps(ry, rw)) return KDA_ERR_INVALID_ARG;
+  const Range in[] = {rx, residual ? rr : Range{nullptr, 0}, rw, rh};
+  const Range out[] = {rc, rs};
+  if (!apart(in, out)) return KDA_ERR_INVALID_ARG;
+  return done(kda::dense::launch_norm({x, x_stride, residual, residual_stride, weight, eps, T, C, dt, h, y, codes, scales}, stream));
+}
+
+kda_status kda_fp8_matmul(const uint8_t* a, int64_t a_stride, const uint8_t* a_scales, const uint8_t* w, int64_t w_stride,
+                          const uint8_t* w_scales, int64_t M, int64_t N, int64_t K, kda_dtype dt, void* out, int64_t out_stride,
+                          cudaStream_t stream) {
+  if (!dtype_ok(dt) || M < 0 || N < 0 || K < 1) return KDA_ERR_INVALID_ARG;
+  if (K % 16 != 0 || M > kMost || N > kMost || K > kMost) return KDA_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return KDA_OK;
+  const auto up16 = [](int64_t v) { return (v + 15) / 16 * 16; };
+  if (M == 1) a_stride = K, out_stride = N;   // a stride over one row has no meaning
+  if (N == 1) w_stride = up16(K);
+  if (!a || !w || !a_scales || !w_scales || !out) return KDA_ERR_INVALID_ARG;
+  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(out, elem(dt)) || a_stride % 16 != 0 || w_stride % 16 != 0) return KDA_ERR_INVALID_ARG;
+  if (!stride_ok(a_stride, K) || !stride_ok(w_stride, K) || !stride_ok(out_stride, N)) return KDA_ERR_INVALID_ARG;
+  const Range in[] = {span(a, M, K, a_stride, 1), span(w, N, K, w_stride, 1), {a_scales, (size_t)(M * blocks_of(K))},
+                      {w_scales, (size_t)(blocks_of(N) * blocks_of(K))}};
+  const Range res[] = {span(out, M, N, out_stride, elem(dt))};
+  if (!apart(in, res)) return KDA_ERR_INVALID_ARG;
+  kda::dense::MatmulProblem p{a, a_scales, w, w_scales, a_stride, w_stride, M, N, K, dt, out, out_stride, nullptr};
+  if (kda::device_error_ptr(&p.dev_err) != cudaSuccess) return KDA_ERR_CUDA;
+  return done(kda::dense::launch_matmul(p, stream));
+}
+
+kda_status kda_rotary(const void* q, int64_t q_token_stride, int64_t q_head_stride, int32_t Hq, const void* k, int64_t k_token_stride,
+                      int64_t k_head_stride, int32_t Hk, const int32_t* positions, int64_t T, int32_t D, int32_t rot, const double* freqs,
+                      float amplitude, int32_t flags, kda_dtype dt, void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                      void* k_out, int64_t k_out_token_stride, int64_t k_out_head_stride, cudaStream_t stream) {
+  if (!dtype_ok(dt) || T < 0 || T > kMost || Hq < 0 || Hk < 0 || D < 1 || rot < 0 || rot > D || rot % 2 != 0 || !isfinite(amplitude) ||
+      (flags & ~(KDA_ROTARY_INTERLEAVED | KDA_ROTARY_INVERSE)) != 0)
+    return KDA_ERR_INVALID_ARG;
+  if (D > 1024 || Hq > 1024 || Hk > 1024 || Hq + Hk > 1024) return KDA_ERR_UNSUPPORTED;
+  if (T == 0 || Hq + Hk == 0) return KDA_OK;
+  if (!positions || !aligned(positions, 4) || (rot > 0 && (!freqs || !aligned(freqs, 8)))) return KDA_ERR_INVALID_ARG;
+  const size_t eb = elem(dt);
+  kda::dense::RotaryPart part[2] = {{q, q_out, q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride, Hq},
+                                    {k, k_out, k_token_stride, k_head_stride, k_out_token_stride, k_out_head_stride, Hk}};
+  Range in[4] = {{nullptr, 0}, {nullptr, 0}, {positions, (size_t)T * 4}, {freqs, (size_t)rot / 2 * 8}}, out[2] = {{nullptr, 0}, {nullptr, 0}};
+  bool place[2] = {false, false};
+  for (int i = 0; i < 2; ++i) {
+    kda::dense::RotaryPart& p = part[i];
+    if (p.H == 0) continue;
+    if (T == 1) p.xt = p.yt = 0;
+    if (p.H == 1) p.xh = p.yh = 0;
+    if (!p.x || !p.y || !aligned(p.x, eb) || !aligned(p.y, eb)) return KDA_ERR_INVALID_ARG;
+    const int64_t st[] = {p.xt, p.xh, p.yt, p.yh};
+    for (int64_t s : st)
+      if (s < 0 || s > kMostStride) return KDA_ERR_INVALID_ARG;
+    // the heads of a token, and the tokens of an output, do not lie over one another
+    if ((p.H > 1 && p.yh < D) || (T > 1 && p.yt < D)) return KDA_ERR_INVALID_ARG;
+    in[i] = {p.x, (size_t)((T - 1) * p.xt + (p.H - 1) * p.xh + D) * eb};
+    out[i] = {p.y, (size_t)((T - 1) * p.yt + (p.H - 1) * p.yh + D) * eb};
+    place[i] = p.x == p.y && p.xt == p.yt && p.xh == p.yh;
+  }
+  for (int i = 0; i < 2; ++i) {
+    if (overlaps(out[i], in[2]) || overlaps(out[i], in[3])) return KDA_ERR_INVALID_ARG;
+    // In place, the other part may lie between the heads or tokens of this one (parts of one projection).
+    if (!place[i] && (overlaps(out[i], in[0]) || overlaps(out[i], in[1]) || overlaps(out[i], out[1 - i]))) return KDA_ERR_INVALID_ARG;
+  }
+  return done(kda::dense::launch_rotary({part[0], part[1], positions, freqs, T, D, rot, amplitude, flags, dt}, stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,242 @@
+// The product of 8-bit matrices for few rows of A (decode steps).
+//
+//   out[m][n] = sum_k A[m][k] W[n][k]
+//
+// Bound: the weights' bytes from HBM.  So the weights are the 128-row operand of the tensor core and
+// the tokens (kRows of them, 16 to 256) its columns: no row of the instruction is padding however
+// few tokens there are.  A cluster of CTAs splits K of one tile, so that few tiles still
+// fill the chip; its partial sums meet in distributed shared memory in a fixed order, with no scratch memory
+// and one launch.
+#include <algorithm>
+
+#include "internal.cuh"
+#include "mma8.cuh"
+
+namespace kda {
+namespace dense {
+namespace {
+
+constexpr int kThreads = 128;   // warp 0 loads tiles, 1 issues products, 2 loads scales; all store
+
+template <int kRows>
+struct Few {
+  static constexpr int kStages = kRows <= 32 ? 5 : kRows == 64 ? 4 : kRows == 128 ? 3 : 4;
+  static constexpr uint32_t kW = 128 * kStageK, kX = kRows * kStageK, kStage = kW + kX;
+  static constexpr int kSets = (kRows + 127) / 128;               // of 128 tokens' scales
+  static constexpr uint32_t kScales = 512 * (1 + kSets);          // one slot: weights', tokens'
+  static constexpr uint32_t oScales = kStages * kStage, oBars = oScales + 2 * kScales;
+  static constexpr int kBars = 2 * kStages + 5;
+  static constexpr uint32_t kBytes = oBars + kBars * 8 + 8, kAlloc = kBytes + 1024;   // + alignment
+  static constexpr uint32_t cScales = kRows, kCols = kRows + 2 * 4 * (1 + kSets);      // TMEM columns
+  static constexpr uint32_t kTmem = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+  static_assert(kStages * kStage >= kRows * 512, "partial sums take the stages' place");
+};
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+  return x;
+}
+
+template <int kRows, typename T>
+__global__ void __launch_bounds__(kThreads)
+    fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapX, const uint8_t* __restrict__ sw,
+                          const uint8_t* __restrict__ sx, int64_t M, int64_t N, int32_t blocks, T* out, int64_t ldo, int32_t split,
+                          int32_t* dev_err) {
+  using F = Few<kRows>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* sm = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + F::oBars);
+  uint64_t *empty = full + F::kStages, *sfull = empty + F::kStages, *sempty = sfull + 2, *done = sempty + 2;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(done + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t tile = blockIdx.x / split, rank = blockIdx.x - tile * split;
+  const int64_t n0 = (int64_t)tile * 128, m0 = (int64_t)blockIdx.y * kRows;
+  const int32_t kb0 = (int32_t)((int64_t)blocks * rank / split), nb = (int32_t)((int64_t)blocks * (rank + 1) / split) - kb0;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int i = 0; i < F::kBars; ++i) tc::mbar_init(full + i, 1);
+      tc::fence_mbar_init();
+    }
+  } else if (warp == 1) {
+    tc::tmem_alloc(tmem_at, F::kTmem);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_at;
+  bool ok = true;
+
+  if (warp == 0) {
+    int issued = 0;
+    if (lane == 0) {
+      for (int i = 0; i < nb && ok; ++i, ++issued) {
+        const int st = i % F::kStages;
+        if (i >= F::kStages) ok = tc::mbar_wait(empty + st, (i / F::kStages - 1) & 1, kWaitLimit);
+        if (!ok) break;
+        uint8_t* w = sm + st * F::kStage;
+        tc::mbar_arrive_expect_tx(full + st, F::kStage);
+        tc::tma_load_2d(w, &mapW, (kb0 + i) * kStageK, (int32_t)n0, full + st);
+        tc::tma_load_2d(w + F::kW, &mapX, (kb0 + i) * kStageK, (int32_t)m0, full + st);
+      }
+    }
+    if (lane == 0 && !ok) {   // end with no copy in flight
+      for (int st = 0; st < F::kStages; ++st) tc::mbar_wait(full + st, issued > st ? ((issued - 1 - st) / F::kStages) & 1 : 1, kWaitLimit);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    const uint64_t dW = tc::desc_kmajor_sw128(tc::smem_u32(sm)), dX = tc::desc_kmajor_sw128(tc::smem_u32(sm + F::kW));
+    const uint64_t dS = desc_scales(tc::smem_u32(sm + F::oScales));
+    for (int i = 0; i < nb && ok; ++i) {
+      const int st = i % F::kStages, g = i >> 2, slot = g & 1;
+      const uint32_t cw = tmem + F::cScales + slot * 4 * (1 + F::kSets), cx = cw + 4;
+      if ((i & 3) == 0) {
+        ok = wait_w(sfull + slot, (g >> 1) & 1);
+        if (!ok) break;
+        tc::tc_fence_after();
+#pragma unroll
+        for (int s = 0; s < 1 + F::kSets; ++s) scales_to_tmem_w<1>(cw + 4 * s, dS + ((slot * F::kScales + 512 * s) >> 4));
+      }
+      ok = wait_w(full + st, (i / F::kStages) & 1);
+      if (!ok) break;
+      tc::tc_fence_after();
+      const uint32_t id = idesc_e4m3(128, kRows) | scale_ids(i & 3);
+#pragma unroll
+      for (int k = 0; k < kStageK / 32; ++k)
+        mma_e4m3_w<1>(tmem, dW + ((st * F::kStage + 32 * k) >> 4), dX + ((st * F::kStage + 32 * k) >> 4), id, cw, cx, (i > 0 || k > 0) ? 1u : 0u);
+      tc::mma_commit_w(empty + st);
+      if ((i & 3) == 3 || i + 1 == nb) tc::mma_commit_w(sempty + slot);
+    }
+    tc::mma_commit_w(done);
+  } else if (warp == 2) {
+    for (int g = 0; 4 * g < nb && ok; ++g) {
+      const int slot = g & 1, n = nb - 4 * g < 4 ? nb - 4 * g : 4;
+      uint4 w[1 + F::kSets];
+      const uint32_t ww = scale_word(sw, (int64_t)tile * blocks + kb0 + 4 * g, n);
+      w[0] = make_uint4(ww, ww, ww, ww);
+#pragma unroll
+      for (int s = 0; s < F::kSets; ++s) {
+        uint32_t x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = 128 * s + 32 * j + lane;
+          x[j] = r < kRows && m0 + r < M ? scale_word(sx, (m0 + r) * blocks + kb0 + 4 * g, n) : 0x7f7f7f7fu;
+        }
+        w[1 + s] = make_uint4(x[0], x[1], x[2], x[3]);
+      }
+      if (g >= 2) ok = wait_w(sempty + slot, ((g >> 1) - 1) & 1);
+      if (!ok) break;
+#pragma unroll
+      for (int s = 0; s < 1 + F::kSets; ++s)
+        *reinterpret_cast<uint4*>(sm + F::oScales + slot * F::kScales + 512 * s + 16 * lane) = w[s];
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(sfull + slot);
+    }
+  }
+  // every product done: the sums are in TMEM, and nothing reads or writes the stages any more
+  ok = wait_w(done, 0) && ok;
+  ok = __syncthreads_and(ok);
+  tc::tc_fence_after();
+  if (!ok && threadIdx.x == 0) atomicExch(dev_err, (int32_t)kDevErrTimeout);
+
+  const int64_t n = n0 + threadIdx.x;
+  const uint32_t td = tc::tmem_addr(tmem, 32 * warp, 0);
+  const int rows = (int)(M - m0 < kRows ? M - m0 : kRows);
+  T* o = out + m0 * ldo + n;
+  if (split == 1) {
+    if (ok) {
+#pragma unroll 1
+      for (int c = 0; c < kRows; c += 16) {
+        if (c >= rows) break;
+        float v[16];
+        tc::tmem_ld16(td + c, v);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (c + e < rows && n < N) o[(c + e) * ldo] = from_f32<T>(v[e]);
+      }
+    }
+  } else {
+    float* part = reinterpret_cast<float*>(sm);   // [kRows][128]
+    if (ok) {
+#pragma unroll 1
+      for (int c = 0; c < kRows; c += 16) {
+        if (c >= rows) break;
+        float v[16];
+        tc::tmem_ld16(td + c, v);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) part[(c + e) * 128 + threadIdx.x] = v[e];
+      }
+    }
+    tc::cluster_sync_all();
+    if (ok) {
+      uint32_t peer[8];
+#pragma unroll
+      for (int s = 0; s < 8; ++s) peer[s] = s < split ? tc::mapa_shared(part + threadIdx.x, s) : 0u;
+      for (int r = rank; r < rows; r += split) {
+        float x[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s) x[s] = s < split ? ld_cluster(peer[s] + r * 512) : 0.f;
+        float sum = x[0];
+#pragma unroll
+        for (int s = 1; s < 8; ++s) sum += x[s];
+        if (n < N) o[r * ldo] = from_f32<T>(sum);
+      }
+    }
+    tc::cluster_sync_all();   // no CTA leaves while another reads its sums
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tc::tmem_dealloc(tmem, F::kTmem);
+}
+
+template <int kRows, typename T>
+cudaError_t launch_few(const MatmulProblem& p, int split, cudaStream_t stream) {
+  using F = Few<kRows>;
+  CUtensorMap mw, mx;
+  if (!codes_map(&mw, p.w, p.N, p.K, p.ldw, 128) || !codes_map(&mx, p.a, p.M, p.K, p.lda, kRows)) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(fp8_matmul_few_kernel<kRows, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F::kAlloc);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((p.N + 127) / 128 * split), (unsigned)((p.M + kRows - 1) / kRows));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = F::kAlloc;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)split;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  prof_begin(stream, "fp8_matmul_few_kernel");
+  e = cudaLaunchKernelEx(&cfg, fp8_matmul_few_kernel<kRows, T>, mw, mx, p.sw, p.sa, p.M, p.N, (int32_t)((p.K + kStageK - 1) / kStageK),
+                         static_cast<T*>(p.out), p.ldo, (int32_t)split, p.dev_err);
+  prof_end(stream);
+  return e;
+}
+
+template <typename T>
+cudaError_t few(const MatmulProblem& p, cudaStream_t stream) {
+  const int rows = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : p.M <= 128 ? 128 : 256;
+  const int64_t tiles = (p.N + 127) / 128 * ((p.M + rows - 1) / rows), blocks = (p.K + kStageK - 1) / kStageK;
+  int split = 1;
+  while (split < 8 && tiles * split < 152 && blocks >= 4 * split) split *= 2;
+  switch (rows) {
+    case 16: return launch_few<16, T>(p, split, stream);
+    case 32: return launch_few<32, T>(p, split, stream);
+    case 64: return launch_few<64, T>(p, split, stream);
+    case 128: return launch_few<128, T>(p, split, stream);
+    default: return launch_few<256, T>(p, split, stream);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_matmul(const MatmulProblem& p, cudaStream_t stream) {
+  return p.dt == KDA_F32 ? few<float>(p, stream) : few<__nv_bfloat16>(p, stream);
+}
+
+}  // namespace dense
+}  // namespace kda

@@ -1,0 +1,125 @@
+// The block-scaled 8-bit tensor-core instructions (tcgen05 kind::mxf8f6f4), what they need of
+// shared memory and TMEM, and tensor maps over 8-bit matrices.
+//
+// D[m][n] += sum over 32 k of A[m][k] 2^(sa - 127) B[n][k] 2^(sb - 127), E4M3 values, E8M0 scale
+// bytes, fp32 in TMEM.  The scales of 128 rows lie in four TMEM columns: the 32-bit word of row r
+// in lane r % 32 (the same in each quarter of the lanes), column r / 32.  A word holds four bytes,
+// and the instruction says which one it takes: here the byte of a K block of 128, so that one word
+// serves four blocks and 16 instructions.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "tc_ptx.cuh"
+
+namespace kda {
+namespace dense {
+
+constexpr long long kWaitLimit = 2000000000LL;   // ~1 s of SM clocks per bounded wait
+constexpr int kStageK = 128;                     // bytes of K of a pipeline stage: one 128-byte swizzle row, one scale
+
+// Instruction descriptor: E4M3 A and B, both K-major, E8M0 scales, shape M x N (x K = 32); the
+// scale bytes that it takes are added by scale_ids.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+  return ((uint32_t)(N >> 3) << 17)     // N / 8
+         | (1u << 23)                   // scale format: E8M0
+         | ((uint32_t)(M >> 4) << 24);  // M / 16
+}
+__host__ __device__ constexpr uint32_t scale_ids(int byte) {
+  return ((uint32_t)byte << 4) | ((uint32_t)byte << 29);   // of B, of A
+}
+
+// Descriptor of scale words in shared memory for tcgen05.cp: 32 rows of 16 bytes, no swizzle, 8-row
+// groups 128 bytes apart.
+__device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(128u >> 4) << 32;   // stride byte offset
+  d |= (uint64_t)1u << 46;            // descriptor version 1
+  return d;
+}
+
+// Warp-level forms as in tc_ptx.cuh: all 32 lanes with uniform operands, one elected lane issues.
+template <int kGroup>
+__device__ __forceinline__ void mma_e4m3_w(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sa_tmem,
+                                           uint32_t sb_tmem, uint32_t accumulate) {
+  if constexpr (kGroup == 1) {
+    asm volatile(
+        "{\n\t.reg .pred p, pe;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "elect.sync _|pe, 0xffffffff;\n\t"
+        "@pe tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p, pe;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "elect.sync _|pe, 0xffffffff;\n\t"
+        "@pe tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+  }
+}
+
+// 128 rows' scale words from shared memory to four TMEM columns; in order with the MMAs that the
+// same thread issues after it.
+template <int kGroup>
+__device__ __forceinline__ void scales_to_tmem_w(uint32_t tmem, uint64_t desc) {
+  if constexpr (kGroup == 1) {
+    asm volatile(
+        "{\n\t.reg .pred pe;\n\t"
+        "elect.sync _|pe, 0xffffffff;\n\t"
+        "@pe tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(tmem), "l"(desc)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred pe;\n\t"
+        "elect.sync _|pe, 0xffffffff;\n\t"
+        "@pe tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(tmem), "l"(desc)
+        : "memory");
+  }
+}
+
+// Wait of a whole warp.
+__device__ __forceinline__ bool wait_w(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, kWaitLimit));
+}
+
+// The four bytes scales[at .. at + 3] as a word, byte i only for i < n (the others 127: a factor 1).
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* scales, int64_t at, int n) {
+  uint32_t w = 0x7f7f7f7fu;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < n) w = (w & ~(0xffu << (8 * i))) | (uint32_t)__ldg(scales + at + i) << (8 * i);
+  return w;
+}
+
+// ------------------------------------------------------------------------------ host
+inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encode() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+// Boxes of 128 bytes of K (zeros behind K) by box_rows rows (zeros behind the last), 128-byte swizzle.
+inline bool codes_map(CUtensorMap* m, const uint8_t* base, int64_t rows, int64_t K, int64_t stride, int box_rows) {
+  const auto fn = tensor_map_encode();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)stride};
+  const cuuint32_t box[2] = {kStageK, (cuuint32_t)box_rows};
+  const cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace dense
+}  // namespace kda

@@ -1,0 +1,161 @@
+// The residual's addition and a root-mean-square norm, in the input's type or in 8 bits.
+//
+//   s = x + r,   h = round(s),   y = s / sqrt(mean s^2 + eps) * w
+//
+// Bound: HBM, each value read and written once.  A row stays in registers between its sum and
+// its output: W warps of a CTA have J x 256 columns each (one warp alone for narrow rows), all
+// loads of a row on their way before the first is used; the 8-bit form takes its block maxima from
+// the same registers, so that nothing is read twice.
+#include <type_traits>
+
+#include "internal.cuh"
+
+namespace kda {
+namespace dense {
+namespace {
+
+constexpr int kRowsPerBlock = 4;   // of the one-warp form
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+  return x;
+}
+
+// Sum over the W warps of a row, the same in each thread (warps in order: the same bits every time).
+template <bool kOneWarp>
+__device__ __forceinline__ float row_sum(float x, float* part, int warp, int lane, int W) {
+  x = warp_sum(x);
+  if constexpr (!kOneWarp) {
+    __syncthreads();   // the last sum's readers are done
+    if (lane == 0) part[warp] = x;
+    __syncthreads();
+    x = warp_sum(lane < W ? part[lane] : 0.f);
+  }
+  return x;
+}
+
+template <typename T, int J, bool kAdd, bool kFp8, bool kWide, bool kOneWarp>
+__global__ void __launch_bounds__(kOneWarp ? 32 * kRowsPerBlock : 1024)
+    add_rmsnorm_kernel(const T* x, int64_t xs, const T* r, int64_t rs, const float* __restrict__ w, float eps,
+                       int64_t rows, int64_t C, T* h, T* y, uint8_t* codes, uint8_t* scales) {
+  __shared__ float part[32];
+  const int lane = threadIdx.x & 31, warp = kOneWarp ? 0 : threadIdx.x >> 5, W = kOneWarp ? 1 : blockDim.x >> 5;
+  const int64_t row = kOneWarp ? (int64_t)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 5) : blockIdx.x;
+  if (kOneWarp && row >= rows) return;
+  float v[J][8];
+#pragma unroll
+  for (int j = 0; j < J; ++j) load8<T, kWide>(x + row * xs, 256 * (int64_t)(warp + W * j), C, lane, v[j]);
+  if constexpr (kAdd) {
+    float u[J][8];
+#pragma unroll
+    for (int j = 0; j < J; ++j) load8<T, kWide>(r + row * rs, 256 * (int64_t)(warp + W * j), C, lane, u[j]);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j][i] += u[j][i];
+      store8<T, kWide>(h + row * C, 256 * (int64_t)(warp + W * j), C, lane, v[j]);
+    }
+  }
+  auto squares = [&]() {
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s = fmaf(v[j][i], v[j][i], s);
+    return row_sum<kOneWarp>(s, part, warp, lane, W);
+  };
+  float ss = squares();
+  // Squares beyond fp32's range, or below it with an eps that does not cover them: the row once more, scaled
+  // by a power of two (every thread of the row has the same ss).
+  const bool high = !(ss < __uint_as_float(0x7f800000u)), low = ss < 0x1p-60f && eps < 0x1p-100f;
+  if (high || low) {
+    const float f = high ? 0x1p-80f : 0x1p80f;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j][i] *= f;
+    eps = high ? 0.f : eps * 0x1p80f * 0x1p80f;   // (beside squares of 2^126 and more, eps counts only above 2^100)
+    ss = squares();
+  }
+  const float inv = 1.0f / sqrtf(ss / (float)C + eps);
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int64_t c0 = 256 * (int64_t)(warp + W * j);
+    if (c0 >= C) continue;
+    if (w) {
+      float g[8];
+      if constexpr (kWide) {
+        const int64_t c = c0 + 8 * lane;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+        if (c < C) a = __ldg(reinterpret_cast<const float4*>(w + c)), b = __ldg(reinterpret_cast<const float4*>(w + c) + 1);
+        g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w, g[4] = b.x, g[5] = b.y, g[6] = b.z, g[7] = b.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int64_t c = c0 + lane + 32 * i;
+          g[i] = c < C ? __ldg(w + c) : 0.f;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j][i] = v[j][i] * inv * g[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j][i] *= inv;
+    }
+    if constexpr (kFp8) {
+      // a row with a sum that is not finite has NaN in the columns behind C as well: they belong to no block
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c0 + column<kWide>(lane, i) >= C) v[j][i] = 0.f;
+      store_fp8<kWide>(codes + row * C, scales + row * ((C + kBlock - 1) / kBlock), c0, C, lane, v[j]);
+    } else {
+      store8<T, kWide>(y + row * C, c0, C, lane, v[j]);
+    }
+  }
+}
+
+template <typename T, int J, bool kAdd, bool kFp8, bool kWide>
+cudaError_t launch4(const NormProblem& p, int warps, cudaStream_t stream) {
+  auto go = [&](auto one) {
+    constexpr bool kOne = decltype(one)::value;
+    const unsigned grid = (unsigned)(kOne ? (p.T + kRowsPerBlock - 1) / kRowsPerBlock : p.T);
+    add_rmsnorm_kernel<T, J, kAdd, kFp8, kWide, kOne><<<grid, kOne ? 32 * kRowsPerBlock : 32 * warps, 0, stream>>>(
+        static_cast<const T*>(p.x), p.xs, static_cast<const T*>(p.r), p.rs, p.w, p.eps, p.T, p.C, static_cast<T*>(p.h),
+        static_cast<T*>(p.y), p.codes, p.scales);
+  };
+  prof_begin(stream, "add_rmsnorm_kernel");
+  if (warps == 1) go(std::true_type{});
+  else go(std::false_type{});
+  prof_end(stream);
+  return cudaGetLastError();
+}
+
+template <typename T, int J, bool kWide>
+cudaError_t launch2(const NormProblem& p, int warps, cudaStream_t stream) {
+  if (p.r) return p.codes ? launch4<T, J, true, true, kWide>(p, warps, stream) : launch4<T, J, true, false, kWide>(p, warps, stream);
+  return p.codes ? launch4<T, J, false, true, kWide>(p, warps, stream) : launch4<T, J, false, false, kWide>(p, warps, stream);
+}
+
+template <typename T>
+cudaError_t launch1(const NormProblem& p, cudaStream_t stream) {
+  const auto at = [](const void* q, size_t n) { return reinterpret_cast<uintptr_t>(q) % n == 0; };
+  const int64_t step = 16 / sizeof(T);
+  const bool wide = p.C % 8 == 0 && p.xs % step == 0 && at(p.x, 16) && (!p.r || (p.rs % step == 0 && at(p.r, 16) && at(p.h, 16))) &&
+                    at(p.w, 16) && (p.codes ? at(p.codes, 8) : at(p.y, 16));
+  const int chunks = (int)((p.C + 255) / 256);   // 256 columns each, at most 128
+  // One or two chunks: a warp a row.  Else two chunks a warp up to 64 of them (32 warps), then four.
+  if (chunks <= 1) return wide ? launch2<T, 1, true>(p, 1, stream) : launch2<T, 1, false>(p, 1, stream);
+  const int J = chunks <= 64 ? 2 : 4, warps = (chunks + J - 1) / J;
+  if (J == 2) return wide ? launch2<T, 2, true>(p, warps, stream) : launch2<T, 2, false>(p, warps, stream);
+  return wide ? launch2<T, 4, true>(p, warps, stream) : launch2<T, 4, false>(p, warps, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_norm(const NormProblem& p, cudaStream_t stream) {
+  return p.dt == KDA_F32 ? launch1<float>(p, stream) : launch1<__nv_bfloat16>(p, stream);
+}
+
+}  // namespace dense
+}  // namespace kda
