@@ -202,6 +202,7 @@ struct MatmulProblem {
   int32_t* dev_err;
 };
 cudaError_t launch_matmul(const MatmulProblem& p, cudaStream_t stream);
+cudaError_t launch_matmul_pair(const MatmulProblem& p, int sms, cudaStream_t stream);   // many rows
 
 struct RotaryPart {   // queries or keys
   const void* x;

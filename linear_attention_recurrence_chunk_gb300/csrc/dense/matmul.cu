@@ -8,6 +8,7 @@
 // fill the chip; its partial sums meet in distributed shared memory in a fixed order, with no scratch memory
 // and one launch.
 #include <algorithm>
+#include <cstdlib>
 
 #include "internal.cuh"
 #include "mma8.cuh"
@@ -24,35 +25,37 @@ struct Few {
   static constexpr uint32_t kW = 128 * kStageK, kX = kRows * kStageK, kStage = kW + kX;
   static constexpr int kSets = (kRows + 127) / 128;               // of 128 tokens' scales
   static constexpr uint32_t kScales = 512 * (1 + kSets);          // one slot: weights', tokens'
-  static constexpr uint32_t oScales = kStages * kStage, oBars = oScales + 2 * kScales;
-  static constexpr int kBars = 2 * kStages + 5;
+  static constexpr uint32_t oScales = kStages * kStage, oBars = oScales + kScaleSlots * kScales;
+  static constexpr int kBars = 2 * kStages + 2 * kScaleSlots + 1;
   static constexpr uint32_t kBytes = oBars + kBars * 8 + 8, kAlloc = kBytes + 1024;   // + alignment
   static constexpr uint32_t cScales = kRows, kCols = kRows + 2 * 4 * (1 + kSets);      // TMEM columns
   static constexpr uint32_t kTmem = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static_assert(kStages * kStage >= kRows * 512, "partial sums take the stages' place");
 };
 
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float x;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(addr) : "memory");
   return x;
 }
 
 template <int kRows, typename T>
 __global__ void __launch_bounds__(kThreads)
     fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapX, const uint8_t* __restrict__ sw,
-                          const uint8_t* __restrict__ sx, int64_t M, int64_t N, int32_t blocks, T* out, int64_t ldo, int32_t split,
-                          int32_t* dev_err) {
+                          const uint8_t* __restrict__ sx, int64_t M, int64_t N, int32_t blocks, T* out, int64_t ldo, int32_t quads,
+                          int32_t words, int32_t split, int32_t* dev_err) {
   using F = Few<kRows>;
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + F::oBars);
-  uint64_t *empty = full + F::kStages, *sfull = empty + F::kStages, *sempty = sfull + 2, *done = sempty + 2;
+  uint64_t *empty = full + F::kStages, *sfull = empty + F::kStages, *sempty = sfull + kScaleSlots, *done = sempty + kScaleSlots;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(done + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t tile = blockIdx.x / split, rank = blockIdx.x - tile * split;
   const int64_t n0 = (int64_t)tile * 128, m0 = (int64_t)blockIdx.y * kRows;
-  const int32_t kb0 = (int32_t)((int64_t)blocks * rank / split), nb = (int32_t)((int64_t)blocks * (rank + 1) / split) - kb0;
+  // this CTA's K blocks: whole groups of four, whose scales share a word
+  const int32_t groups = (blocks + 3) / 4, kb0 = (int32_t)((int64_t)groups * rank / split) * 4;
+  const int32_t nb = (int32_t)min((int64_t)groups * (rank + 1) / split * 4, (int64_t)blocks) - kb0;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -90,10 +93,11 @@ __global__ void __launch_bounds__(kThreads)
     const uint64_t dW = tc::desc_kmajor_sw128(tc::smem_u32(sm)), dX = tc::desc_kmajor_sw128(tc::smem_u32(sm + F::kW));
     const uint64_t dS = desc_scales(tc::smem_u32(sm + F::oScales));
     for (int i = 0; i < nb && ok; ++i) {
-      const int st = i % F::kStages, g = i >> 2, slot = g & 1;
-      const uint32_t cw = tmem + F::cScales + slot * 4 * (1 + F::kSets), cx = cw + 4;
+      const int st = i % F::kStages, g = i >> 2, slot = g % kScaleSlots;
+      const uint32_t cw = tmem + F::cScales + (g & 1) * 4 * (1 + F::kSets), cx = cw + 4;
       if ((i & 3) == 0) {
-        ok = wait_w(sfull + slot, (g >> 1) & 1);
+        // the products that read these columns, two groups ago, are done
+        ok = (g < 2 || wait_w(sempty + (g - 2) % kScaleSlots, ((g - 2) / kScaleSlots) & 1)) && wait_w(sfull + slot, (g / kScaleSlots) & 1);
         if (!ok) break;
         tc::tc_fence_after();
 #pragma unroll
@@ -112,25 +116,19 @@ __global__ void __launch_bounds__(kThreads)
     tc::mma_commit_w(done);
   } else if (warp == 2) {
     for (int g = 0; 4 * g < nb && ok; ++g) {
-      const int slot = g & 1, n = nb - 4 * g < 4 ? nb - 4 * g : 4;
-      uint4 w[1 + F::kSets];
-      const uint32_t ww = scale_word(sw, (int64_t)tile * blocks + kb0 + 4 * g, n);
-      w[0] = make_uint4(ww, ww, ww, ww);
-#pragma unroll
-      for (int s = 0; s < F::kSets; ++s) {
-        uint32_t x[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = 128 * s + 32 * j + lane;
-          x[j] = r < kRows && m0 + r < M ? scale_word(sx, (m0 + r) * blocks + kb0 + 4 * g, n) : 0x7f7f7f7fu;
-        }
-        w[1 + s] = make_uint4(x[0], x[1], x[2], x[3]);
-      }
-      if (g >= 2) ok = wait_w(sempty + slot, ((g >> 1) - 1) & 1);
+      const int slot = g % kScaleSlots;
+      uint32_t ww[1], wx[4 * F::kSets];
+      load_scales(sw, blocks, kb0 + 4 * g, words, ww, [&](int) { return (int64_t)tile; });
+      load_scales(sx, blocks, kb0 + 4 * g, words, wx, [&](int i) {
+        const int r = 32 * i + lane;
+        return r < kRows && m0 + r < M ? m0 + r : (int64_t)-1;
+      });
+      if (g >= kScaleSlots) ok = wait_w(sempty + slot, (g / kScaleSlots - 1) & 1);
       if (!ok) break;
+      uint4* to = reinterpret_cast<uint4*>(sm + F::oScales + slot * F::kScales) + lane;
+      to[0] = make_uint4(ww[0], ww[0], ww[0], ww[0]);
 #pragma unroll
-      for (int s = 0; s < 1 + F::kSets; ++s)
-        *reinterpret_cast<uint4*>(sm + F::oScales + slot * F::kScales + 512 * s + 16 * lane) = w[s];
+      for (int s = 0; s < F::kSets; ++s) to[32 * (1 + s)] = make_uint4(wx[4 * s], wx[4 * s + 1], wx[4 * s + 2], wx[4 * s + 3]);
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(sfull + slot);
@@ -172,17 +170,31 @@ __global__ void __launch_bounds__(kThreads)
     }
     tc::cluster_sync_all();
     if (ok) {
+      // this CTA's rows are rank, rank + split, ...: a warp takes a row at a time, a lane four columns
       uint32_t peer[8];
 #pragma unroll
-      for (int s = 0; s < 8; ++s) peer[s] = s < split ? tc::mapa_shared(part + threadIdx.x, s) : 0u;
-      for (int r = rank; r < rows; r += split) {
-        float x[8];
+      for (int s = 0; s < 8; ++s) peer[s] = s < split ? tc::mapa_shared(part + 4 * lane, s) : 0u;
+      const int64_t nl = n0 + 4 * lane;
+      const int left = (int)(N - nl < 4 ? N - nl : 4);   // columns of this lane
+#pragma unroll 2
+      for (int r = rank + split * warp; r < rows; r += split * (kThreads / 32)) {
+        float4 x[8];
 #pragma unroll
-        for (int s = 0; s < 8; ++s) x[s] = s < split ? ld_cluster(peer[s] + r * 512) : 0.f;
-        float sum = x[0];
+        for (int s = 0; s < 8; ++s)
+          if (s < split) x[s] = ld_cluster(peer[s] + r * 512);
+        float v[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
 #pragma unroll
-        for (int s = 1; s < 8; ++s) sum += x[s];
-        if (n < N) o[r * ldo] = from_f32<T>(sum);
+        for (int s = 1; s < 8; ++s)
+          if (s < split) v[0] += x[s].x, v[1] += x[s].y, v[2] += x[s].z, v[3] += x[s].w;
+        T* y = out + (m0 + r) * ldo + nl;
+        if (quads && left == 4) {
+          if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(y) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+          else *reinterpret_cast<float4*>(y) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < left) y[i] = from_f32<T>(v[i]);
+        }
       }
     }
     tc::cluster_sync_all();   // no CTA leaves while another reads its sums
@@ -210,9 +222,11 @@ cudaError_t launch_few(const MatmulProblem& p, int split, cudaStream_t stream) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  const bool quads = reinterpret_cast<uintptr_t>(p.out) % (4 * sizeof(T)) == 0 && p.ldo % 4 == 0;   // four columns a store
   prof_begin(stream, "fp8_matmul_few_kernel");
   e = cudaLaunchKernelEx(&cfg, fp8_matmul_few_kernel<kRows, T>, mw, mx, p.sw, p.sa, p.M, p.N, (int32_t)((p.K + kStageK - 1) / kStageK),
-                         static_cast<T*>(p.out), p.ldo, (int32_t)split, p.dev_err);
+                         static_cast<T*>(p.out), p.ldo, (int32_t)quads,
+                         (int32_t)scale_words(p.sa, p.sw, (p.K + kStageK - 1) / kStageK), (int32_t)split, p.dev_err);
   prof_end(stream);
   return e;
 }
@@ -222,7 +236,7 @@ cudaError_t few(const MatmulProblem& p, cudaStream_t stream) {
   const int rows = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : p.M <= 128 ? 128 : 256;
   const int64_t tiles = (p.N + 127) / 128 * ((p.M + rows - 1) / rows), blocks = (p.K + kStageK - 1) / kStageK;
   int split = 1;
-  while (split < 8 && tiles * split < 152 && blocks >= 4 * split) split *= 2;
+  while (split < 8 && tiles * split < 152 && blocks >= 8 * split) split *= 2;
   switch (rows) {
     case 16: return launch_few<16, T>(p, split, stream);
     case 32: return launch_few<32, T>(p, split, stream);
@@ -235,6 +249,13 @@ cudaError_t few(const MatmulProblem& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_matmul(const MatmulProblem& p, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  bool pair = p.M > 256;
+  if (const char* env = std::getenv("KDA_FP8_PAIR")) pair = std::atoi(env) != 0;
+  if (pair) return launch_matmul_pair(p, sms, stream);
   return p.dt == KDA_F32 ? few<float>(p, stream) : few<__nv_bfloat16>(p, stream);
 }
 

@@ -1,0 +1,301 @@
+// The product of 8-bit matrices for many rows of A (prompts).
+//
+//   out[m][n] = sum_k A[m][k] W[n][k]
+//
+// Bound: the tensor core.  Two CTAs of a cluster make one tile of 256 x 240 (cta_group::2: each holds half the
+// rows of A and half the columns' weights, so that a byte of shared memory serves twice the products
+// of a single CTA's tile).  240 columns, not 256, because the 512 columns of TMEM hold two accumulators, the one being
+// filled and the one being stored, and the scales.  Persistent: a pair takes tile after tile, and loads, products and
+// stores of neighbouring tiles overlap.
+//
+// Warps of a CTA: 0 loads tiles, 1 issues products (of the leading CTA alone), 2 loads scales, 3 TMEM,
+// 4 to 7 store.
+#include <algorithm>
+
+#include "internal.cuh"
+#include "mma8.cuh"
+
+namespace kda {
+namespace dense {
+namespace {
+
+constexpr int kTM = 256, kTN = 240, kThreads = 256, kStages = 6;
+constexpr uint32_t kA = 128 * kStageK, kB = kTN / 2 * kStageK, kStage = kA + kB;
+constexpr uint32_t kScales = 3 * 512;   // one slot: 128 rows of A, twice 128 of W
+constexpr uint32_t oScales = kStages * kStage, oTurn = oScales + kScaleSlots * kScales, kTurnRow = 33;
+constexpr uint32_t oBars = oTurn + 4 * 32 * kTurnRow * 4;
+constexpr int kBars = 2 * kStages + 2 * kScaleSlots + 4;
+constexpr uint32_t kAlloc = oBars + kBars * 8 + 8 + 1024;
+constexpr uint32_t cScales = 2 * kTN;   // TMEM columns: two accumulators, two slots of scales
+constexpr int kGroupM = 8;              // tiles are taken in bands of so many rows of tiles
+static_assert(kAlloc <= 227 * 1024, "shared memory");
+
+// ------------------------------------------------------------- forms for a pair of CTAs
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          tc::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+// Arrival on an mbarrier of the cluster (address from mapa_shared), released at CTA scope: what it orders lies in
+// this CTA's own shared memory (behind a proxy fence) or TMEM.  (A release at cluster scope costs about 1,000 cycles.)
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Arrive at this barrier of both CTAs once every MMA issued so far by the elected lane has completed.
+__device__ __forceinline__ void commit_both_w(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred pe;\n\t.reg .b16 m;\n\t"
+      "mov.b16 m, 3;\n\t"
+      "elect.sync _|pe, 0xffffffff;\n\t"
+      "@pe tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(tc::smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::smem_u32(dst)) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free_pair(uint32_t taddr) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
+}
+
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+               "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// Tile t of tm x tn: bands of kGroupM rows of tiles, column after column inside a band, so that the tiles in
+// flight share both their rows of A and their weights in L2.
+__device__ __forceinline__ void place(int64_t t, int64_t tm, int64_t tn, int64_t& im, int64_t& in) {
+  const int64_t band = t / (kGroupM * tn), first = band * kGroupM, rows = tm - first < kGroupM ? tm - first : kGroupM;
+  const int64_t rest = t - band * kGroupM * tn;
+  in = rest / rows;
+  im = first + rest - in * rows;
+}
+
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    fp8_matmul_pair_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB, const uint8_t* __restrict__ sa,
+                           const uint8_t* __restrict__ sw, int64_t M, int64_t N, int32_t blocks, int64_t tm, int64_t tn, T* out, int64_t ldo,
+                           int32_t wide, int32_t words, int32_t* dev_err) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* sm = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + oBars);        // of the leading CTA: both CTAs' tiles are there
+  uint64_t* empty = full + kStages;                                // of both: the stage has been used
+  uint64_t *sfull = empty + kStages, *sempty = sfull + kScaleSlots;          // the same of the scales' slots
+  uint64_t *tfull = sempty + kScaleSlots, *tempty = tfull + 2;               // accumulators: filled (both), stored (the leading CTA's)
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(tempty + 2);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = tc::cluster_ctarank();
+  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, tiles = tm * tn;
+  const int groups = (blocks + 3) / 4;   // of four K blocks: a word of scales
+
+  if (warp == 0 && lane == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      tc::mbar_init(full + i, 1);
+      tc::mbar_init(empty + i, 1);
+    }
+    for (int i = 0; i < kScaleSlots; ++i) {
+      tc::mbar_init(sfull + i, 2);
+      tc::mbar_init(sempty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(tfull + i, 1);
+      tc::mbar_init(tempty + i, 8);
+    }
+    tc::fence_mbar_init();
+  }
+  if (warp == 3) tmem_alloc_pair(tmem_at);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::cluster_sync_all();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_at;
+  bool ok = true;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int64_t n = 0;   // stages so far
+      for (int64_t t = pair; t < tiles && ok; t += pairs) {
+        int64_t im, in;
+        place(t, tm, tn, im, in);
+        const int32_t ya = (int32_t)(im * kTM + 128 * rank), yb = (int32_t)(in * kTN + kTN / 2 * rank);
+        for (int32_t kb = 0; kb < blocks; ++kb, ++n) {
+          const int st = (int)(n % kStages);
+          if (n >= kStages && !(ok = tc::mbar_wait(empty + st, (uint32_t)(n / kStages - 1) & 1, kWaitLimit))) break;
+          const uint32_t bar = tc::mapa_shared(full + st, 0);
+          // the leading CTA expects both CTAs' bytes; the other's may come first, its arrival is what ends the phase
+          if (rank == 0) tc::mbar_arrive_expect_tx(full + st, 2 * kStage);
+          tma_load_pair(sm + st * kStage, &mapA, kb * kStageK, ya, bar);
+          tma_load_pair(sm + st * kStage + kA, &mapB, kb * kStageK, yb, bar);
+        }
+      }
+      // end with no copy and no arrival in flight
+      for (int64_t i = n > kStages ? n - kStages : 0; i < n; ++i) ok = tc::mbar_wait(empty + i % kStages, (uint32_t)(i / kStages) & 1, kWaitLimit) && ok;
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0) {
+      const uint64_t dA = tc::desc_kmajor_sw128(tc::smem_u32(sm)), dB = tc::desc_kmajor_sw128(tc::smem_u32(sm + kA));
+      const uint64_t dS = desc_scales(tc::smem_u32(sm + oScales));
+      int st = 0, it = 0;
+      uint32_t phase = 0, g = 0;
+      for (int64_t t = pair; t < tiles && ok; t += pairs, ++it) {
+        const uint32_t acc = tmem + (it & 1) * kTN;
+        if (it >= 2 && !(ok = wait_w(tempty + (it & 1), ((it >> 1) - 1) & 1))) break;
+        tc::tc_fence_after();
+        for (int32_t k0 = 0; k0 < blocks && ok; k0 += 4, ++g) {   // four K blocks, a word of scales
+          const uint32_t slot = g % kScaleSlots, ca = tmem + cScales + (g & 1) * 12, cb = ca + 4;
+          // the products that read these columns, two groups ago, are done
+          if (g >= 2 && !(ok = wait_w(sempty + (g - 2) % kScaleSlots, ((g - 2) / kScaleSlots) & 1))) break;
+          if (!(ok = wait_w(sfull + slot, (g / kScaleSlots) & 1))) break;
+          tc::tc_fence_after();
+#pragma unroll
+          for (int s = 0; s < 3; ++s) scales_to_tmem_w<2>(ca + 4 * s, dS + ((slot * kScales + 512 * s) >> 4));
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            if (k0 + b >= blocks) break;
+            if (!(ok = wait_w(full + st, phase))) break;
+            tc::tc_fence_after();
+            const uint64_t da = dA + (st * kStage >> 4), db = dB + (st * kStage >> 4);
+#pragma unroll
+            for (int k = 0; k < kStageK / 32; ++k)
+              mma_e4m3_w<2>(acc, da + 2 * k, db + 2 * k, idesc_e4m3(kTM, kTN) | scale_ids(b), ca, cb, (b > 0 || k > 0) ? 1u : (uint32_t)k0);
+            commit_both_w(empty + st);
+            if (++st == kStages) st = 0, phase ^= 1;
+          }
+          if (ok) commit_both_w(sempty + slot);
+        }
+        if (!ok) break;
+        commit_both_w(tfull + (it & 1));
+      }
+      for (int i = it > 2 ? it - 2 : 0; i < it; ++i) ok = wait_w(tempty + (i & 1), (i >> 1) & 1) && ok;
+    }
+  } else if (warp == 2) {
+    uint32_t g = 0, wa[4], wb[8];
+    int64_t t = pair, im, in;
+    int gg = 0;
+    auto load = [&]() {   // of group gg of tile t
+      place(t, tm, tn, im, in);
+      load_scales(sa, blocks, 4 * gg, words, wa, [&](int i) {
+        const int64_t m = im * kTM + 128 * rank + 32 * i + lane;
+        return m < M ? m : -1;
+      });
+      load_scales(sw, blocks, 4 * gg, words, wb, [&](int i) {
+        const int64_t c = in * kTN + 32 * i + lane;
+        return c < N ? c / kBlock : -1;
+      });
+    };
+    if (t < tiles) load();
+    while (t < tiles) {
+      const uint32_t slot = g % kScaleSlots;
+      if (g >= kScaleSlots && !(ok = wait_w(sempty + slot, (g / kScaleSlots - 1) & 1))) break;
+      uint4* to = reinterpret_cast<uint4*>(sm + oScales + slot * kScales) + lane;
+      to[0] = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+      to[32] = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+      to[64] = make_uint4(wb[4], wb[5], wb[6], wb[7]);
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (++gg == groups) gg = 0, t += pairs;
+      if (t < tiles) load();   // on their way during the arrival
+      if (lane == 0) arrive_cluster(tc::mapa_shared(sfull + slot, 0));
+      ++g;
+    }
+    for (uint32_t i = g > kScaleSlots ? g - kScaleSlots : 0; i < g; ++i)
+      ok = wait_w(sempty + i % kScaleSlots, (i / kScaleSlots) & 1) && ok;
+  } else if (warp >= 4) {
+    const int q = warp - 4;
+    float* turn = reinterpret_cast<float*>(sm + oTurn) + q * 32 * kTurnRow;
+    int it = 0;
+    for (int64_t t = pair; t < tiles; t += pairs, ++it) {
+      int64_t im, in;
+      place(t, tm, tn, im, in);
+      if (!(ok = wait_w(tfull + (it & 1), (it >> 1) & 1))) break;
+      tc::tc_fence_after();
+      const uint32_t acc = tc::tmem_addr(tmem, 32 * q, (it & 1) * kTN);
+      const int64_t m0 = im * kTM + 128 * rank + 32 * q, n0 = in * kTN;
+      const int rows = (int)(M - m0 < 32 ? M - m0 : 32), cols = (int)(N - n0 < kTN ? N - n0 : kTN);
+#pragma unroll 1
+      for (int c = 0; c < kTN; c += 16) {
+        float v[16];
+        tc::tmem_ld16(acc + c, v);
+        if (c + 16 == kTN) {   // the accumulator is free
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_cluster(tc::mapa_shared(tempty + (it & 1), 0));
+        }
+        if (c + 16 <= cols && wide) {
+          T* o = out + (m0 + lane) * ldo + n0 + c;
+          if (lane < rows) {
+            if constexpr (sizeof(T) == 2) {
+              uint32_t w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[i] = bf16x2(v[2 * i], v[2 * i + 1]);
+              if (wide == 2) {
+                store32(o, w);
+              } else {
+                reinterpret_cast<uint4*>(o)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                reinterpret_cast<uint4*>(o)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+              }
+            } else {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 * h + i]);
+                if (wide == 2) {
+                  store32(o + 8 * h, w);
+                } else {
+                  reinterpret_cast<uint4*>(o)[2 * h] = make_uint4(w[0], w[1], w[2], w[3]);
+                  reinterpret_cast<uint4*>(o)[2 * h + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+              }
+            }
+          }
+        } else if (c < cols) {   // through shared memory: a row's columns next to one another
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) turn[lane * kTurnRow + i] = v[i];
+          __syncwarp();
+          const int cc = lane & 15;
+          for (int r = lane >> 4; r < rows; r += 2)
+            if (c + cc < cols) out[(m0 + r) * ldo + n0 + c + cc] = from_f32<T>(turn[r * kTurnRow + cc]);
+        }
+      }
+    }
+  }
+  if (!__all_sync(0xffffffffu, ok) && lane == 0) atomicExch(dev_err, (int32_t)kDevErrTimeout);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::cluster_sync_all();   // both CTAs are done with one another's barriers and TMEM
+  tc::tc_fence_after();
+  if (warp == 3) tmem_free_pair(tmem);
+}
+
+template <typename T>
+cudaError_t launch(const MatmulProblem& p, int sms, cudaStream_t stream) {
+  CUtensorMap ma, mb;
+  if (!codes_map(&ma, p.a, p.M, p.K, p.lda, 128) || !codes_map(&mb, p.w, p.N, p.K, p.ldw, kTN / 2)) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(fp8_matmul_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAlloc);
+  if (e != cudaSuccess) return e;
+  const int64_t tm = (p.M + kTM - 1) / kTM, tn = (p.N + kTN - 1) / kTN;
+  const auto step = [&](size_t n) { return reinterpret_cast<uintptr_t>(p.out) % n == 0 && (size_t)p.ldo * sizeof(T) % n == 0; };
+  const unsigned grid = 2 * (unsigned)std::min<int64_t>(tm * tn, sms / 2);
+  prof_begin(stream, "fp8_matmul_pair_kernel");
+  fp8_matmul_pair_kernel<T><<<grid, kThreads, kAlloc, stream>>>(ma, mb, p.sa, p.sw, p.M, p.N, (int32_t)((p.K + kStageK - 1) / kStageK), tm, tn,
+                                                               static_cast<T*>(p.out), p.ldo, step(32) ? 2 : step(16) ? 1 : 0,
+                                                               scale_words(p.sa, p.sw, (p.K + kStageK - 1) / kStageK), p.dev_err);
+  prof_end(stream);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_matmul_pair(const MatmulProblem& p, int sms, cudaStream_t stream) {
+  return p.dt == KDA_F32 ? launch<float>(p, sms, stream) : launch<__nv_bfloat16>(p, sms, stream);
+}
+
+}  // namespace dense
+}  // namespace kda

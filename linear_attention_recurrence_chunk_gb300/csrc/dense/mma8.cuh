@@ -82,18 +82,46 @@ __device__ __forceinline__ void scales_to_tmem_w(uint32_t tmem, uint64_t desc) {
   }
 }
 
-// Wait of a whole warp.
+// Wait of a whole warp; one lane asks.
 __device__ __forceinline__ bool wait_w(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, kWaitLimit));
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = tc::mbar_wait(bar, parity, kWaitLimit);
+  return __all_sync(0xffffffffu, ok);
 }
 
-// The four bytes scales[at .. at + 3] as a word, byte i only for i < n (the others 127: a factor 1).
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* scales, int64_t at, int n) {
-  uint32_t w = 0x7f7f7f7fu;
+constexpr int kScaleSlots = 4;   // groups of four K blocks whose scales are on their way (two of them in TMEM)
+
+// Scale words of four K blocks, kb .. kb + 3 of `blocks` (bytes behind the last: 127, a factor 1), for kWords rows:
+// row(i) gives a row's number, negative for none (a factor 1).  No branch stands between the loads, so
+// that all are on their way together.  `words`: rows of whole 32-bit words.
+template <int kWords, typename F>
+__device__ __forceinline__ void load_scales(const uint8_t* __restrict__ scales, int32_t blocks, int32_t kb, bool words, uint32_t (&w)[kWords],
+                                            F row) {
+  int64_t r[kWords];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < n) w = (w & ~(0xffu << (8 * i))) | (uint32_t)__ldg(scales + at + i) << (8 * i);
-  return w;
+  for (int i = 0; i < kWords; ++i) r[i] = row(i);
+  if (words) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(scales + (r[i] < 0 ? 0 : r[i]) * blocks + kb));
+  } else {
+    uint32_t b[kWords][4];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[i][j] = __ldg(scales + (r[i] < 0 ? 0 : r[i]) * blocks + (kb + j < blocks ? kb + j : blocks - 1));
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      w[i] = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[i] |= (kb + j < blocks ? b[i][j] : 127u) << (8 * j);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kWords; ++i)
+    if (r[i] < 0) w[i] = 0x7f7f7f7fu;
+}
+inline bool scale_words(const void* a, const void* b, int64_t blocks) {
+  return blocks % 4 == 0 && reinterpret_cast<uintptr_t>(a) % 4 == 0 && reinterpret_cast<uintptr_t>(b) % 4 == 0;
 }
 
 // ------------------------------------------------------------------------------ host
