@@ -39,6 +39,12 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
   return x;
 }
 
+__device__ __forceinline__ uint32_t cluster_address(uint32_t shared, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(shared), "r"(rank));
+  return r;
+}
+
 template <int kRows, typename T>
 __global__ void __launch_bounds__(kThreads)
     fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapX, const uint8_t* __restrict__ sw,
@@ -73,45 +79,46 @@ __global__ void __launch_bounds__(kThreads)
   bool ok = true;
 
   if (warp == 0) {
-    int issued = 0;
-    if (lane == 0) {
-      for (int i = 0; i < nb && ok; ++i, ++issued) {
-        const int st = i % F::kStages;
-        if (i >= F::kStages) ok = tc::mbar_wait(empty + st, (i / F::kStages - 1) & 1, kWaitLimit);
-        if (!ok) break;
-        uint8_t* w = sm + st * F::kStage;
-        tc::mbar_arrive_expect_tx(full + st, F::kStage);
-        tc::tma_load_2d(w, &mapW, (kb0 + i) * kStageK, (int32_t)n0, full + st);
-        tc::tma_load_2d(w + F::kW, &mapX, (kb0 + i) * kStageK, (int32_t)m0, full + st);
-      }
+    const uint32_t at = tc::smem_u32(sm), bar = tc::smem_u32(full);
+    int st = 0, i = 0;
+    uint32_t phase = 1;
+    for (; i < nb; ++i) {
+      if (i >= F::kStages && !(ok = wait_w(empty + st, phase))) break;
+      expect_w(bar + 8 * st, F::kStage);
+      tma_load_w<1>(at + st * F::kStage, &mapW, (kb0 + i) * kStageK, (int32_t)n0, bar + 8 * st);
+      tma_load_w<1>(at + st * F::kStage + F::kW, &mapX, (kb0 + i) * kStageK, (int32_t)m0, bar + 8 * st);
+      if (++st == F::kStages) st = 0, phase ^= 1;
     }
-    if (lane == 0 && !ok) {   // end with no copy in flight
-      for (int st = 0; st < F::kStages; ++st) tc::mbar_wait(full + st, issued > st ? ((issued - 1 - st) / F::kStages) & 1 : 1, kWaitLimit);
-    }
-    __syncwarp();
+    if (!ok)   // end with no copy in flight
+      for (int j = max(0, i - F::kStages); j < i; ++j) wait_w(full + j % F::kStages, (j / F::kStages) & 1);
   } else if (warp == 1) {
     const uint64_t dW = tc::desc_kmajor_sw128(tc::smem_u32(sm)), dX = tc::desc_kmajor_sw128(tc::smem_u32(sm + F::kW));
     const uint64_t dS = desc_scales(tc::smem_u32(sm + F::oScales));
-    for (int i = 0; i < nb && ok; ++i) {
-      const int st = i % F::kStages, g = i >> 2, slot = g % kScaleSlots;
-      const uint32_t cw = tmem + F::cScales + (g & 1) * 4 * (1 + F::kSets), cx = cw + 4;
-      if ((i & 3) == 0) {
-        // the products that read these columns, two groups ago, are done
-        ok = (g < 2 || wait_w(sempty + (g - 2) % kScaleSlots, ((g - 2) / kScaleSlots) & 1)) && wait_w(sfull + slot, (g / kScaleSlots) & 1);
-        if (!ok) break;
-        tc::tc_fence_after();
-#pragma unroll
-        for (int s = 0; s < 1 + F::kSets; ++s) scales_to_tmem_w<1>(cw + 4 * s, dS + ((slot * F::kScales + 512 * s) >> 4));
-      }
-      ok = wait_w(full + st, (i / F::kStages) & 1);
+    int st = 0;
+    uint32_t phase = 0, cw = tmem + F::cScales;
+    for (int i = 0, g = 0; i < nb && ok; i += 4, ++g) {   // four K blocks, a word of scales
+      const int slot = g % kScaleSlots;
+      // the products that read these columns, two groups ago, are done
+      ok = (g < 2 || wait_w(sempty + (g - 2) % kScaleSlots, ((g - 2) / kScaleSlots) & 1)) && wait_w(sfull + slot, (g / kScaleSlots) & 1);
       if (!ok) break;
       tc::tc_fence_after();
-      const uint32_t id = idesc_e4m3(128, kRows) | scale_ids(i & 3);
 #pragma unroll
-      for (int k = 0; k < kStageK / 32; ++k)
-        mma_e4m3_w<1>(tmem, dW + ((st * F::kStage + 32 * k) >> 4), dX + ((st * F::kStage + 32 * k) >> 4), id, cw, cx, (i > 0 || k > 0) ? 1u : 0u);
-      tc::mma_commit_w(empty + st);
-      if ((i & 3) == 3 || i + 1 == nb) tc::mma_commit_w(sempty + slot);
+      for (int s = 0; s < 1 + F::kSets; ++s) scales_to_tmem_w<1>(cw + 4 * s, dS + ((slot * F::kScales + 512 * s) >> 4));
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        if (i + b >= nb) break;
+        ok = wait_w(full + st, phase);
+        if (!ok) break;
+        tc::tc_fence_after();
+        const uint64_t dw = dW + (st * F::kStage >> 4), dx = dX + (st * F::kStage >> 4);
+#pragma unroll
+        for (int k = 0; k < kStageK / 32; ++k)
+          mma_e4m3_w<1>(tmem, dw + 2 * k, dx + 2 * k, idesc_e4m3(128, kRows) | scale_ids(b), cw, cw + 4, (b > 0 || k > 0) ? 1u : (uint32_t)i);
+        tc::mma_commit_w(empty + st);
+        if (++st == F::kStages) st = 0, phase ^= 1;
+      }
+      tc::mma_commit_w(sempty + slot);
+      cw = tmem + F::cScales + ((g + 1) & 1) * 4 * (1 + F::kSets);
     }
     tc::mma_commit_w(done);
   } else if (warp == 2) {
@@ -147,21 +154,26 @@ __global__ void __launch_bounds__(kThreads)
   if (split == 1) {
     if (ok) {
 #pragma unroll 1
-      for (int c = 0; c < kRows; c += 16) {
-        if (c >= rows) break;
+      for (int c = 0; c < rows; c += 16) {
         float v[16];
         tc::tmem_ld16(td + c, v);
+        if (n < N) {
+          if (c + 16 <= rows) {   // (a branch for each value costs 50 cycles)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (c + e < rows && n < N) o[(c + e) * ldo] = from_f32<T>(v[e]);
+            for (int e = 0; e < 16; ++e, o += ldo) *o = from_f32<T>(v[e]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 15; ++e, o += ldo)
+              if (c + e < rows) *o = from_f32<T>(v[e]);
+          }
+        }
       }
     }
   } else {
     float* part = reinterpret_cast<float*>(sm);   // [kRows][128]
     if (ok) {
 #pragma unroll 1
-      for (int c = 0; c < kRows; c += 16) {
-        if (c >= rows) break;
+      for (int c = 0; c < rows; c += 16) {
         float v[16];
         tc::tmem_ld16(td + c, v);
 #pragma unroll
@@ -170,30 +182,34 @@ __global__ void __launch_bounds__(kThreads)
     }
     tc::cluster_sync_all();
     if (ok) {
-      // this CTA's rows are rank, rank + split, ...: a warp takes a row at a time, a lane four columns
-      uint32_t peer[8];
-#pragma unroll
-      for (int s = 0; s < 8; ++s) peer[s] = s < split ? tc::mapa_shared(part + 4 * lane, s) : 0u;
+      // this CTA's rows are rank, rank + split, ...: a warp takes four at a time, a lane four columns of each
       const int64_t nl = n0 + 4 * lane;
       const int left = (int)(N - nl < 4 ? N - nl : 4);   // columns of this lane
-#pragma unroll 2
-      for (int r = rank + split * warp; r < rows; r += split * (kThreads / 32)) {
-        float4 x[8];
+      const uint32_t mine = tc::smem_u32(part + 4 * lane);
+      for (int r0 = rank + split * 4 * warp; r0 < rows; r0 += split * 4 * (kThreads / 32)) {
+        float4 x[4] = {};
+#pragma unroll 1
+        for (int s = 0; s < split; ++s) {   // in the order of K
+          const uint32_t from = cluster_address(mine, s);
+          float4 y[4];
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
-          if (s < split) x[s] = ld_cluster(peer[s] + r * 512);
-        float v[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
+          for (int j = 0; j < 4; ++j) y[j] = ld_cluster(from + min(r0 + split * j, rows - 1) * 512);
 #pragma unroll
-        for (int s = 1; s < 8; ++s)
-          if (s < split) v[0] += x[s].x, v[1] += x[s].y, v[2] += x[s].z, v[3] += x[s].w;
-        T* y = out + (m0 + r) * ldo + nl;
-        if (quads && left == 4) {
-          if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(y) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
-          else *reinterpret_cast<float4*>(y) = make_float4(v[0], v[1], v[2], v[3]);
-        } else {
+          for (int j = 0; j < 4; ++j) x[j].x += y[j].x, x[j].y += y[j].y, x[j].z += y[j].z, x[j].w += y[j].w;
+        }
+        T* y = out + (m0 + r0) * ldo + nl;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < left) y[i] = from_f32<T>(v[i]);
+        for (int j = 0; j < 4; ++j, y += split * ldo) {
+          if (r0 + split * j >= rows) break;
+          if (quads && left == 4) {
+            if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(y) = make_uint2(bf16x2(x[j].x, x[j].y), bf16x2(x[j].z, x[j].w));
+            else *reinterpret_cast<float4*>(y) = x[j];
+          } else {
+            if (left > 0) y[0] = from_f32<T>(x[j].x);
+            if (left > 1) y[1] = from_f32<T>(x[j].y);
+            if (left > 2) y[2] = from_f32<T>(x[j].z);
+            if (left > 3) y[3] = from_f32<T>(x[j].w);
+          }
         }
       }
     }

@@ -31,13 +31,6 @@ constexpr int kGroupM = 8;              // tiles are taken in bands of so many r
 static_assert(kAlloc <= 227 * 1024, "shared memory");
 
 // ------------------------------------------------------------- forms for a pair of CTAs
-__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          tc::smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
 // Arrival on an mbarrier of the cluster (address from mapa_shared), released at CTA scope: what it orders lies in
 // this CTA's own shared memory (behind a proxy fence) or TMEM.  (A release at cluster scope costs about 1,000 cycles.)
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
@@ -116,26 +109,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   bool ok = true;
 
   if (warp == 0) {
-    if (lane == 0) {
-      int64_t n = 0;   // stages so far
-      for (int64_t t = pair; t < tiles && ok; t += pairs) {
-        int64_t im, in;
-        place(t, tm, tn, im, in);
-        const int32_t ya = (int32_t)(im * kTM + 128 * rank), yb = (int32_t)(in * kTN + kTN / 2 * rank);
-        for (int32_t kb = 0; kb < blocks; ++kb, ++n) {
-          const int st = (int)(n % kStages);
-          if (n >= kStages && !(ok = tc::mbar_wait(empty + st, (uint32_t)(n / kStages - 1) & 1, kWaitLimit))) break;
-          const uint32_t bar = tc::mapa_shared(full + st, 0);
-          // the leading CTA expects both CTAs' bytes; the other's may come first, its arrival is what ends the phase
-          if (rank == 0) tc::mbar_arrive_expect_tx(full + st, 2 * kStage);
-          tma_load_pair(sm + st * kStage, &mapA, kb * kStageK, ya, bar);
-          tma_load_pair(sm + st * kStage + kA, &mapB, kb * kStageK, yb, bar);
-        }
+    const uint32_t at = tc::smem_u32(sm), lead = tc::mapa_shared(full, 0);
+    int st = 0;
+    uint32_t phase = 1;
+    int64_t n = 0;   // stages so far
+    for (int64_t t = pair; t < tiles && ok; t += pairs) {
+      int64_t im, in;
+      place(t, tm, tn, im, in);
+      const int32_t ya = (int32_t)(im * kTM + 128 * rank), yb = (int32_t)(in * kTN + kTN / 2 * rank);
+      for (int32_t kb = 0; kb < blocks; ++kb, ++n) {
+        if (n >= kStages && !(ok = wait_w(empty + st, phase))) break;
+        // the leading CTA expects both CTAs' bytes; the other's may come first, its arrival is what ends the phase
+        if (rank == 0) expect_w(tc::smem_u32(full + st), 2 * kStage);
+        tma_load_w<2>(at + st * kStage, &mapA, kb * kStageK, ya, lead + 8 * st);
+        tma_load_w<2>(at + st * kStage + kA, &mapB, kb * kStageK, yb, lead + 8 * st);
+        if (++st == kStages) st = 0, phase ^= 1;
       }
-      // end with no copy and no arrival in flight
-      for (int64_t i = n > kStages ? n - kStages : 0; i < n; ++i) ok = tc::mbar_wait(empty + i % kStages, (uint32_t)(i / kStages) & 1, kWaitLimit) && ok;
     }
-    __syncwarp();
+    // end with no copy and no arrival in flight
+    for (int64_t i = n > kStages ? n - kStages : 0; i < n; ++i) ok = wait_w(empty + i % kStages, (uint32_t)(i / kStages) & 1) && ok;
   } else if (warp == 1) {
     if (rank == 0) {
       const uint64_t dA = tc::desc_kmajor_sw128(tc::smem_u32(sm)), dB = tc::desc_kmajor_sw128(tc::smem_u32(sm + kA));

@@ -82,11 +82,38 @@ __device__ __forceinline__ void scales_to_tmem_w(uint32_t tmem, uint64_t desc) {
   }
 }
 
-// Wait of a whole warp; one lane asks.
+// Wait of a whole warp; every lane asks (a branch for one lane costs some 500 cycles before the warp is together again).
 __device__ __forceinline__ bool wait_w(uint64_t* bar, uint32_t parity) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = tc::mbar_wait(bar, parity, kWaitLimit);
-  return __all_sync(0xffffffffu, ok);
+  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, kWaitLimit));
+}
+
+// A tile's load, and an arrival that expects its bytes, by the elected lane (kGroup 2: `bar` may be the other CTA's,
+// an address of the cluster).
+template <int kGroup>
+__device__ __forceinline__ void tma_load_w(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
+  if constexpr (kGroup == 1) {
+    asm volatile(
+        "{\n\t.reg .pred pe;\n\t"
+        "elect.sync _|pe, 0xffffffff;\n\t"
+        "@pe cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred pe;\n\t"
+        "elect.sync _|pe, 0xffffffff;\n\t"
+        "@pe cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  }
+}
+__device__ __forceinline__ void expect_w(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred pe;\n\t"
+      "elect.sync _|pe, 0xffffffff;\n\t"
+      "@pe mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes)
+      : "memory");
 }
 
 constexpr int kScaleSlots = 4;   // groups of four K blocks whose scales are on their way (two of them in TMEM)

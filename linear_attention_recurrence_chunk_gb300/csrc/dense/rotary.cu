@@ -168,8 +168,10 @@ cudaError_t launch(const RotaryProblem& p, cudaStream_t stream) {
   const size_t smem = (size_t)s.half * 8 + (size_t)s.tokens * s.half * 8 + (size_t)s.tokens * 4;
   const dim3 grid((unsigned)((p.T + s.tokens - 1) / s.tokens), (unsigned)split);
   auto go = [&](auto kernel) -> cudaError_t {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 72 * 1024);
-    if (e != cudaSuccess) return e;
+    if (smem > 48 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 72 * 1024);
+      if (e != cudaSuccess) return e;
+    }
     kernel<<<grid, kThreads, smem, stream>>>(s);
     return cudaGetLastError();
   };

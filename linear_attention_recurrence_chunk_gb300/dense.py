@@ -26,13 +26,16 @@ from typing import Optional, Tuple
 
 import torch
 
-from .kv4 import _check, _device, _dtype, _run
+from .kv4 import _current_raw_stream, _run
 
 __all__ = ["kda_add_rmsnorm", "kda_add_rmsnorm_fp8", "kda_fp8_quant", "kda_fp8_values", "kda_fp8_matmul", "kda_rotary",
            "kda_rotary_freqs"]
 
-_BLOCK = 128        # columns (and weight rows) of a scale
-_E4M3 = torch.float8_e4m3fn
+_E4M3, _U8 = torch.float8_e4m3fn, torch.uint8
+_DT = {torch.float32: 0, torch.bfloat16: 1}
+_empty = torch.empty
+# The bare query: a call of these functions is mostly host time, and the tensors are CUDA tensors already.
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 _fns = None
 
@@ -55,6 +58,30 @@ def _lib():
     return _fns
 
 
+def _fail(status: int, where: str):
+    from . import KdaError
+    raise KdaError(status, where)
+
+
+def _device(name: str, t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: a CUDA tensor is expected")
+    return dev
+
+
+def _dtype(dt: torch.dtype) -> int:
+    code = _DT.get(dt)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dt} (float32 or bfloat16)")
+    return code
+
+
+def _e4m3(name: str, t: torch.Tensor):
+    if t.dtype is not _E4M3:
+        raise TypeError(f"{name}: {_E4M3} expected, got {t.dtype}")
+
+
 def _matrix(name: str, t: torch.Tensor, dev: int) -> Tuple[int, int, int]:
     """(rows, columns, row stride) of [rows, columns] with contiguous columns."""
     if t.dim() != 2 or t.get_device() != dev:
@@ -66,66 +93,66 @@ def _matrix(name: str, t: torch.Tensor, dev: int) -> Tuple[int, int, int]:
     return T, C, s if T > 1 else C   # a stride over one row has no meaning
 
 
-def _blocks(n: int) -> int:
-    return (n + _BLOCK - 1) // _BLOCK
-
-
 def _scales(name: str, t: torch.Tensor, rows: int, cols: int, dev: int) -> int:
-    if t.dtype is not torch.uint8:
+    if t.dtype is not _U8:
         raise TypeError(f"{name}: uint8 expected, got {t.dtype}")
     if t.get_device() != dev or not t.is_contiguous() or t.shape != (rows, cols):
         raise ValueError(f"{name}: a contiguous [{rows}, {cols}] tensor on cuda:{dev} expected, got {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
+def _block_rows(n: int):
+    if n != 1 and n != 128:
+        raise ValueError(f"block_rows: 1 or 128 expected, got {n}")
+
+
 def kda_fp8_quant(x: torch.Tensor, block_rows: int = 1, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """x ``[T, C]`` (any row stride) in 8 bits: codes ``[T, C]`` and a scale byte for each
     block of ``block_rows`` (1: activations, 128: weights) x 128 values."""
-    lib = _lib()
     dev = _device("x", x)
+    if stream is not None or dev != _current_device():
+        return _run(dev, stream, lambda _: kda_fp8_quant(x, block_rows))
     T, C, xs = _matrix("x", x, dev)
     dt = _dtype(x.dtype)
-    if block_rows not in (1, _BLOCK):
-        raise ValueError(f"block_rows: 1 or {_BLOCK} expected, got {block_rows}")
-
-    def call(st):
-        codes = x.new_empty((T, C), dtype=_E4M3)
-        scales = x.new_empty((T if block_rows == 1 else _blocks(T), _blocks(C)), dtype=torch.uint8)
-        _check(lib.kda_fp8_quant(x.data_ptr(), xs, T, C, block_rows, dt, codes.data_ptr(), scales.data_ptr(), st), "kda_fp8_quant")
-        return codes, scales
-
-    return _run(dev, stream, call)
+    _block_rows(block_rows)
+    codes = _empty((T, C), dtype=_E4M3, device=x.device)
+    scales = _empty((T if block_rows == 1 else (T + 127) // 128, (C + 127) // 128), dtype=_U8, device=x.device)
+    st = _lib().kda_fp8_quant(x.data_ptr(), xs, T, C, block_rows, dt, codes.data_ptr(), scales.data_ptr(), _current_raw_stream(dev))
+    if st:
+        _fail(st, "kda_fp8_quant")
+    return codes, scales
 
 
 def kda_fp8_values(codes: torch.Tensor, scales: torch.Tensor, block_rows: int = 1, dtype: torch.dtype = torch.bfloat16,
                    stream=None) -> torch.Tensor:
     """The values ``[T, C]`` of ``dtype`` that codes ``[T, C]`` (contiguous) and their scale
     bytes stand for."""
-    lib = _lib()
-    dev = _device("codes", codes, _E4M3)
+    _e4m3("codes", codes)
+    dev = _device("codes", codes)
+    if stream is not None or dev != _current_device():
+        return _run(dev, stream, lambda _: kda_fp8_values(codes, scales, block_rows, dtype))
     T, C, _ = _matrix("codes", codes, dev)
     if not codes.is_contiguous():
         raise ValueError("codes: a contiguous matrix is expected")
-    if block_rows not in (1, _BLOCK):
-        raise ValueError(f"block_rows: 1 or {_BLOCK} expected, got {block_rows}")
-    dt, sp = _dtype(dtype), _scales("scales", scales, T if block_rows == 1 else _blocks(T), _blocks(C), dev)
-
-    def call(st):
-        y = codes.new_empty((T, C), dtype=dtype)
-        _check(lib.kda_fp8_values(codes.data_ptr(), sp, T, C, block_rows, dt, y.data_ptr(), st), "kda_fp8_values")
-        return y
-
-    return _run(dev, stream, call)
+    _block_rows(block_rows)
+    dt, sp = _dtype(dtype), _scales("scales", scales, T if block_rows == 1 else (T + 127) // 128, (C + 127) // 128, dev)
+    y = _empty((T, C), dtype=dtype, device=codes.device)
+    st = _lib().kda_fp8_values(codes.data_ptr(), sp, T, C, block_rows, dt, y.data_ptr(), _current_raw_stream(dev))
+    if st:
+        _fail(st, "kda_fp8_values")
+    return y
 
 
 def _norm(x, residual, weight, eps, h, fp8, stream):
-    lib = _lib()
     dev = _device("x", x)
+    if stream is not None or dev != _current_device():
+        return _run(dev, stream, lambda _: _norm(x, residual, weight, eps, h, fp8, None))
     T, C, xs = _matrix("x", x, dev)
-    dt, rp, rs, wp = _dtype(x.dtype), None, 0, None
+    dtype = x.dtype
+    dt, rp, rs, wp, hp, device = _dtype(dtype), None, 0, None, None, x.device
     if residual is not None:
-        if residual.dtype is not x.dtype or residual.shape != x.shape:
-            raise ValueError(f"residual: {x.dtype} {tuple(x.shape)} expected, got {residual.dtype} {tuple(residual.shape)}")
+        if residual.dtype is not dtype or residual.shape != x.shape:
+            raise ValueError(f"residual: {dtype} {tuple(x.shape)} expected, got {residual.dtype} {tuple(residual.shape)}")
         rs, rp = _matrix("residual", residual, dev)[2], residual.data_ptr()
     if weight is not None:
         if weight.dtype is not torch.float32:
@@ -133,22 +160,23 @@ def _norm(x, residual, weight, eps, h, fp8, stream):
         if weight.shape != (C,) or weight.get_device() != dev or not weight.is_contiguous():
             raise ValueError(f"weight: a contiguous [{C}] tensor on cuda:{dev} expected, got {tuple(weight.shape)} on {weight.device}")
         wp = weight.data_ptr()
-    if h is not None and (residual is None or h.dtype is not x.dtype or h.shape != x.shape or not h.is_contiguous() or h.get_device() != dev):
-        raise ValueError("residual_out: a contiguous tensor of the residual's type, shape and device is expected")
-
-    def call(st):
-        out = x.new_empty((T, C)) if residual is not None and h is None else h
-        hp = None if out is None else out.data_ptr()
-        if fp8:
-            codes, scales = x.new_empty((T, C), dtype=_E4M3), x.new_empty((T, _blocks(C)), dtype=torch.uint8)
-            _check(lib.kda_add_rmsnorm(x.data_ptr(), xs, rp, rs, wp, eps, T, C, dt, hp, None, codes.data_ptr(), scales.data_ptr(), st),
-                   "kda_add_rmsnorm")
-            return codes, scales, out
-        y = x.new_empty((T, C))
-        _check(lib.kda_add_rmsnorm(x.data_ptr(), xs, rp, rs, wp, eps, T, C, dt, hp, y.data_ptr(), None, None, st), "kda_add_rmsnorm")
-        return y, out
-
-    return _run(dev, stream, call)
+    if h is not None:
+        if residual is None or h.dtype is not dtype or h.shape != x.shape or not h.is_contiguous() or h.get_device() != dev:
+            raise ValueError("residual_out: a contiguous tensor of the residual's type, shape and device is expected")
+        hp = h.data_ptr()
+    elif residual is not None:
+        h = _empty((T, C), dtype=dtype, device=device)
+        hp = h.data_ptr()
+    if fp8:
+        y, scales = _empty((T, C), dtype=_E4M3, device=device), _empty((T, (C + 127) // 128), dtype=_U8, device=device)
+        st = _lib().kda_add_rmsnorm(x.data_ptr(), xs, rp, rs, wp, eps, T, C, dt, hp, None, y.data_ptr(), scales.data_ptr(),
+                                    _current_raw_stream(dev))
+    else:
+        y, scales = _empty((T, C), dtype=dtype, device=device), None
+        st = _lib().kda_add_rmsnorm(x.data_ptr(), xs, rp, rs, wp, eps, T, C, dt, hp, y.data_ptr(), None, None, _current_raw_stream(dev))
+    if st:
+        _fail(st, "kda_add_rmsnorm")
+    return (y, scales, h) if fp8 else (y, h)
 
 
 def kda_add_rmsnorm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
@@ -171,29 +199,29 @@ def kda_fp8_matmul(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_s
                    dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """``a w^T``, ``[M, N]`` of ``dtype``: a ``[M, K]`` with scales ``[M, ceil(K / 128)]`` and w ``[N, K]``
     with scales ``[ceil(N / 128), ceil(K / 128)]``.  K and the row strides are multiples of 16;
-    ``out`` may have any row stride."""
-    lib = _lib()
-    dev = _device("a", a, _E4M3)
-    _device("w", w, _E4M3)
+    ``out`` (whose type counts then) may have any row stride."""
+    _e4m3("a", a)
+    _e4m3("w", w)
+    dev = _device("a", a)
+    if stream is not None or dev != _current_device():
+        return _run(dev, stream, lambda _: kda_fp8_matmul(a, a_scales, w, w_scales, dtype, out))
     M, K, lda = _matrix("a", a, dev)
     N, KW, ldw = _matrix("w", w, dev)
     if KW != K:
         raise ValueError(f"w: [N, {K}] expected, got {tuple(w.shape)}")
-    kb = _blocks(K)
-    sa, sw = _scales("a_scales", a_scales, M, kb, dev), _scales("w_scales", w_scales, _blocks(N), kb, dev)
-    if out is not None:
-        dtype = out.dtype
+    kb = (K + 127) // 128
+    sa, sw = _scales("a_scales", a_scales, M, kb, dev), _scales("w_scales", w_scales, (N + 127) // 128, kb, dev)
+    if out is None:
+        dt, ldo = _dtype(dtype), N
+        out = _empty((M, N), dtype=dtype, device=a.device)
+    else:
         if out.shape != (M, N):
             raise ValueError(f"out: [{M}, {N}] expected, got {tuple(out.shape)}")
-    dt = _dtype(dtype)
-    ldo = N if out is None else _matrix("out", out, dev)[2]
-
-    def call(st):
-        y = a.new_empty((M, N), dtype=dtype) if out is None else out
-        _check(lib.kda_fp8_matmul(a.data_ptr(), lda, sa, w.data_ptr(), ldw, sw, M, N, K, dt, y.data_ptr(), ldo, st), "kda_fp8_matmul")
-        return y
-
-    return _run(dev, stream, call)
+        dt, ldo = _dtype(out.dtype), _matrix("out", out, dev)[2]
+    st = _lib().kda_fp8_matmul(a.data_ptr(), lda, sa, w.data_ptr(), ldw, sw, M, N, K, dt, out.data_ptr(), ldo, _current_raw_stream(dev))
+    if st:
+        _fail(st, "kda_fp8_matmul")
+    return out
 
 
 def kda_rotary_freqs(rot: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
@@ -238,6 +266,14 @@ def _heads(name: str, t: torch.Tensor, T: int, dim: int, dev: int, dtype) -> Tup
     return ts, hs
 
 
+def _vector(name: str, t: torch.Tensor, n: int, dtype, dev: int) -> int:
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: {dtype} expected, got {t.dtype}")
+    if t.get_device() != dev or not t.is_contiguous() or t.shape != (n,):
+        raise ValueError(f"{name}: a contiguous [{n}] tensor on cuda:{dev} expected, got {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
 def kda_rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, freqs: torch.Tensor, amplitude: float = 1.0,
                interleaved: bool = False, inverse: bool = False, q_out: Optional[torch.Tensor] = None,
                k_out: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
@@ -246,40 +282,41 @@ def kda_rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tens
     freqs (fp64), in pairs (i, i + len(freqs)), or (2 i, 2 i + 1) when interleaved.  Tokens with a
     negative position stay as they are.  Returns ``(q_out, k_out)``, new tensors unless given;
     an output may be its input (in place)."""
-    lib = _lib()
     dev = _device("q", q)
-    dt = _dtype(q.dtype)
+    if stream is not None or dev != _current_device():
+        return _run(dev, stream, lambda _: kda_rotary(q, k, positions, freqs, amplitude, interleaved, inverse, q_out, k_out))
+    dtype = q.dtype
+    dt = _dtype(dtype)
     if q.dim() != 3:
         raise ValueError(f"q: [tokens, heads, channels] expected, got {tuple(q.shape)}")
     T, Hq, D = q.shape
-    qt, qh = _heads("q", q, T, D, dev, q.dtype)
-    Hk, kt, kh, kp = 0, 0, 0, None
+    qt, qh = _heads("q", q, T, D, dev, dtype)
+    n = freqs.numel()
+    pp, fp = _vector("positions", positions, T, torch.int32, dev), _vector("freqs", freqs, n, torch.float64, dev)
+    if q_out is None:
+        q_out = _empty((T, Hq, D), dtype=dtype, device=q.device)
+        qot, qoh = Hq * D, D
+    else:
+        qot, qoh = _heads("q_out", q_out, T, D, dev, dtype)
+        if q_out.shape[1] != Hq:
+            raise ValueError("q_out: q's shape is expected")
+    Hk = kt = kh = kot = koh = 0
+    kp = kop = None
     if k is not None:
-        kt, kh = _heads("k", k, T, D, dev, q.dtype)
+        kt, kh = _heads("k", k, T, D, dev, dtype)
         Hk, kp = k.shape[1], k.data_ptr()
+        if k_out is None:
+            k_out = _empty((T, Hk, D), dtype=dtype, device=q.device)
+            kot, koh = Hk * D, D
+        else:
+            kot, koh = _heads("k_out", k_out, T, D, dev, dtype)
+            if k_out.shape[1] != Hk:
+                raise ValueError("k_out: k's shape is expected")
+        kop = k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
-    if positions.dtype is not torch.int32:
-        raise TypeError(f"positions: torch.int32 expected, got {positions.dtype}")
-    if freqs.dtype is not torch.float64:
-        raise TypeError(f"freqs: torch.float64 expected, got {freqs.dtype}")
-    for name, t, n in (("positions", positions, T), ("freqs", freqs, freqs.numel())):
-        if t.get_device() != dev or not t.is_contiguous() or t.shape != (n,):
-            raise ValueError(f"{name}: a contiguous [{n}] tensor on cuda:{dev} expected, got {tuple(t.shape)} on {t.device}")
-    rot, flags = 2 * freqs.numel(), (1 if interleaved else 0) | (2 if inverse else 0)
-    qo = None if q_out is None else _heads("q_out", q_out, T, D, dev, q.dtype)
-    ko = None if k_out is None else _heads("k_out", k_out, T, D, dev, q.dtype)
-    if (q_out is not None and q_out.shape != q.shape) or (k_out is not None and k_out.shape != k.shape):
-        raise ValueError("an output has its input's shape")
-
-    def call(st):
-        yq, yk, (qot, qoh), (kot, koh) = q_out, k_out, qo or (Hq * D, D), ko or (Hk * D, D)
-        if yq is None:
-            yq = q.new_empty((T, Hq, D))
-        if yk is None and k is not None:
-            yk = q.new_empty((T, Hk, D))
-        _check(lib.kda_rotary(q.data_ptr(), qt, qh, Hq, kp, kt, kh, Hk, positions.data_ptr(), T, D, rot, freqs.data_ptr(), amplitude, flags,
-                              dt, yq.data_ptr(), qot, qoh, None if yk is None else yk.data_ptr(), kot, koh, st), "kda_rotary")
-        return yq, yk
-
-    return _run(dev, stream, call)
+    st = _lib().kda_rotary(q.data_ptr(), qt, qh, Hq, kp, kt, kh, Hk, pp, T, D, 2 * n, fp, amplitude, (1 if interleaved else 0) | (2 if inverse else 0),
+                           dt, q_out.data_ptr(), qot, qoh, kop, kot, koh, _current_raw_stream(dev))
+    if st:
+        _fail(st, "kda_rotary")
+    return q_out, k_out
