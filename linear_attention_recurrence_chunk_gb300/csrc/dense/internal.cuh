@@ -46,33 +46,26 @@ __device__ __forceinline__ int column(int lane, int i) {
   return kWide ? 8 * lane + i : lane + 32 * i;
 }
 
+// The eight values as they lie in memory (zeros behind C), and as fp32.
 template <typename T, bool kWide>
-__device__ __forceinline__ void load8(const T* row, int64_t c0, int64_t C, int lane, float (&v)[8]) {
-  if constexpr (kWide) {
-    const int64_t c = c0 + 8 * lane;
-    if (c >= C) {
+struct Eight {
+  alignas(kWide ? 16 : sizeof(T)) T x[8];
+  __device__ __forceinline__ void load(const T* row, int64_t c0, int64_t C, int lane) {
+    if constexpr (kWide) {
+      const int64_t c = c0 + 8 * lane;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    } else if constexpr (sizeof(T) == 2) {
-      const uint4 u = __ldcs(reinterpret_cast<const uint4*>(row + c));
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+        reinterpret_cast<uint4*>(x)[i] = c < C ? __ldcs(reinterpret_cast<const uint4*>(row + c) + i) : make_uint4(0, 0, 0, 0);
     } else {
-      const float4 a = __ldcs(reinterpret_cast<const float4*>(row + c)), b = __ldcs(reinterpret_cast<const float4*>(row + c) + 1);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    }
-  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t c = c0 + lane + 32 * i;
-      v[i] = c < C ? to_f32<T>(row[c]) : 0.f;
+      for (int i = 0; i < 8; ++i) {
+        const int64_t c = c0 + lane + 32 * i;
+        x[i] = c < C ? row[c] : from_f32<T>(0.f);
+      }
     }
   }
-}
+  __device__ __forceinline__ float at(int i) const { return to_f32<T>(x[i]); }
+};
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 z = __floats2bfloat162_rn(lo, hi);
@@ -99,22 +92,44 @@ __device__ __forceinline__ void store8(T* row, int64_t c0, int64_t C, int lane, 
   }
 }
 
-__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+// Largest size of three or two values, a NaN above all.
+__device__ __forceinline__ float top3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
+  return d;
+}
+__device__ __forceinline__ float top2(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return d;
+}
 
-// Largest |value| bits of each lane's block or blocks: `a` of values 0 .. 3, `b` of 4 .. 7
-// (kWide: the same block).
+// The fp32 bits of the largest size of each lane's block or blocks: `a` of values 0 .. 3, `b` of 4 .. 7
+// (kWide: the same block, of 16 lanes).
+__device__ __forceinline__ uint32_t half_warp_max(uint32_t t) {
+#pragma unroll
+  for (int m = 8; m > 0; m >>= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, m));
+  return t;
+}
 template <bool kWide>
 __device__ __forceinline__ void block_tops(const float (&v)[8], uint32_t& a, uint32_t& b) {
-  a = max(max(magnitude(v[0]), magnitude(v[1])), max(magnitude(v[2]), magnitude(v[3])));
-  b = max(max(magnitude(v[4]), magnitude(v[5])), max(magnitude(v[6]), magnitude(v[7])));
+  const float lo = top2(v[3], top3(v[0], v[1], v[2])), hi = top2(v[7], top3(v[4], v[5], v[6]));
   if constexpr (kWide) {
-    a = max(a, b);
-#pragma unroll
-    for (int m = 8; m > 0; m >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, m));
-    b = a;
+    a = b = half_warp_max(__float_as_uint(top2(lo, hi)));
   } else {
-    a = __reduce_max_sync(0xffffffffu, a);
-    b = __reduce_max_sync(0xffffffffu, b);
+    a = __reduce_max_sync(0xffffffffu, __float_as_uint(lo));
+    b = __reduce_max_sync(0xffffffffu, __float_as_uint(hi));
+  }
+}
+// The lane's own largest size.
+template <typename T, bool kWide>
+__device__ __forceinline__ uint32_t lane_top(const Eight<T, kWide>& v) {
+  if constexpr (sizeof(T) == 2 && kWide) {   // two values a word: sizes compare as whole numbers
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(v.x);
+    const uint32_t m = 0x7fff7fffu, t = __vmaxu2(__vmaxu2(w[0] & m, w[1] & m), __vmaxu2(w[2] & m, w[3] & m));
+    return max(t << 16, t & 0xffff0000u);
+  } else {
+    return __float_as_uint(top3(top3(v.at(0), v.at(1), v.at(2)), top3(v.at(3), v.at(4), v.at(5)), top2(v.at(6), v.at(7))));
   }
 }
 
@@ -127,6 +142,30 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], uint32_t byte_a, ui
   if (byte_a == 255u) w.x = 0;
   if (byte_b == 255u) w.y = 0;
   return w;
+}
+template <typename T, bool kWide>
+__device__ __forceinline__ uint2 codes8(const Eight<T, kWide>& v, uint32_t byte) {
+  float f[8];
+  if constexpr (sizeof(T) == 2 && kWide) {
+    // scaled in bf16: exact but below 2^-126, where every code is 0
+    const __nv_bfloat16 i1 = __float2bfloat16_rn(scale_inverse(byte));
+    const __nv_bfloat162 i2 = __halves2bfloat162(i1, i1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 z = __hmul2(reinterpret_cast<const __nv_bfloat162*>(v.x)[i], i2);
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(&z);
+      f[2 * i] = __uint_as_float(w << 16);
+      f[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
+    }
+    uint2 w;
+    w.x = e4m3x2(f[0], f[1]) | e4m3x2(f[2], f[3]) << 16;
+    w.y = e4m3x2(f[4], f[5]) | e4m3x2(f[6], f[7]) << 16;
+    return byte == 255u ? make_uint2(0, 0) : w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = v.at(i);
+    return codes8(f, byte, byte);
+  }
 }
 
 template <bool kWide>

@@ -44,18 +44,21 @@ __global__ void __launch_bounds__(kOneWarp ? 32 * kRowsPerBlock : 1024)
   const int64_t row = kOneWarp ? (int64_t)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 5) : blockIdx.x;
   if (kOneWarp && row >= rows) return;
   float v[J][8];
-#pragma unroll
-  for (int j = 0; j < J; ++j) load8<T, kWide>(x + row * xs, 256 * (int64_t)(warp + W * j), C, lane, v[j]);
-  if constexpr (kAdd) {
-    float u[J][8];
-#pragma unroll
-    for (int j = 0; j < J; ++j) load8<T, kWide>(r + row * rs, 256 * (int64_t)(warp + W * j), C, lane, u[j]);
+  {
+    Eight<T, kWide> a[J], b[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] += u[j][i];
-      store8<T, kWide>(h + row * C, 256 * (int64_t)(warp + W * j), C, lane, v[j]);
+      a[j].load(x + row * xs, 256 * (int64_t)(warp + W * j), C, lane);
+      if constexpr (kAdd) b[j].load(r + row * rs, 256 * (int64_t)(warp + W * j), C, lane);
     }
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j][i] = kAdd ? a[j].at(i) + b[j].at(i) : a[j].at(i);
+  }
+  if constexpr (kAdd) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) store8<T, kWide>(h + row * C, 256 * (int64_t)(warp + W * j), C, lane, v[j]);
   }
   auto squares = [&]() {
     float s = 0.f;
@@ -144,9 +147,11 @@ cudaError_t launch1(const NormProblem& p, cudaStream_t stream) {
   const bool wide = p.C % 8 == 0 && p.xs % step == 0 && at(p.x, 16) && (!p.r || (p.rs % step == 0 && at(p.r, 16) && at(p.h, 16))) &&
                     at(p.w, 16) && (p.codes ? at(p.codes, 8) : at(p.y, 16));
   const int chunks = (int)((p.C + 255) / 256);   // 256 columns each, at most 128
-  // One or two chunks: a warp a row.  Else two chunks a warp up to 64 of them (32 warps), then four.
+  // One or two chunks: a warp a row.  Else two a warp, four where 32 warps are not enough and for 8-bit output of
+  // many rows (32,768 x 4,096: 157 us with two, 143 with four; 16,384 x 8,192: 182 and 147; but 1 x 4,096: 3.0 and
+  // 3.6, 256 x 8,192: 5.5 and 5.9; in the input's type the two differ by 1 %).
   if (chunks <= 1) return wide ? launch2<T, 1, true>(p, 1, stream) : launch2<T, 1, false>(p, 1, stream);
-  const int J = chunks <= 64 ? 2 : 4, warps = (chunks + J - 1) / J;
+  const int J = chunks > 64 || (p.codes && chunks > 8 && p.T >= 1024) ? 4 : 2, warps = (chunks + J - 1) / J;
   if (J == 2) return wide ? launch2<T, 2, true>(p, warps, stream) : launch2<T, 2, false>(p, warps, stream);
   return wide ? launch2<T, 4, true>(p, warps, stream) : launch2<T, 4, false>(p, warps, stream);
 }

@@ -3,79 +3,161 @@
 //   e = least e >= -126 with max |x| <= 448 * 2^e over a block,  code = E4M3(x * 2^-e),  value = code * 2^e
 //
 // Both scalings are exact and the hardware's conversion rounds once, so that the result is
-// defined bit by bit.  Bound: HBM.  Blocks of 1 x 128: a warp takes 4 x 256 columns of a row, all loads
-// first.  Blocks of 128 x 128: a CTA holds one in registers between its maximum and its codes.
+// defined bit by bit.  Bound: HBM.  Blocks of 1 x 128: half a warp has a block (eight values a lane; any
+// alignment: a warp, four values a lane), four of them at once, whatever rows they lie in.  Blocks of 128 x 128: a CTA
+// holds one in registers between its maximum and its codes.
 #include "internal.cuh"
 
 namespace kda {
 namespace dense {
 namespace {
 
-constexpr int kJ = 4;          // 256-column chunks of a warp
-constexpr int kWarps = 4;
+constexpr int kJ = 4;          // blocks of 1 x 128 of half a warp (kWide) or twice as many of a warp
+constexpr int kWarps = 4, kSquareThreads = 512;
+
+// Where the blocks of a warp lie: block i of its kBlocks follows on block i - 1, row after row.
+template <bool kWide>
+struct Walk {
+  static constexpr int kBlocks = 2 * kJ;
+  int64_t row0, C;
+  uint32_t b0, per_row, magic;
+  __device__ __forceinline__ Walk(int64_t C_, uint32_t per_row_, uint32_t magic_) : C(C_), per_row(per_row_), magic(magic_) {
+    const int64_t first = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * kBlocks;
+    row0 = first / per_row;
+    b0 = (uint32_t)(first - row0 * per_row);
+  }
+  __device__ __forceinline__ void at(uint32_t i, int64_t& row, int64_t& c) const {
+    const uint32_t b = b0 + i, down = magic ? __umulhi(b, magic) : per_row == 1 ? b : b / per_row;
+    row = row0 + down;
+    c = (int64_t)(b - down * per_row) * kBlock;
+  }
+};
+// ceil(2^32 / d) where n / d = n magic >> 32 for every n < d + 2^8; else 0.
+uint32_t walk_magic(int64_t d) { return d > 1 && d < 60000 ? (uint32_t)((0x100000000ull + d - 1) / d) : 0u; }
 
 template <typename T, bool kWide>
 __global__ void __launch_bounds__(32 * kWarps)
-    fp8_quant_kernel(const T* __restrict__ x, int64_t xs, int64_t rows, int64_t C, int64_t per_row, uint8_t* codes, uint8_t* scales) {
+    fp8_quant_kernel(const T* __restrict__ x, int64_t xs, int64_t rows, int64_t C, uint32_t per_row, uint32_t magic, uint8_t* codes, uint8_t* scales) {
+  const Walk<kWide> walk(C, per_row, magic);
   const int lane = threadIdx.x & 31;
-  const int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), row = task / per_row;
-  if (row >= rows) return;
-  const int64_t c0 = (task - row * per_row) * (256 * kJ);
-  float v[kJ][8];
+  if constexpr (kWide) {
+    Eight<T, true> v[kJ];
+    // one block's place after another, or (all in one row) 256 columns on each time
+    const bool whole = walk.b0 + walk.kBlocks <= per_row;
+    int64_t row, c;
+    walk.at(lane >> 4, row, c);
+    if (whole) {
+      if (row >= rows) return;
+      const T* from = x + row * xs;
 #pragma unroll
-  for (int j = 0; j < kJ; ++j) load8<T, kWide>(x + row * xs, c0 + 256 * j, C, lane, v[j]);
-#pragma unroll
-  for (int j = 0; j < kJ; ++j)
-    if (c0 + 256 * j < C)
-      store_fp8<kWide>(codes + row * C, scales + row * ((C + kBlock - 1) / kBlock), c0 + 256 * j, C, lane, v[j]);
-}
-
-// A block of 128 x 128: 256 threads, half a warp's 16 lanes a row of 128 columns, 8 values each, 8 rows a
-// thread (kWide); else a warp a row, 4 values a lane, 16 rows.
-template <typename T, bool kWide>
-__global__ void __launch_bounds__(256)
-    fp8_quant_square_kernel(const T* __restrict__ x, int64_t xs, int64_t rows, int64_t C, uint8_t* codes, uint8_t* scales) {
-  __shared__ uint32_t part[8];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t blocks = (C + kBlock - 1) / kBlock, br = blockIdx.x / blocks, bc = blockIdx.x - br * blocks;
-  const int64_t r0 = br * kBlock, c0 = bc * kBlock;
-  float v[8][8];
-  uint32_t top = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if constexpr (kWide) {
-      // load8's lane stands for 8 columns: 16 lanes of two rows
-      const int64_t row = r0 + 16 * j + 2 * warp + (lane >> 4);
-      const bool in = row < rows;
-      load8<T, true>(x + (in ? row : r0) * xs, c0, in ? C : 0, lane & 15, v[j]);
+      for (int j = 0; j < kJ; ++j) v[j].load(from, c + 256 * j, C, lane & 15);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t row = r0 + 16 * j + 2 * warp + (i >> 2), c = c0 + lane + 32 * (i & 3);
-        v[j][i] = row < rows && c < C ? to_f32<T>(x[row * xs + c]) : 0.f;
+      for (int j = 0; j < kJ; ++j) {
+        walk.at(2 * j + (lane >> 4), row, c);
+        v[j].load(x + (row < rows ? row : 0) * xs, c, row < rows ? C : 0, lane & 15);
+      }
+      walk.at(lane >> 4, row, c);
+    }
+    uint8_t* to = codes + row * C + c;
+    uint8_t* sc = scales + row * per_row + c / kBlock;
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+      const uint32_t byte = scale_byte(half_warp_max(lane_top(v[j])));
+      const uint2 w = codes8(v[j], byte);
+      if (whole) {
+        store_codes<true>(to + 256 * j, 0, C - c - 256 * j, lane & 15, w);
+        if ((lane & 15) == 0) sc[2 * j] = (uint8_t)byte;
+      } else {
+        walk.at(2 * j + (lane >> 4), row, c);
+        if (row < rows) {
+          store_codes<true>(codes + row * C, c, C, lane & 15, w);
+          if ((lane & 15) == 0) scales[row * per_row + c / kBlock] = (uint8_t)byte;
+        }
       }
     }
+  } else {
+    T v[2 * kJ][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, magnitude(v[j][i]));
-  }
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (lane == 0) part[warp] = top;
-  __syncthreads();
-  top = __reduce_max_sync(0xffffffffu, part[lane & 7]);
-  const uint32_t byte = scale_byte(top);
-  if (threadIdx.x == 0) scales[br * blocks + bc] = (uint8_t)byte;
+    for (int j = 0; j < 2 * kJ; ++j) {
+      int64_t row, c;
+      walk.at(j, row, c);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint2 w = codes8(v[j], byte, byte);
-    if constexpr (kWide) {
-      const int64_t row = r0 + 16 * j + 2 * warp + (lane >> 4);
-      if (row < rows) store_codes<true>(codes + row * C, c0, C, lane & 15, w);
-    } else {
+      for (int i = 0; i < 4; ++i) v[j][i] = row < rows && c + lane + 32 * i < C ? x[row * xs + c + lane + 32 * i] : from_f32<T>(0.f);
+    }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t row = r0 + 16 * j + 2 * warp + (i >> 2), c = c0 + lane + 32 * (i & 3);
-        if (row < rows && c < C) codes[row * C + c] = (uint8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+    for (int j = 0; j < kJ; ++j) {   // two blocks at a time
+      float f[8];
+      uint32_t a, b;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = to_f32<T>(v[2 * j + (i >> 2)][i & 3]);
+      block_tops<false>(f, a, b);
+      const uint32_t byte[2] = {scale_byte(a), scale_byte(b)};
+      const uint2 w = codes8(f, byte[0], byte[1]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        int64_t row, c;
+        walk.at(2 * j + k, row, c);
+        if (row >= rows) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c + lane + 32 * i < C) codes[row * C + c + lane + 32 * i] = (uint8_t)((k ? w.y : w.x) >> (8 * i));
+        if (lane == 0) scales[row * per_row + c / kBlock] = (uint8_t)byte[k];
       }
+    }
+  }
+}
+
+// Two blocks of 128 x 128 side by side (whole lines of 512 bytes of bf16 from each row: 256 each took 81 us for
+// 32,768 x 4,096): 16 warps, each with 256 columns of 8 rows.
+template <typename T, bool kWide>
+__global__ void __launch_bounds__(kSquareThreads)
+    fp8_quant_square_kernel(const T* __restrict__ x, int64_t xs, int64_t rows, int64_t C, uint8_t* codes, uint8_t* scales) {
+  constexpr int W = kSquareThreads / 32, kRows = kBlock / W;
+  __shared__ uint32_t part[2][W];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t pairs = (C + 2 * kBlock - 1) / (2 * kBlock), br = blockIdx.x / pairs, bc = blockIdx.x - br * pairs;
+  const int64_t r0 = br * kBlock + warp, c0 = bc * 2 * kBlock;
+  Eight<T, kWide> v[kRows];
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    const int64_t row = r0 + W * j;
+    v[j].load(x + (row < rows ? row : 0) * xs, c0, row < rows ? C : 0, lane);
+  }
+  uint32_t top[2] = {0, 0};
+  if constexpr (kWide) {
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) top[0] = max(top[0], lane_top(v[j]));
+    top[0] = half_warp_max(top[0]);   // of the lane's block
+    if ((lane & 15) == 0) part[lane >> 4][warp] = top[0];
+  } else {
+#pragma unroll
+    for (int j = 0; j < kRows; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top[i >> 2] = max(top[i >> 2], __float_as_uint(top2(v[j].at(i), 0.f)));
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      top[k] = __reduce_max_sync(0xffffffffu, top[k]);
+      if (lane == 0) part[k][warp] = top[k];
+    }
+  }
+  __syncthreads();
+  uint32_t byte[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) byte[k] = scale_byte(__reduce_max_sync(0xffffffffu, part[k][lane & (W - 1)]));
+  if (threadIdx.x < 2 && c0 + kBlock * threadIdx.x < C)
+    scales[br * ((C + kBlock - 1) / kBlock) + c0 / kBlock + threadIdx.x] = (uint8_t)(threadIdx.x ? byte[1] : byte[0]);
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    const int64_t row = r0 + W * j;
+    if (row >= rows) break;
+    if constexpr (kWide) {
+      store_codes<true>(codes + row * C, c0, C, lane, codes8(v[j], lane < 16 ? byte[0] : byte[1]));
+    } else {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = v[j].at(i);
+      store_codes<false>(codes + row * C, c0, C, lane, codes8(f, byte[0], byte[1]));
     }
   }
 }
@@ -83,44 +165,48 @@ __global__ void __launch_bounds__(256)
 template <typename T, bool kWide>
 __global__ void __launch_bounds__(32 * kWarps)
     fp8_values_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows, int64_t C, int32_t block_rows,
-                      int64_t per_row, T* y) {
+                      uint32_t per_row, uint32_t magic, T* y) {
+  const Walk<kWide> walk(C, per_row, magic);
   const int lane = threadIdx.x & 31;
-  const int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), row = task / per_row;
-  if (row >= rows) return;
-  const int64_t c0 = (task - row * per_row) * (256 * kJ);
-  const uint8_t* in = codes + row * C;
-  const uint8_t* sc = scales + (block_rows == 1 ? row : row / kBlock) * ((C + kBlock - 1) / kBlock);
-  uint2 w[kJ];
-  uint32_t s[kJ][2];
+  constexpr int kN = kWide ? kJ : 2 * kJ, kPer = kWide ? 2 : 1;   // blocks of a lane; half a warp or a warp each
+  const int sub = kWide ? lane >> 4 : 0;
+  uint2 w[kN];
+  uint32_t s[kN];
 #pragma unroll
-  for (int j = 0; j < kJ; ++j) {
-    const int64_t c = c0 + 256 * j;
+  for (int j = 0; j < kN; ++j) {
+    int64_t row, c;
+    walk.at(kPer * j + sub, row, c);
     w[j] = make_uint2(0, 0);
+    s[j] = row < rows ? scales[(block_rows == 1 ? row : row / kBlock) * per_row + c / kBlock] : 127u;
     if constexpr (kWide) {
-      const bool in_row = c + 8 * lane < C;
-      if (in_row) w[j] = __ldcs(reinterpret_cast<const uint2*>(in + c) + lane);
-      s[j][0] = s[j][1] = in_row ? sc[(c + 8 * lane) / kBlock] : 127u;
+      c += 8 * (lane & 15);
+      if (row < rows && c < C) w[j] = __ldcs(reinterpret_cast<const uint2*>(codes + row * C + c));
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t b = c + lane + 32 * i < C ? in[c + lane + 32 * i] : 0u;
-        (i < 4 ? w[j].x : w[j].y) |= b << (8 * (i & 3));
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) s[j][i] = c + kBlock * i < C ? sc[c / kBlock + i] : 127u;
+      for (int i = 0; i < 4; ++i)
+        if (row < rows && c + lane + 32 * i < C) w[j].x |= (uint32_t)codes[row * C + c + lane + 32 * i] << (8 * i);
     }
   }
 #pragma unroll
-  for (int j = 0; j < kJ; ++j) {
+  for (int j = 0; j < kN; ++j) {
+    int64_t row, c;
+    walk.at(kPer * j + sub, row, c);
+    if (row >= rows) continue;
+    const float f = scale_value(s[j]);
     float v[8];
-    const float a = scale_value(s[j][0]), b = scale_value(s[j][1]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < (kWide ? 4 : 2); ++i) {
       const float2 z = e4m3x2_values((i < 2 ? w[j].x : w[j].y) >> (16 * (i & 1)) & 0xffffu);
-      v[2 * i] = z.x * (i < 2 ? a : b);
-      v[2 * i + 1] = z.y * (i < 2 ? a : b);
+      v[2 * i] = z.x * f;
+      v[2 * i + 1] = z.y * f;
     }
-    store8<T, kWide>(y + row * C, c0 + 256 * j, C, lane, v);
+    if constexpr (kWide) {
+      store8<T, true>(y + row * C, c, C, lane & 15, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + lane + 32 * i < C) y[row * C + c + lane + 32 * i] = from_f32<T>(v[i]);
+    }
   }
 }
 
@@ -132,14 +218,14 @@ cudaError_t quant(const QuantProblem& p, cudaStream_t stream) {
   const T* x = static_cast<const T*>(p.x);
   prof_begin(stream, "fp8_quant_kernel");
   if (p.rows == 1) {
-    const int64_t per_row = (p.C + 256 * kJ - 1) / (256 * kJ);
-    const unsigned grid = (unsigned)((p.T * per_row + kWarps - 1) / kWarps);
-    if (wide) fp8_quant_kernel<T, true><<<grid, 32 * kWarps, 0, stream>>>(x, p.stride, p.T, p.C, per_row, p.codes, p.scales);
-    else fp8_quant_kernel<T, false><<<grid, 32 * kWarps, 0, stream>>>(x, p.stride, p.T, p.C, per_row, p.codes, p.scales);
+    const uint32_t per_row = (uint32_t)((p.C + kBlock - 1) / kBlock), magic = walk_magic(per_row);
+    const unsigned grid = (unsigned)((p.T * per_row + 2 * kJ * kWarps - 1) / (2 * kJ * kWarps));
+    if (wide) fp8_quant_kernel<T, true><<<grid, 32 * kWarps, 0, stream>>>(x, p.stride, p.T, p.C, per_row, magic, p.codes, p.scales);
+    else fp8_quant_kernel<T, false><<<grid, 32 * kWarps, 0, stream>>>(x, p.stride, p.T, p.C, per_row, magic, p.codes, p.scales);
   } else {
-    const unsigned grid = (unsigned)(((p.T + kBlock - 1) / kBlock) * ((p.C + kBlock - 1) / kBlock));
-    if (wide) fp8_quant_square_kernel<T, true><<<grid, 256, 0, stream>>>(x, p.stride, p.T, p.C, p.codes, p.scales);
-    else fp8_quant_square_kernel<T, false><<<grid, 256, 0, stream>>>(x, p.stride, p.T, p.C, p.codes, p.scales);
+    const unsigned grid = (unsigned)(((p.T + kBlock - 1) / kBlock) * ((p.C + 2 * kBlock - 1) / (2 * kBlock)));
+    if (wide) fp8_quant_square_kernel<T, true><<<grid, kSquareThreads, 0, stream>>>(x, p.stride, p.T, p.C, p.codes, p.scales);
+    else fp8_quant_square_kernel<T, false><<<grid, kSquareThreads, 0, stream>>>(x, p.stride, p.T, p.C, p.codes, p.scales);
   }
   prof_end(stream);
   return cudaGetLastError();
@@ -148,11 +234,11 @@ cudaError_t quant(const QuantProblem& p, cudaStream_t stream) {
 template <typename T>
 cudaError_t values(const ValuesProblem& p, cudaStream_t stream) {
   const bool wide = p.C % 8 == 0 && at(p.codes, 8) && at(p.y, 16);
-  const int64_t per_row = (p.C + 256 * kJ - 1) / (256 * kJ);
-  const unsigned grid = (unsigned)((p.T * per_row + kWarps - 1) / kWarps);
+  const uint32_t per_row = (uint32_t)((p.C + kBlock - 1) / kBlock), magic = walk_magic(per_row);
+  const unsigned grid = (unsigned)((p.T * per_row + 2 * kJ * kWarps - 1) / (2 * kJ * kWarps));
   prof_begin(stream, "fp8_values_kernel");
-  if (wide) fp8_values_kernel<T, true><<<grid, 32 * kWarps, 0, stream>>>(p.codes, p.scales, p.T, p.C, p.rows, per_row, static_cast<T*>(p.y));
-  else fp8_values_kernel<T, false><<<grid, 32 * kWarps, 0, stream>>>(p.codes, p.scales, p.T, p.C, p.rows, per_row, static_cast<T*>(p.y));
+  if (wide) fp8_values_kernel<T, true><<<grid, 32 * kWarps, 0, stream>>>(p.codes, p.scales, p.T, p.C, p.rows, per_row, magic, static_cast<T*>(p.y));
+  else fp8_values_kernel<T, false><<<grid, 32 * kWarps, 0, stream>>>(p.codes, p.scales, p.T, p.C, p.rows, per_row, magic, static_cast<T*>(p.y));
   prof_end(stream);
   return cudaGetLastError();
 }

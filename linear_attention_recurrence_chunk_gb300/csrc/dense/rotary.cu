@@ -7,10 +7,12 @@
 // modulo 2^64 is the fraction of a turn to p 2^-63, with no reduction and no table.  The top 32 bits, signed,
 // are half turns in [-1, 1) for sincospi.
 //
-// Bound: HBM, each value read and written once.  A block takes a few tokens: their cosines and sines
-// once into shared memory, then all heads of queries and keys, eight pairs (two 16-byte loads of bf16) a
-// thread and four such items on their way at once.
+// Bound: HBM, each value read and written once.  A warp takes a token at a time (a part of its heads when there are
+// few tokens): the first loads go out, then the token's cosines and sines into the warp's shared memory, each once,
+// then all heads of queries and keys, eight pairs (two 16-byte loads of bf16) a lane and three such items on their
+// way at once.
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.cuh"
 
@@ -18,7 +20,7 @@ namespace kda {
 namespace dense {
 namespace {
 
-constexpr int kThreads = 256, kItems = 4;
+constexpr int kWarps = 8, kItems = 3;
 
 // n / d for n d < 2^32, m = ceil(2^32 / d) (d = 1: m = 0).
 __device__ __forceinline__ uint32_t divide(uint32_t n, uint32_t m) { return m ? __umulhi(n, m) : n; }
@@ -36,10 +38,10 @@ struct Shape {
   int64_t T;
   int32_t D, rot, half;   // half = rot / 2 pairs
   float amplitude;
-  int32_t tokens;         // of a block
-  int32_t heads;          // of a block (blockIdx.y)
-  int32_t parts, turned;  // items of a head: of pairs, then of channels that stay
-  uint32_t m_heads, m_parts;
+  int32_t split, heads;   // warps of a token, heads of each
+  int32_t tokens;         // of a warp at a time (1 where split > 1)
+  int32_t parts, turned;  // items of a head: of pairs first, then of channels that stay
+  uint32_t m_parts, m_token;
 };
 
 // kE consecutive values of one side of kE pairs.
@@ -64,85 +66,112 @@ struct Values {
   }
 };
 
-template <typename T, int kE, bool kNext, bool kInverse>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const Shape s) {
+// kMany: several tokens a warp at a time (or whatever the sizes ask for); else one, or a part of its heads.
+template <typename T, int kE, bool kNext, bool kInverse, bool kMany>
+__global__ void __launch_bounds__(32 * kWarps, 2) rotary_kernel(const Shape s) {
   extern __shared__ uint64_t sm[];
-  uint64_t* turn = sm;                                          // [half] turns per position, 2^-64 each
-  float2* cs = reinterpret_cast<float2*>(turn + s.half);        // [tokens][half]
-  int32_t* pos = reinterpret_cast<int32_t*>(cs + s.tokens * s.half);
-  const int64_t t0 = (int64_t)blockIdx.x * s.tokens;
-  const int nt = (int)(s.T - t0 < s.tokens ? s.T - t0 : s.tokens);
-  const int H = s.q.H + s.k.H, h0 = blockIdx.y * s.heads, nh = H - h0 < s.heads ? H - h0 : s.heads;
-  const int tid = threadIdx.x;
-  for (int i = tid; i < s.half; i += kThreads) {
+  uint64_t* turn = sm;   // [half] turns per position, 2^-64 each
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // its tokens' (cos, sin), of each kE / 2 blocks of [turned][2 pairs] (kE = 1: [half]): lanes of neighbouring parts read neighbouring banks
+  float2* cs = reinterpret_cast<float2*>(turn + s.half) + (size_t)warp * s.tokens * s.half;
+  for (int i = threadIdx.x; i < s.half; i += 32 * kWarps) {
     // freq / (2 pi) as a rounded product and what it lacks: 1 / (2 pi) = kHi + kLo to 2^-110
     constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
     const double w = s.freqs[i], f = w * kHi, low = fma(w, kHi, -f) + w * kLo;
     turn[i] = fraction(f) + fraction(low);
   }
-  for (int i = tid; i < nt; i += kThreads) pos[i] = s.pos[t0 + i];
   __syncthreads();
-  for (int i = tid; i < nt * s.half; i += kThreads) {
-    const int t = i / s.half, e = i - t * s.half;
-    const int32_t frac = (int32_t)((uint64_t)(uint32_t)pos[t] * turn[e] >> 32);
-    float sn, c;
-    sincospif((float)frac * 0x1p-31f, &sn, &c);
-    cs[i] = make_float2(c * s.amplitude, (kInverse ? -sn : sn) * s.amplitude);
-  }
-  __syncthreads();
-
-  const uint32_t n = (uint32_t)(nt * s.heads * s.parts);
-  for (uint32_t i0 = tid; i0 < n; i0 += kThreads * kItems) {
+  const int H = s.q.H + s.k.H;
+  const int64_t units = s.split == 1 ? (s.T + s.tokens - 1) / s.tokens : s.T * s.split, step = (int64_t)gridDim.x * kWarps;
+  int64_t u = (int64_t)blockIdx.x * kWarps + warp;
+  // lane g has the position of the unit's token g
+  auto token = [&](int64_t unit) { return s.split == 1 ? unit * s.tokens : unit / s.split; };
+  auto position = [&](int64_t unit) {
+    const int64_t t = token(unit) + lane;
+    return unit < units && lane < s.tokens && t < s.T ? __ldg(s.pos + t) : -1;
+  };
+  int32_t next = position(u);
+  for (; u < units; u += step) {
+    const int64_t t = token(u);
+    const int h0 = s.split == 1 ? 0 : (int)(u - t * s.split) * s.heads, nh = min(H - h0, s.heads);
+    const int32_t p = next;
+    next = position(u + step);
+    const T *xq = static_cast<const T*>(s.q.x) + t * s.q.xt, *xk = static_cast<const T*>(s.k.x) + t * s.k.xt;
+    T *yq = static_cast<T*>(s.q.y) + t * s.q.yt, *yk = static_cast<T*>(s.k.y) + t * s.k.yt;
+    const int nt = kMany ? (int)min((int64_t)s.tokens, s.T - t) : 1, n = s.split == 1 ? nt * nh * s.parts : nh * s.parts;
     Values<T, kE> a[kItems], b[kItems];
-    T *ya[kItems], *yb[kItems];                                  // NULL: nothing to write
-    const float2* c[kItems];                                     // NULL: the values stay
+    T *ya[kItems], *yb[kItems];   // NULL: nothing to write
+    int c[kItems];                // negative: the values stay
+    auto load = [&](int i0) {
 #pragma unroll
-    for (int j = 0; j < kItems; ++j) {
-      ya[j] = yb[j] = nullptr;
-      c[j] = nullptr;
-      const uint32_t i = i0 + kThreads * j, th = divide(i, s.m_parts), part = i - th * s.parts;
-      const uint32_t t = divide(th, s.m_heads), hl = th - t * s.heads;
-      if (i >= n || (int)hl >= nh) continue;
-      const int h = h0 + (int)hl;
-      const bool isq = h < s.q.H;
-      const RotaryPart& p = isq ? s.q : s.k;
-      const int hh = isq ? h : h - s.q.H;
-      const T* x = static_cast<const T*>(p.x) + (t0 + t) * p.xt + hh * p.xh;
-      T* y = static_cast<T*>(p.y) + (t0 + t) * p.yt + hh * p.yh;
-      const bool turned = (int)part < s.turned && pos[t] >= 0;
-      int ca, cb;
-      if ((int)part < s.turned) {
-        ca = kNext ? 2 * kE * part : kE * part;
-        cb = kNext ? ca + kE : s.half + ca;
-      } else {
-        ca = s.rot + 2 * kE * (part - s.turned);
-        cb = ca + kE < s.D ? ca + kE : -1;
-      }
-      if (!turned && x == y) continue;                           // in place
-      a[j].load(x + ca);
-      ya[j] = y + ca;
-      if (cb >= 0) {
-        b[j].load(x + cb);
-        yb[j] = y + cb;
-      }
-      if (turned) c[j] = cs + t * s.half + kE * part;
-    }
-#pragma unroll
-    for (int j = 0; j < kItems; ++j) {
-      if (c[j]) {
-#pragma unroll
-        for (int e = 0; e < kE; ++e) {
-          // kNext: pair e is values 2 e, 2 e + 1 of a and b together
-          T& u = kNext && kE > 1 ? (2 * e < kE ? a[j].x[(2 * e) % kE] : b[j].x[(2 * e) % kE]) : a[j].x[e];
-          T& w = kNext && kE > 1 ? (2 * e < kE ? a[j].x[(2 * e + 1) % kE] : b[j].x[(2 * e + 1) % kE]) : b[j].x[e];
-          const float2 z = c[j][e];
-          const float x0 = to_f32<T>(u), x1 = to_f32<T>(w);
-          u = from_f32<T>(x0 * z.x - x1 * z.y);
-          w = from_f32<T>(x0 * z.y + x1 * z.x);
+      for (int j = 0; j < kItems; ++j) {
+        ya[j] = yb[j] = nullptr;
+        c[j] = -1;
+        const uint32_t i = i0 + 32 * j, g = kMany ? divide(i, s.m_token) : 0, r = i - g * s.heads * s.parts, hl = divide(r, s.m_parts);
+        const int part = (int)(r - hl * s.parts), h = h0 + (int)hl, hk = h - s.q.H;
+        const int32_t at = __shfl_sync(0xffffffffu, p, kMany ? g & 31 : 0);
+        if ((int)i >= n) continue;
+        const T* x = hk < 0 ? xq + g * s.q.xt + h * s.q.xh : xk + g * s.k.xt + hk * s.k.xh;
+        T* y = hk < 0 ? yq + g * s.q.yt + h * s.q.yh : yk + g * s.k.yt + hk * s.k.yh;
+        const bool pairs = part < s.turned, turned = pairs && at >= 0;
+        const int ca = !pairs ? s.rot + 2 * kE * (part - s.turned) : kNext ? 2 * kE * part : kE * part;
+        const int cb = pairs && !kNext ? s.half + ca : ca + kE;
+        if (!turned && x == y) continue;   // in place
+        a[j].load(x + ca);
+        ya[j] = y + ca;
+        if (cb < s.D) {
+          b[j].load(x + cb);
+          yb[j] = y + cb;
         }
+        if (turned) c[j] = (int)g * s.half + (kE == 1 ? part : 2 * part);
       }
-      if (ya[j]) a[j].store(ya[j]);
-      if (yb[j]) b[j].store(yb[j]);
+    };
+    load(lane);
+    __syncwarp();   // the last token's cosines have been read
+    for (int g = 0; g < nt; ++g) {
+      const int32_t at = __shfl_sync(0xffffffffu, p, g);
+      if (at < 0) continue;
+      for (int i = lane; i < s.half; i += 32) {
+        const int32_t frac = (int32_t)((uint64_t)(uint32_t)at * turn[i] >> 32);
+        float sn, cc;
+        sincospif((float)frac * 0x1p-31f, &sn, &cc);
+        // pair i is pair i % kE of part i / kE
+        const int to = kE == 1 ? i : ((i % kE >> 1) * s.turned + i / kE) * 2 + (i & 1);
+        cs[g * s.half + to] = make_float2(cc * s.amplitude, (kInverse ? -sn : sn) * s.amplitude);
+      }
+    }
+    __syncwarp();
+    for (int i0 = lane;;) {
+#pragma unroll
+      for (int j = 0; j < kItems; ++j) {
+        if (c[j] >= 0) {
+          if constexpr (kE == 1) {
+            const float2 z = cs[c[j]];
+            const float x0 = to_f32<T>(a[j].x[0]), x1 = to_f32<T>(b[j].x[0]);
+            a[j].x[0] = from_f32<T>(x0 * z.x - x1 * z.y);
+            b[j].x[0] = from_f32<T>(x0 * z.y + x1 * z.x);
+          } else {
+#pragma unroll
+            for (int e = 0; e < kE; e += 2) {
+              const float4 z = *reinterpret_cast<const float4*>(cs + c[j] + e * s.turned);
+#pragma unroll
+              for (int d = 0; d < 2; ++d) {
+                // kNext: pair e is values 2 e, 2 e + 1 of a and b together
+                T& u0 = kNext ? (2 * (e + d) < kE ? a[j].x[2 * (e + d) % kE] : b[j].x[2 * (e + d) % kE]) : a[j].x[e + d];
+                T& u1 = kNext ? (2 * (e + d) < kE ? a[j].x[(2 * (e + d) + 1) % kE] : b[j].x[(2 * (e + d) + 1) % kE]) : b[j].x[e + d];
+                const float x0 = to_f32<T>(u0), x1 = to_f32<T>(u1), cc = d ? z.z : z.x, sn = d ? z.w : z.y;
+                u0 = from_f32<T>(x0 * cc - x1 * sn);
+                u1 = from_f32<T>(x0 * sn + x1 * cc);
+              }
+            }
+          }
+        }
+        if (ya[j]) a[j].store(ya[j]);
+        if (yb[j]) b[j].store(yb[j]);
+      }
+      i0 += 32 * kItems;
+      if (i0 - lane >= n) break;
+      load(i0);
     }
   }
 }
@@ -151,34 +180,41 @@ uint32_t magic(uint32_t d) { return d == 1 ? 0u : (uint32_t)((0x100000000ull + d
 
 template <typename T, int kE>
 cudaError_t launch(const RotaryProblem& p, cudaStream_t stream) {
-  Shape s{p.q, p.k, p.pos, p.freqs, p.T, p.D, p.rot, p.rot / 2, p.amplitude, 1, 0, 0, 0, 0, 0};
+  Shape s{p.q, p.k, p.pos, p.freqs, p.T, p.D, p.rot, p.rot / 2, p.amplitude, 1, 0, 1, 0, 0, 0, 0};
   const int H = p.q.H + p.k.H;
   s.turned = s.half / kE;
   s.parts = s.turned + (p.D - p.rot + 2 * kE - 1) / (2 * kE);
-  // Tokens of a block: 32 KB of values or more, as long as that leaves 1,024 blocks; few tokens: their heads
-  // over several blocks, at least one item a thread.
-  const int64_t per_token = (int64_t)H * p.D * (int64_t)sizeof(T);
-  s.tokens = (int)std::max<int64_t>(1, std::min<int64_t>({16, (32768 + per_token - 1) / per_token, p.T / 1024}));
-  int split = 1;
-  if (p.T < 512) split = (int)std::min<int64_t>(std::max<int64_t>(1, (int64_t)H * s.parts / kThreads), (512 + p.T - 1) / p.T);
-  s.heads = (H + split - 1) / split;
-  split = (H + s.heads - 1) / s.heads;
-  s.m_heads = magic((uint32_t)s.heads);
   s.m_parts = magic((uint32_t)s.parts);
-  const size_t smem = (size_t)s.half * 8 + (size_t)s.tokens * s.half * 8 + (size_t)s.tokens * 4;
-  const dim3 grid((unsigned)((p.T + s.tokens - 1) / s.tokens), (unsigned)split);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  // Two blocks an SM.  With fewer tokens than warps, several warps a token, each with an item a lane at least;
+  // with many tokens of few heads, several tokens a warp, three items a lane (2 + 1 heads of 64, 65,536 tokens:
+  // 34 us with one token at a time).
+  const int64_t warps = (int64_t)2 * sms * kWarps, items = (int64_t)H * s.parts;
+  const int64_t split = std::min<int64_t>(std::max<int64_t>(1, warps / p.T), std::max<int64_t>(1, items / 32));
+  s.heads = (int)((H + split - 1) / split);
+  s.split = (H + s.heads - 1) / s.heads;
+  if (s.split == 1)
+    s.tokens = (int)std::max<int64_t>(1, std::min<int64_t>({8, 32 * kItems / items, 512 / std::max(s.half, 1), p.T / warps}));
+  s.m_token = magic((uint32_t)(s.heads * s.parts));
+  const size_t smem = (size_t)s.half * 8 * (1 + kWarps * s.tokens);   // 36 KB at most
+  const int64_t units = s.split == 1 ? (p.T + s.tokens - 1) / s.tokens : p.T * s.split;
+  const dim3 grid((unsigned)std::min<int64_t>(2 * sms, (units + kWarps - 1) / kWarps));
   auto go = [&](auto kernel) -> cudaError_t {
-    if (smem > 48 * 1024) {
-      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 72 * 1024);
-      if (e != cudaSuccess) return e;
-    }
-    kernel<<<grid, kThreads, smem, stream>>>(s);
+    kernel<<<grid, 32 * kWarps, smem, stream>>>(s);
     return cudaGetLastError();
   };
   prof_begin(stream, "rotary_kernel");
-  cudaError_t e;
-  if (p.flags & KDA_ROTARY_INTERLEAVED) e = p.flags & KDA_ROTARY_INVERSE ? go(rotary_kernel<T, kE, true, true>) : go(rotary_kernel<T, kE, true, false>);
-  else e = p.flags & KDA_ROTARY_INVERSE ? go(rotary_kernel<T, kE, false, true>) : go(rotary_kernel<T, kE, false, false>);
+  auto pick = [&](auto many) -> cudaError_t {
+    constexpr bool kMany = decltype(many)::value;
+    const bool inverse = (p.flags & KDA_ROTARY_INVERSE) != 0;
+    if (p.flags & KDA_ROTARY_INTERLEAVED) return inverse ? go(rotary_kernel<T, kE, true, true, kMany>) : go(rotary_kernel<T, kE, true, false, kMany>);
+    return inverse ? go(rotary_kernel<T, kE, false, true, kMany>) : go(rotary_kernel<T, kE, false, false, kMany>);
+  };
+  if constexpr (kE == 1) e = pick(std::true_type{});
+  else e = s.tokens > 1 ? pick(std::true_type{}) : pick(std::false_type{});
   prof_end(stream);
   return e;
 }

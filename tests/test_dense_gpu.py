@@ -261,6 +261,32 @@ def test_rotary_far_positions_of_fast_pairs():
     assert (np.abs(_np(y) - want) <= _rot_tol(_np(x), want, 1.0, "f32")).all()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T,Hq,Hk,D,rot", [(9731, 1, 1, 64, 64), (20000, 2, 1, 64, 32), (10007, 1, 0, 6, 4), (40001, 4, 2, 128, 128)])
+def test_rotary_many_tokens(T, Hq, Hk, D, rot, interleaved, dt):
+    """Few heads and more tokens than the chip holds warps, the formula in fp64 on the GPU (angles below 2^31 * 1e-4, so
+    that fp64's own error in them stays below 2^-30)."""
+    x = _rows(T * (Hq + Hk), D, dt, T).view(T, Hq + Hk, D).cuda()
+    q, k = x[:, :Hq], x[:, Hq:] if Hk else None
+    pos = torch.randint(-1000, 2 ** 31 - 1, (T,), generator=torch.Generator().manual_seed(T)).to(torch.int32).cuda()
+    pos[5::7] = -1
+    freqs, _ = kda.kda_rotary_freqs(rot, 100.0)
+    freqs = freqs * 1e-4
+    yq, yk = kda.kda_rotary(q, k, pos, freqs, 1.0, interleaved)
+    y = yq if yk is None else torch.cat([yq, yk], 1)
+    ang = (pos.double()[:, None] * freqs)[:, None]
+    still = (pos < 0)[:, None, None]
+    c, s = torch.where(still, 1.0, ang.cos()), torch.where(still, 0.0, ang.sin())
+    want = x.double().clone()
+    i = 2 * torch.arange(rot // 2, device="cuda") if interleaved else torch.arange(rot // 2, device="cuda")
+    j = i + 1 if interleaved else i + rot // 2
+    want[..., i], want[..., j] = x.double()[..., i] * c - x.double()[..., j] * s, x.double()[..., i] * s + x.double()[..., j] * c
+    size = 2 * x.double().abs().amax(-1, keepdim=True)
+    assert ((y.double() - want).abs() <= 2.0 ** -20 * size + (2.0 ** -8 if dt == "bf16" else 0) * want.abs()).all()
+    assert torch.equal(y[pos < 0], x[pos < 0])
+
+
 def test_rotary_no_tokens():
     q = torch.zeros(0, 4, 64, device="cuda")
     y, _ = kda.kda_rotary(q, None, torch.zeros(0, dtype=torch.int32, device="cuda"), torch.ones(32, dtype=torch.float64, device="cuda"))
