@@ -26,7 +26,7 @@ struct Few {
   static constexpr int kSets = (kRows + 127) / 128;               // of 128 tokens' scales
   static constexpr uint32_t kScales = 512 * (1 + kSets);          // one slot: weights', tokens'
   static constexpr uint32_t oScales = kStages * kStage, oBars = oScales + kScaleSlots * kScales;
-  static constexpr int kBars = 2 * kStages + 2 * kScaleSlots + 1;
+  static constexpr int kBars = 2 * kStages + 2 * kScaleSlots + 1;   // at most 32: a lane initialises one each
   static constexpr uint32_t kBytes = oBars + kBars * 8 + 8, kAlloc = kBytes + 1024;   // + alignment
   static constexpr uint32_t cScales = kRows, kCols = kRows + 2 * 4 * (1 + kSets);      // TMEM columns
   static constexpr uint32_t kTmem = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
@@ -63,14 +63,32 @@ __global__ void __launch_bounds__(kThreads)
   const int32_t groups = (blocks + 3) / 4, kb0 = (int32_t)((int64_t)groups * rank / split) * 4;
   const int32_t nb = (int32_t)min((int64_t)groups * (rank + 1) / split * 4, (int64_t)blocks) - kb0;
 
+  // Before the CTA meets: the first loads go out, and the first scales are read.
+  const uint32_t at = tc::smem_u32(sm), bar = tc::smem_u32(full);
+  const int first = min(nb, F::kStages);
+  uint32_t ww[1], wx[4 * F::kSets];
+  auto load_tile = [&](int i, int st) {
+    expect_w(bar + 8 * st, F::kStage);
+    tma_load_w<1>(at + st * F::kStage, &mapW, (kb0 + i) * kStageK, (int32_t)n0, bar + 8 * st);
+    tma_load_w<1>(at + st * F::kStage + F::kW, &mapX, (kb0 + i) * kStageK, (int32_t)m0, bar + 8 * st);
+  };
+  auto load_words = [&](int g) {
+    load_scales(sw, blocks, kb0 + 4 * g, words, ww, [&](int) { return (int64_t)tile; });
+    load_scales(sx, blocks, kb0 + 4 * g, words, wx, [&](int i) {
+      const int r = 32 * i + lane;
+      return r < kRows && m0 + r < M ? m0 + r : (int64_t)-1;
+    });
+  };
   if (warp == 0) {
-    if (lane == 0) {
-      for (int i = 0; i < F::kBars; ++i) tc::mbar_init(full + i, 1);
-      tc::fence_mbar_init();
-    }
+    if (lane < F::kBars) tc::mbar_init(full + lane, 1);
+    tc::fence_mbar_init();
+    __syncwarp();
+    for (int i = 0; i < first; ++i) load_tile(i, i);
   } else if (warp == 1) {
     tc::tmem_alloc(tmem_at, F::kTmem);
     tc::tmem_relinquish();
+  } else if (warp == 2) {
+    load_words(0);
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -79,14 +97,11 @@ __global__ void __launch_bounds__(kThreads)
   bool ok = true;
 
   if (warp == 0) {
-    const uint32_t at = tc::smem_u32(sm), bar = tc::smem_u32(full);
-    int st = 0, i = 0;
-    uint32_t phase = 1;
+    int st = 0, i = first;
+    uint32_t phase = 0;
     for (; i < nb; ++i) {
-      if (i >= F::kStages && !(ok = wait_w(empty + st, phase))) break;
-      expect_w(bar + 8 * st, F::kStage);
-      tma_load_w<1>(at + st * F::kStage, &mapW, (kb0 + i) * kStageK, (int32_t)n0, bar + 8 * st);
-      tma_load_w<1>(at + st * F::kStage + F::kW, &mapX, (kb0 + i) * kStageK, (int32_t)m0, bar + 8 * st);
+      if (!(ok = wait_w(empty + st, phase))) break;
+      load_tile(i, st);
       if (++st == F::kStages) st = 0, phase ^= 1;
     }
     if (!ok)   // end with no copy in flight
@@ -124,21 +139,19 @@ __global__ void __launch_bounds__(kThreads)
   } else if (warp == 2) {
     for (int g = 0; 4 * g < nb && ok; ++g) {
       const int slot = g % kScaleSlots;
-      uint32_t ww[1], wx[4 * F::kSets];
-      load_scales(sw, blocks, kb0 + 4 * g, words, ww, [&](int) { return (int64_t)tile; });
-      load_scales(sx, blocks, kb0 + 4 * g, words, wx, [&](int i) {
-        const int r = 32 * i + lane;
-        return r < kRows && m0 + r < M ? m0 + r : (int64_t)-1;
-      });
       if (g >= kScaleSlots) ok = wait_w(sempty + slot, (g / kScaleSlots - 1) & 1);
       if (!ok) break;
       uint4* to = reinterpret_cast<uint4*>(sm + F::oScales + slot * F::kScales) + lane;
       to[0] = make_uint4(ww[0], ww[0], ww[0], ww[0]);
 #pragma unroll
+      for (int i = 0; i < 4 * F::kSets; ++i)
+        if (32 * i + lane >= min((int64_t)kRows, M - m0)) wx[i] = kOnes;
+#pragma unroll
       for (int s = 0; s < F::kSets; ++s) to[32 * (1 + s)] = make_uint4(wx[4 * s], wx[4 * s + 1], wx[4 * s + 2], wx[4 * s + 3]);
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(sfull + slot);
+      if (4 * (g + 1) < nb) load_words(g + 1);
     }
   }
   // every product done: the sums are in TMEM, and nothing reads or writes the stages any more

@@ -10,6 +10,8 @@
 //
 // Warps of a CTA: 0 loads tiles, 1 issues products (of the leading CTA alone), 2 loads scales, 3 TMEM,
 // 4 to 7 store.
+#include <limits.h>
+
 #include <algorithm>
 
 #include "internal.cuh"
@@ -22,13 +24,15 @@ namespace {
 constexpr int kTM = 256, kTN = 240, kThreads = 256, kStages = 6;
 constexpr uint32_t kA = 128 * kStageK, kB = kTN / 2 * kStageK, kStage = kA + kB;
 constexpr uint32_t kScales = 3 * 512;   // one slot: 128 rows of A, twice 128 of W
-constexpr uint32_t oScales = kStages * kStage, oTurn = oScales + kScaleSlots * kScales, kTurnRow = 33;
-constexpr uint32_t oBars = oTurn + 4 * 32 * kTurnRow * 4;
+constexpr uint32_t oScales = kStages * kStage, oOut = oScales + kScaleSlots * kScales;
+// Per storing warp two pieces of 32 rows by 96 bytes of the output; or 32 rows of 16 sums (17 words apart).
+constexpr uint32_t kPiece = 32 * 96, kTurnRow = 17;
+constexpr uint32_t oBars = oOut + 4 * 2 * kPiece;
 constexpr int kBars = 2 * kStages + 2 * kScaleSlots + 4;
 constexpr uint32_t kAlloc = oBars + kBars * 8 + 8 + 1024;
 constexpr uint32_t cScales = 2 * kTN;   // TMEM columns: two accumulators, two slots of scales
 constexpr int kGroupM = 8;              // tiles are taken in bands of so many rows of tiles
-static_assert(kAlloc <= 227 * 1024, "shared memory");
+static_assert(kAlloc <= 227 * 1024 && 32 * kTurnRow * 4 <= 2 * kPiece && oOut % 128 == 0, "shared memory");
 
 // ------------------------------------------------------------- forms for a pair of CTAs
 // Arrival on an mbarrier of the cluster (address from mapa_shared), released at CTA scope: what it orders lies in
@@ -53,25 +57,49 @@ __device__ __forceinline__ void tmem_free_pair(uint32_t taddr) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
 }
 
-__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
-               "r"(w[5]), "r"(w[6]), "r"(w[7])
+// 8 columns of TMEM, not there before tmem_ld_end has waited for them.
+__device__ __forceinline__ void tmem_ld8_begin(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
                : "memory");
+}
+// The registers pass through the wait, so that nothing uses them before it.
+template <int N>
+__device__ __forceinline__ void tmem_ld_end(uint32_t (&r)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i])::"memory");
+}
+// Store of a piece by the elected lane, as a bulk group of its own; and a wait until at most kLeft of them still read shared memory.
+__device__ __forceinline__ void tma_store_w(const CUtensorMap* map, int32_t x, int32_t y, uint32_t src) {
+  asm volatile(
+      "{\n\t.reg .pred pe;\n\t"
+      "elect.sync _|pe, 0xffffffff;\n\t"
+      "@pe cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\t"
+      "@pe cp.async.bulk.commit_group;\n\t}" ::"l"(reinterpret_cast<uint64_t>(map)),
+      "r"(x), "r"(y), "r"(src)
+      : "memory");
+}
+template <int kLeft>
+__device__ __forceinline__ void stores_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
 }
 
 // Tile t of tm x tn: bands of kGroupM rows of tiles, column after column inside a band, so that the tiles in
 // flight share both their rows of A and their weights in L2.
-__device__ __forceinline__ void place(int64_t t, int64_t tm, int64_t tn, int64_t& im, int64_t& in) {
-  const int64_t band = t / (kGroupM * tn), first = band * kGroupM, rows = tm - first < kGroupM ? tm - first : kGroupM;
-  const int64_t rest = t - band * kGroupM * tn;
+__device__ __forceinline__ void place(uint32_t t, uint32_t tm, uint32_t tn, uint32_t& im, uint32_t& in) {
+  const uint32_t band = t / (kGroupM * tn), first = band * kGroupM, rows = min(tm - first, (uint32_t)kGroupM);
+  const uint32_t rest = t - band * kGroupM * tn;
   in = rest / rows;
   im = first + rest - in * rows;
 }
 
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    fp8_matmul_pair_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB, const uint8_t* __restrict__ sa,
-                           const uint8_t* __restrict__ sw, int64_t M, int64_t N, int32_t blocks, int64_t tm, int64_t tn, T* out, int64_t ldo,
+    fp8_matmul_pair_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB, const __grid_constant__ CUtensorMap mapO,
+                           const uint8_t* __restrict__ sa,
+                           const uint8_t* __restrict__ sw, int64_t M, int64_t N, int32_t blocks, uint32_t tm, uint32_t tn, T* out, int64_t ldo,
                            int32_t wide, int32_t words, int32_t* dev_err) {
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);
@@ -82,25 +110,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(tempty + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = tc::cluster_ctarank();
-  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, tiles = tm * tn;
+  const uint32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, tiles = tm * tn;
   const int groups = (blocks + 3) / 4;   // of four K blocks: a word of scales
 
-  if (warp == 0 && lane == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      tc::mbar_init(full + i, 1);
-      tc::mbar_init(empty + i, 1);
-    }
-    for (int i = 0; i < kScaleSlots; ++i) {
-      tc::mbar_init(sfull + i, 2);
-      tc::mbar_init(sempty + i, 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(tfull + i, 1);
-      tc::mbar_init(tempty + i, 8);
+  // Before the cluster meets: the first scales are read, and the leading CTA's own first loads go out.
+  const uint32_t at = tc::smem_u32(sm), lead = tc::mapa_shared(full, 0);
+  uint32_t wa[4], wb[8];
+  auto load_words = [&](uint32_t t, int gg) {   // of group gg of tile t
+    uint32_t im, in;
+    place(t, tm, tn, im, in);
+    load_scales(sa, blocks, 4 * gg, words, wa, [&](int i) {
+      const int64_t m = (int64_t)im * kTM + 128 * rank + 32 * i + lane;
+      return m < M ? m : -1;
+    });
+    load_scales(sw, blocks, 4 * gg, words, wb, [&](int i) {
+      const int64_t c = (int64_t)in * kTN + 32 * i + lane;
+      return c < N ? c / kBlock : -1;
+    });
+  };
+  auto load_tile = [&](int32_t kb, int st, int32_t ya, int32_t yb) {
+    // the leading CTA expects both CTAs' bytes; the other's may come first, its arrival is what ends the phase
+    if (rank == 0) expect_w(tc::smem_u32(full + st), 2 * kStage);
+    tma_load_w<2>(at + st * kStage, &mapA, kb * kStageK, ya, lead + 8 * st);
+    tma_load_w<2>(at + st * kStage + kA, &mapB, kb * kStageK, yb, lead + 8 * st);
+  };
+  const int early = rank == 0 ? min(blocks, kStages) : 0;   // of the first tile
+  if (warp == 0) {
+    if (lane < kBars) {   // in the order of their declaration: full, empty, sfull, sempty, tfull, tempty
+      const int i = lane - 2 * kStages - kScaleSlots;
+      tc::mbar_init(full + lane, i < -kScaleSlots ? 1 : i < 0 ? 2 : i < kScaleSlots + 2 ? 1 : 8);
     }
     tc::fence_mbar_init();
+    __syncwarp();
+    if (early > 0) {
+      uint32_t im, in;
+      place(pair, tm, tn, im, in);
+      for (int kb = 0; kb < early; ++kb) load_tile(kb, kb, (int32_t)(im * kTM), (int32_t)(in * kTN));
+    }
+  } else if (warp == 2) {
+    load_words(pair, 0);
+  } else if (warp == 3) {
+    tmem_alloc_pair(tmem_at);
   }
-  if (warp == 3) tmem_alloc_pair(tmem_at);
   tc::tc_fence_before();
   __syncthreads();
   tc::cluster_sync_all();
@@ -109,20 +160,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   bool ok = true;
 
   if (warp == 0) {
-    const uint32_t at = tc::smem_u32(sm), lead = tc::mapa_shared(full, 0);
     int st = 0;
     uint32_t phase = 1;
     int64_t n = 0;   // stages so far
-    for (int64_t t = pair; t < tiles && ok; t += pairs) {
-      int64_t im, in;
+    for (uint32_t t = pair; t < tiles && ok; t += pairs) {
+      uint32_t im, in;
       place(t, tm, tn, im, in);
       const int32_t ya = (int32_t)(im * kTM + 128 * rank), yb = (int32_t)(in * kTN + kTN / 2 * rank);
       for (int32_t kb = 0; kb < blocks; ++kb, ++n) {
         if (n >= kStages && !(ok = wait_w(empty + st, phase))) break;
-        // the leading CTA expects both CTAs' bytes; the other's may come first, its arrival is what ends the phase
-        if (rank == 0) expect_w(tc::smem_u32(full + st), 2 * kStage);
-        tma_load_w<2>(at + st * kStage, &mapA, kb * kStageK, ya, lead + 8 * st);
-        tma_load_w<2>(at + st * kStage + kA, &mapB, kb * kStageK, yb, lead + 8 * st);
+        if (n >= early) load_tile(kb, st, ya, yb);
         if (++st == kStages) st = 0, phase ^= 1;
       }
     }
@@ -134,7 +181,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint64_t dS = desc_scales(tc::smem_u32(sm + oScales));
       int st = 0, it = 0;
       uint32_t phase = 0, g = 0;
-      for (int64_t t = pair; t < tiles && ok; t += pairs, ++it) {
+      for (uint32_t t = pair; t < tiles && ok; t += pairs, ++it) {
         const uint32_t acc = tmem + (it & 1) * kTN;
         if (it >= 2 && !(ok = wait_w(tempty + (it & 1), ((it >> 1) - 1) & 1))) break;
         tc::tc_fence_after();
@@ -166,97 +213,99 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int i = it > 2 ? it - 2 : 0; i < it; ++i) ok = wait_w(tempty + (i & 1), (i >> 1) & 1) && ok;
     }
   } else if (warp == 2) {
-    uint32_t g = 0, wa[4], wb[8];
-    int64_t t = pair, im, in;
+    uint32_t g = 0, t = pair;
     int gg = 0;
-    auto load = [&]() {   // of group gg of tile t
-      place(t, tm, tn, im, in);
-      load_scales(sa, blocks, 4 * gg, words, wa, [&](int i) {
-        const int64_t m = im * kTM + 128 * rank + 32 * i + lane;
-        return m < M ? m : -1;
-      });
-      load_scales(sw, blocks, 4 * gg, words, wb, [&](int i) {
-        const int64_t c = in * kTN + 32 * i + lane;
-        return c < N ? c / kBlock : -1;
-      });
-    };
-    if (t < tiles) load();
     while (t < tiles) {
       const uint32_t slot = g % kScaleSlots;
       if (g >= kScaleSlots && !(ok = wait_w(sempty + slot, (g / kScaleSlots - 1) & 1))) break;
       uint4* to = reinterpret_cast<uint4*>(sm + oScales + slot * kScales) + lane;
+      {   // rows behind the last: a factor 1
+        uint32_t im, in;
+        place(t, tm, tn, im, in);
+        const int64_t ml = M - (int64_t)im * kTM - 128 * rank - lane, nl = N - (int64_t)in * kTN - lane;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wa[i] = 32 * i < ml ? wa[i] : kOnes;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) wb[i] = 32 * i < nl ? wb[i] : kOnes;
+      }
       to[0] = make_uint4(wa[0], wa[1], wa[2], wa[3]);
       to[32] = make_uint4(wb[0], wb[1], wb[2], wb[3]);
       to[64] = make_uint4(wb[4], wb[5], wb[6], wb[7]);
       tc::fence_proxy_async_smem();
       __syncwarp();
-      if (++gg == groups) gg = 0, t += pairs;
-      if (t < tiles) load();   // on their way during the arrival
       if (lane == 0) arrive_cluster(tc::mapa_shared(sfull + slot, 0));
+      if (++gg == groups) gg = 0, t += pairs;
+      if (t < tiles) load_words(t, gg);
       ++g;
     }
     for (uint32_t i = g > kScaleSlots ? g - kScaleSlots : 0; i < g; ++i)
       ok = wait_w(sempty + i % kScaleSlots, (i / kScaleSlots) & 1) && ok;
   } else if (warp >= 4) {
     const int q = warp - 4;
-    float* turn = reinterpret_cast<float*>(sm + oTurn) + q * 32 * kTurnRow;
+    uint8_t* mine = sm + oOut + q * 2 * kPiece;
+    constexpr int kCols = 96 / sizeof(T);   // of a piece
+    uint32_t piece = 0;
     int it = 0;
-    for (int64_t t = pair; t < tiles; t += pairs, ++it) {
-      int64_t im, in;
+    for (uint32_t t = pair; t < tiles; t += pairs, ++it) {
+      uint32_t im, in;
       place(t, tm, tn, im, in);
       if (!(ok = wait_w(tfull + (it & 1), (it >> 1) & 1))) break;
       tc::tc_fence_after();
       const uint32_t acc = tc::tmem_addr(tmem, 32 * q, (it & 1) * kTN);
-      const int64_t m0 = im * kTM + 128 * rank + 32 * q, n0 = in * kTN;
+      const int64_t m0 = (int64_t)im * kTM + 128 * rank + 32 * q, n0 = (int64_t)in * kTN;
       const int rows = (int)(M - m0 < 32 ? M - m0 : 32), cols = (int)(N - n0 < kTN ? N - n0 : kTN);
+      auto freed = [&]() {   // the accumulator has been read
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(tc::mapa_shared(tempty + (it & 1), 0));
+      };
+      if (rows <= 0) {
+        freed();
+      } else if (wide) {
 #pragma unroll 1
-      for (int c = 0; c < kTN; c += 16) {
-        float v[16];
-        tc::tmem_ld16(acc + c, v);
-        if (c + 16 == kTN) {   // the accumulator is free
-          tc::tc_fence_before();
+        for (int c = 0; c < cols; c += kCols, piece ^= 1) {   // a store for each, so that the last but one had this place
+          uint32_t v[kCols];
+#pragma unroll
+          for (int i = 0; i < kCols; i += 8) tmem_ld8_begin(acc + c + i, v + i);
+          stores_read<1>();   // that one has been read (a lane without stores does not wait)
+          tmem_ld_end(v);
+          if (c + kCols >= cols) freed();
           __syncwarp();
-          if (lane == 0) arrive_cluster(tc::mapa_shared(tempty + (it & 1), 0));
-        }
-        if (c + 16 <= cols && wide) {
-          T* o = out + (m0 + lane) * ldo + n0 + c;
-          if (lane < rows) {
+          uint4* to = reinterpret_cast<uint4*>(mine + piece * kPiece + 96 * lane);
+#pragma unroll
+          for (int i = 0; i < 6; ++i) {
             if constexpr (sizeof(T) == 2) {
-              uint32_t w[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) w[i] = bf16x2(v[2 * i], v[2 * i + 1]);
-              if (wide == 2) {
-                store32(o, w);
-              } else {
-                reinterpret_cast<uint4*>(o)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                reinterpret_cast<uint4*>(o)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-              }
+              const float* f = reinterpret_cast<const float*>(v + 8 * i);
+              to[i] = make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]), bf16x2(f[6], f[7]));
             } else {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint32_t w[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 * h + i]);
-                if (wide == 2) {
-                  store32(o + 8 * h, w);
-                } else {
-                  reinterpret_cast<uint4*>(o)[2 * h] = make_uint4(w[0], w[1], w[2], w[3]);
-                  reinterpret_cast<uint4*>(o)[2 * h + 1] = make_uint4(w[4], w[5], w[6], w[7]);
-                }
-              }
+              to[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
             }
           }
-        } else if (c < cols) {   // through shared memory: a row's columns next to one another
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          tma_store_w(&mapO, (int32_t)n0 + c, (int32_t)m0, tc::smem_u32(mine + piece * kPiece));
+        }
+      } else {   // through shared memory: a row's columns next to one another
+        float* turn = reinterpret_cast<float*>(mine);
+#pragma unroll 1
+        for (int c = 0; c < cols; c += 16) {
+          float v[16];
+          tc::tmem_ld16(acc + c, v);
+          if (c + 16 >= cols) freed();
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 16; ++i) turn[lane * kTurnRow + i] = v[i];
           __syncwarp();
-          const int cc = lane & 15;
-          for (int r = lane >> 4; r < rows; r += 2)
-            if (c + cc < cols) out[(m0 + r) * ldo + n0 + c + cc] = from_f32<T>(turn[r * kTurnRow + cc]);
+          const int cc = c + (lane & 15);
+          if (cc < cols) {
+            T* o = out + (m0 + (lane >> 4)) * ldo + n0 + cc;
+#pragma unroll 4
+            for (int r = lane >> 4; r < rows; r += 2, o += 2 * ldo) *o = from_f32<T>(turn[r * kTurnRow + (lane & 15)]);
+          }
         }
       }
     }
+    tc::bulk_wait0();
   }
   if (!__all_sync(0xffffffffu, ok) && lane == 0) atomicExch(dev_err, (int32_t)kDevErrTimeout);
   tc::tc_fence_before();
@@ -268,16 +317,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 template <typename T>
 cudaError_t launch(const MatmulProblem& p, int sms, cudaStream_t stream) {
-  CUtensorMap ma, mb;
+  CUtensorMap ma, mb, mo;
   if (!codes_map(&ma, p.a, p.M, p.K, p.lda, 128) || !codes_map(&mb, p.w, p.N, p.K, p.ldw, kTN / 2)) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(fp8_matmul_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAlloc);
   if (e != cudaSuccess) return e;
   const int64_t tm = (p.M + kTM - 1) / kTM, tn = (p.N + kTN - 1) / kTN;
-  const auto step = [&](size_t n) { return reinterpret_cast<uintptr_t>(p.out) % n == 0 && (size_t)p.ldo * sizeof(T) % n == 0; };
+  // rows that begin on 16-byte boundaries leave by tensor stores
+  const bool wide = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && (size_t)p.ldo * sizeof(T) % 16 == 0;
+  if (!wide) mo = ma;
+  else if (!out_map(&mo, p.out, p.M, p.N, p.ldo, sizeof(T), 96 / sizeof(T), 32)) return cudaErrorInvalidValue;
+  if (tm * tn > INT32_MAX) return cudaErrorInvalidValue;   // (2^44 products of a K: no memory holds them)
   const unsigned grid = 2 * (unsigned)std::min<int64_t>(tm * tn, sms / 2);
   prof_begin(stream, "fp8_matmul_pair_kernel");
-  fp8_matmul_pair_kernel<T><<<grid, kThreads, kAlloc, stream>>>(ma, mb, p.sa, p.sw, p.M, p.N, (int32_t)((p.K + kStageK - 1) / kStageK), tm, tn,
-                                                               static_cast<T*>(p.out), p.ldo, step(32) ? 2 : step(16) ? 1 : 0,
+  fp8_matmul_pair_kernel<T><<<grid, kThreads, kAlloc, stream>>>(ma, mb, mo, p.sa, p.sw, p.M, p.N, (int32_t)((p.K + kStageK - 1) / kStageK), (uint32_t)tm, (uint32_t)tn,
+                                                               static_cast<T*>(p.out), p.ldo, (int32_t)wide,
                                                                scale_words(p.sa, p.sw, (p.K + kStageK - 1) / kStageK), p.dev_err);
   prof_end(stream);
   return cudaGetLastError();

@@ -119,23 +119,26 @@ __device__ __forceinline__ void expect_w(uint32_t bar, uint32_t bytes) {
 constexpr int kScaleSlots = 4;   // groups of four K blocks whose scales are on their way (two of them in TMEM)
 
 // Scale words of four K blocks, kb .. kb + 3 of `blocks` (bytes behind the last: 127, a factor 1), for kWords rows:
-// row(i) gives a row's number, negative for none (a factor 1).  No branch stands between the loads, so
-// that all are on their way together.  `words`: rows of whole 32-bit words.
+// row(i) gives a row's number, negative for none (any word then).  No branch stands between the loads, so
+// that all are on their way together, and nothing here waits for whole words.  `words`: rows of whole 32-bit words.
 template <int kWords, typename F>
 __device__ __forceinline__ void load_scales(const uint8_t* __restrict__ scales, int32_t blocks, int32_t kb, bool words, uint32_t (&w)[kWords],
                                             F row) {
   int64_t r[kWords];
 #pragma unroll
-  for (int i = 0; i < kWords; ++i) r[i] = row(i);
+  for (int i = 0; i < kWords; ++i) {
+    r[i] = row(i);
+    r[i] = r[i] < 0 ? 0 : r[i];
+  }
   if (words) {
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(scales + (r[i] < 0 ? 0 : r[i]) * blocks + kb));
+    for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(scales + r[i] * blocks + kb));
   } else {
     uint32_t b[kWords][4];
 #pragma unroll
     for (int i = 0; i < kWords; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) b[i][j] = __ldg(scales + (r[i] < 0 ? 0 : r[i]) * blocks + (kb + j < blocks ? kb + j : blocks - 1));
+      for (int j = 0; j < 4; ++j) b[i][j] = __ldg(scales + r[i] * blocks + (kb + j < blocks ? kb + j : blocks - 1));
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       w[i] = 0;
@@ -143,10 +146,8 @@ __device__ __forceinline__ void load_scales(const uint8_t* __restrict__ scales, 
       for (int j = 0; j < 4; ++j) w[i] |= (kb + j < blocks ? b[i][j] : 127u) << (8 * j);
     }
   }
-#pragma unroll
-  for (int i = 0; i < kWords; ++i)
-    if (r[i] < 0) w[i] = 0x7f7f7f7fu;
 }
+constexpr uint32_t kOnes = 0x7f7f7f7fu;   // four factors of 1
 inline bool scale_words(const void* a, const void* b, int64_t blocks) {
   return blocks % 4 == 0 && reinterpret_cast<uintptr_t>(a) % 4 == 0 && reinterpret_cast<uintptr_t>(b) % 4 == 0;
 }
@@ -174,6 +175,19 @@ inline bool codes_map(CUtensorMap* m, const uint8_t* base, int64_t rows, int64_t
   const cuuint32_t es[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Boxes of box_cols x box_rows of an output of elements of eb bytes, for stores.
+inline bool out_map(CUtensorMap* m, void* base, int64_t rows, int64_t cols, int64_t stride, size_t eb, int box_cols, int box_rows) {
+  const auto fn = tensor_map_encode();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)stride * eb};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+  const cuuint32_t es[2] = {1, 1};
+  return fn(m, eb == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace dense
