@@ -38,7 +38,10 @@ def _dense(codes, scales, rows):
 SIZES = [(1, 1, 16), (1, 128, 128), (1, 2052, 512), (3, 300, 1040), (8, 513, 4096), (16, 256, 4112), (17, 130, 144), (33, 1000, 1088), (64, 384, 640),
          (65, 129, 528), (100, 2052, 512), (128, 4096, 2048), (129, 640, 12288), (256, 513, 4096), (257, 384, 1040), (300, 2048, 272),
          (511, 1000, 512), (512, 1024, 1024), (777, 513, 2064), (1000, 2052, 512), (1024, 4096, 1024), (1500, 129, 16), (2049, 1111, 1152),
-         (4096, 4096, 528), (3000, 5000, 2048)]
+         (4096, 4096, 528), (3000, 5000, 2048),
+         # each way of cutting the product that the choice by sizes has: rows of a tile, parts of K, one or two CTAs an SM
+         (2, 6188, 2624), (42, 21, 15280), (1122, 514, 64), (52, 561, 15056), (6687, 62, 2784), (159, 2068, 6912), (1363, 54, 8800),
+         (611, 16, 16048), (2357, 2519, 80), (6705, 108, 8864), (2749, 18, 11040), (1075, 7427, 2960), (2657, 713, 14704), (1586, 400, 15472)]
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
@@ -51,6 +54,23 @@ def test_exact_sums(M, N, K, dt):
     got = kda.kda_fp8_matmul(a, sa, w, sw, t)
     assert torch.equal(got, want.to(t))
     assert torch.equal(got, kda.kda_fp8_matmul(a, sa, w, sw, t))
+    assert kda.kda_device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("pair", ["0", "1"])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 16), (5, 239, 512), (127, 241, 1040), (129, 480, 2064), (256, 8, 4096), (255, 1200, 528), (513, 1001, 272),
+                                   (2304, 2160, 144), (700, 30000, 128)])
+def test_both_kernels(M, N, K, dt, pair, monkeypatch):
+    """Pairs of CTAs on small and ragged sizes, and single ones on large, against the exact sums."""
+    monkeypatch.setenv("KDA_FP8_PAIR", pair)
+    a, sa, w, sw = (t.cuda() for t in _exact_operands(M, N, K, M + N + K))
+    want = _dense(a, sa, 1) @ _dense(w, sw, 128).t()
+    t = torch.float32 if dt == "f32" else torch.bfloat16
+    assert torch.equal(kda.kda_fp8_matmul(a, sa, w, sw, t), want.to(t))
+    big = torch.full((M, N + 5), -5.0, device="cuda", dtype=t)         # rows that begin anywhere
+    kda.kda_fp8_matmul(a, sa, w, sw, out=big[:, 2:2 + N])
+    assert torch.equal(big[:, 2:2 + N], want.to(t)) and (big[:, :2] == -5).all() and (big[:, N + 2:] == -5).all()
     assert kda.kda_device_error() == (0, 0)
 
 
