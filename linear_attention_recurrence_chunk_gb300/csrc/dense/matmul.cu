@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreads)
         }
       }
     }
-    tc::cluster_sync_all();   // no CTA leaves while another reads its sums
+    cluster_meet();   // no CTA leaves while another reads its sums
   }
   tc::tc_fence_before();
   __syncthreads();

@@ -116,9 +116,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // Before the cluster meets: the first scales are read, and the leading CTA's own first loads go out.
   const uint32_t at = tc::smem_u32(sm), lead = tc::mapa_shared(full, 0);
   uint32_t wa[4], wb[8];
+  int left_a = 0, left_b = 0;   // rows of A, and of W, from this lane's first one on
   auto load_words = [&](uint32_t t, int gg) {   // of group gg of tile t
     uint32_t im, in;
     place(t, tm, tn, im, in);
+    left_a = (int)min(M - (int64_t)im * kTM - 128 * rank - lane, (int64_t)128);
+    left_b = (int)min(N - (int64_t)in * kTN - lane, (int64_t)256);
     load_scales(sa, blocks, 4 * gg, words, wa, [&](int i) {
       const int64_t m = (int64_t)im * kTM + 128 * rank + 32 * i + lane;
       return m < M ? m : -1;
@@ -154,7 +157,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   tc::tc_fence_before();
   __syncthreads();
-  tc::cluster_sync_all();
+  cluster_meet();   // (the barriers' initialisation is released by its own fence)
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_at;
   bool ok = true;
@@ -219,15 +222,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t slot = g % kScaleSlots;
       if (g >= kScaleSlots && !(ok = wait_w(sempty + slot, (g / kScaleSlots - 1) & 1))) break;
       uint4* to = reinterpret_cast<uint4*>(sm + oScales + slot * kScales) + lane;
-      {   // rows behind the last: a factor 1
-        uint32_t im, in;
-        place(t, tm, tn, im, in);
-        const int64_t ml = M - (int64_t)im * kTM - 128 * rank - lane, nl = N - (int64_t)in * kTN - lane;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) wa[i] = 32 * i < ml ? wa[i] : kOnes;
+      for (int i = 0; i < 4; ++i) wa[i] = 32 * i < left_a ? wa[i] : kOnes;   // rows behind the last: a factor 1
 #pragma unroll
-        for (int i = 0; i < 8; ++i) wb[i] = 32 * i < nl ? wb[i] : kOnes;
-      }
+      for (int i = 0; i < 8; ++i) wb[i] = 32 * i < left_b ? wb[i] : kOnes;
       to[0] = make_uint4(wa[0], wa[1], wa[2], wa[3]);
       to[32] = make_uint4(wb[0], wb[1], wb[2], wb[3]);
       to[64] = make_uint4(wb[4], wb[5], wb[6], wb[7]);
@@ -305,12 +303,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
     }
-    tc::bulk_wait0();
+    stores_read<0>();
   }
   if (!__all_sync(0xffffffffu, ok) && lane == 0) atomicExch(dev_err, (int32_t)kDevErrTimeout);
   tc::tc_fence_before();
   __syncthreads();
-  tc::cluster_sync_all();   // both CTAs are done with one another's barriers and TMEM
+  cluster_meet();   // both CTAs are done with one another's barriers and TMEM
   tc::tc_fence_after();
   if (warp == 3) tmem_free_pair(tmem);
 }

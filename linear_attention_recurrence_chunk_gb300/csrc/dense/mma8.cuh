@@ -116,6 +116,12 @@ __device__ __forceinline__ void expect_w(uint32_t bar, uint32_t bytes) {
       : "memory");
 }
 
+// The CTAs of a cluster meet, with no order of memory (tc::cluster_sync_all's release costs up to 2,000 cycles while
+// loads are on their way).
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
 constexpr int kScaleSlots = 4;   // groups of four K blocks whose scales are on their way (two of them in TMEM)
 
 // Scale words of four K blocks, kb .. kb + 3 of `blocks` (bytes behind the last: 127, a factor 1), for kWords rows:
