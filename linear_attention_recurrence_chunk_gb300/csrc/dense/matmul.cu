@@ -21,11 +21,14 @@ namespace {
 
 constexpr int kThreads = 128;   // warp 0 loads tiles, 1 issues products, 2 loads scales; all store
 
-// kDeep: one CTA an SM with all of its shared memory; else two.  (256 rows: one either way.)
+// kDeep: one CTA an SM with all of its shared memory, else two.  (256 tokens: one.)
 template <int kRows, bool kDeep>
 struct Few {
-  static constexpr int kStages = kRows == 16 ? (kDeep ? 11 : 5) : kRows == 32 ? (kDeep ? 10 : 5) : kRows == 64 ? (kDeep ? 8 : 4)
-                                 : kRows == 128 ? (kDeep ? 6 : 3) : 4;
+  static constexpr int kStages = kRows == 16    ? (kDeep ? 11 : 5)
+                                 : kRows == 32  ? (kDeep ? 10 : 5)
+                                 : kRows == 64  ? (kDeep ? 8 : 4)
+                                 : kRows == 128 ? (kDeep ? 6 : 3)
+                                                : 4;
   static constexpr uint32_t kW = 128 * kStageK, kX = kRows * kStageK, kStage = kW + kX;
   static constexpr int kSets = (kRows + 127) / 128;               // of 128 tokens' scales
   static constexpr uint32_t kScales = 512 * (1 + kSets);          // one slot: weights', tokens'
@@ -34,7 +37,7 @@ struct Few {
   static constexpr uint32_t kBytes = oBars + kBars * 8 + 8, kAlloc = kBytes + 1024;   // + alignment
   static constexpr uint32_t cScales = kRows, kCols = kRows + 2 * 4 * (1 + kSets);      // TMEM columns
   static constexpr uint32_t kTmem = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-  static_assert(kStages * kStage >= kRows * 512, "partial sums take the stages' place");
+  static_assert(kStages * kStage >= kRows * 512 && kBars <= 32 && kAlloc <= 227 * 1024, "shared memory; partial sums take the stages' place");
 };
 
 __device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
@@ -61,11 +64,11 @@ __global__ void __launch_bounds__(kThreads)
   uint64_t *empty = full + F::kStages, *sfull = empty + F::kStages, *sempty = sfull + kScaleSlots, *done = sempty + kScaleSlots;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(done + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t tile = blockIdx.x / split, rank = blockIdx.x - tile * split;
+  const int32_t tile = blockIdx.x / split, part = blockIdx.x - tile * split;   // a cluster a tile, a CTA a part of K
   const int64_t n0 = (int64_t)tile * 128, m0 = (int64_t)blockIdx.y * kRows;
-  // this CTA's K blocks: whole groups of four, whose scales share a word
-  const int32_t groups = (blocks + 3) / 4, kb0 = (int32_t)((int64_t)groups * rank / split) * 4;
-  const int32_t nb = (int32_t)min((int64_t)groups * (rank + 1) / split * 4, (int64_t)blocks) - kb0;
+  // this part's K blocks: whole groups of four, whose scales share a word
+  const int32_t groups = (blocks + 3) / 4, kb0 = (int32_t)((int64_t)groups * part / split) * 4;
+  const int32_t nb = (int32_t)min((int64_t)groups * (part + 1) / split * 4, (int64_t)blocks) - kb0;
 
   // Before the CTA meets: the first loads go out, and the first scales are read.
   const uint32_t at = tc::smem_u32(sm), bar = tc::smem_u32(full);
@@ -115,30 +118,28 @@ __global__ void __launch_bounds__(kThreads)
     const uint64_t dS = desc_scales(tc::smem_u32(sm + F::oScales));
     int st = 0;
     uint32_t phase = 0, cw = tmem + F::cScales;
-    for (int i = 0, g = 0; i < nb && ok; i += 4, ++g) {   // four K blocks, a word of scales
+    long long limit = kWaitLimit;
+    for (int i = 0, g = 0; i < nb; i += 4, ++g) {   // four K blocks, a word of scales
       const int slot = g % kScaleSlots;
       // the products that read these columns, two groups ago, are done
-      ok = (g < 2 || wait_w(sempty + (g - 2) % kScaleSlots, ((g - 2) / kScaleSlots) & 1)) && wait_w(sfull + slot, (g / kScaleSlots) & 1);
-      if (!ok) break;
+      if (g >= 2) wait_lane(sempty + (g - 2) % kScaleSlots, ((g - 2) / kScaleSlots) & 1, limit);
+      wait_lane(sfull + slot, (g / kScaleSlots) & 1, limit);
       tc::tc_fence_after();
 #pragma unroll
       for (int s = 0; s < 1 + F::kSets; ++s) scales_to_tmem_w<1>(cw + 4 * s, dS + ((slot * F::kScales + 512 * s) >> 4));
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         if (i + b >= nb) break;
-        ok = wait_w(full + st, phase);
-        if (!ok) break;
+        wait_lane(full + st, phase, limit);
         tc::tc_fence_after();
-        const uint64_t dw = dW + (st * F::kStage >> 4), dx = dX + (st * F::kStage >> 4);
-#pragma unroll
-        for (int k = 0; k < kStageK / 32; ++k)
-          mma_e4m3_w<1>(tmem, dw + 2 * k, dx + 2 * k, idesc_e4m3(128, kRows) | scale_ids(b), cw, cw + 4, (b > 0 || k > 0) ? 1u : (uint32_t)i);
-        tc::mma_commit_w(empty + st);
+        mma_block_w<1>(tmem, dW + (st * F::kStage >> 4), dX + (st * F::kStage >> 4), idesc_e4m3(128, kRows) | scale_ids(b), cw,
+                               cw + 4, b > 0 ? 1u : (uint32_t)i, empty + st, 0);
         if (++st == F::kStages) st = 0, phase ^= 1;
       }
       tc::mma_commit_w(sempty + slot);
       cw = tmem + F::cScales + ((g + 1) & 1) * 4 * (1 + F::kSets);
     }
+    ok = __all_sync(0xffffffffu, limit != 0);
     tc::mma_commit_w(done);
   } else if (warp == 2) {
     for (int g = 0; 4 * g < nb && ok; ++g) {
@@ -187,36 +188,43 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
   } else {
-    float* part = reinterpret_cast<float*>(sm);   // [kRows][128]
+    float* sums = reinterpret_cast<float*>(sm);   // [kRows][128]
     if (ok) {
 #pragma unroll 1
       for (int c = 0; c < rows; c += 16) {
         float v[16];
         tc::tmem_ld16(td + c, v);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) part[(c + e) * 128 + threadIdx.x] = v[e];
+        for (int e = 0; e < 16; ++e) sums[(c + e) * 128 + threadIdx.x] = v[e];
       }
     }
     tc::cluster_sync_all();
     if (ok) {
-      // this CTA's rows are rank, rank + split, ...: a warp takes four at a time, a lane four columns of each
+      // this CTA's rows are part, part + split, ...: a warp takes eight at a time, a lane four columns of each
+      constexpr int kAt = kRows < 64 ? 4 : 8;
       const int64_t nl = n0 + 4 * lane;
       const int left = (int)(N - nl < 4 ? N - nl : 4);   // columns of this lane
-      const uint32_t mine = tc::smem_u32(part + 4 * lane);
-      for (int r0 = rank + split * 4 * warp; r0 < rows; r0 += split * 4 * (kThreads / 32)) {
-        float4 x[4] = {};
+      const uint32_t from = tc::smem_u32(sums + 4 * lane);
+      for (int r0 = part + split * kAt * warp; r0 < rows; r0 += split * kAt * (kThreads / 32)) {
+        float4 x[kAt] = {};
 #pragma unroll 1
-        for (int s = 0; s < split; ++s) {   // in the order of K
-          const uint32_t from = cluster_address(mine, s);
-          float4 y[4];
+        for (int s = 0; s < split; s += 2) {   // in the order of K, two parts on their way
+          const uint32_t p0 = cluster_address(from, s), p1 = cluster_address(from, min(s + 1, split - 1));
+          float4 y0[kAt], y1[kAt];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) y[j] = ld_cluster(from + min(r0 + split * j, rows - 1) * 512);
+          for (int j = 0; j < kAt; ++j) y0[j] = ld_cluster(p0 + min(r0 + split * j, rows - 1) * 512);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[j].x += y[j].x, x[j].y += y[j].y, x[j].z += y[j].z, x[j].w += y[j].w;
+          for (int j = 0; j < kAt; ++j) y1[j] = ld_cluster(p1 + min(r0 + split * j, rows - 1) * 512);
+#pragma unroll
+          for (int j = 0; j < kAt; ++j) x[j].x += y0[j].x, x[j].y += y0[j].y, x[j].z += y0[j].z, x[j].w += y0[j].w;
+          if (s + 1 < split) {
+#pragma unroll
+            for (int j = 0; j < kAt; ++j) x[j].x += y1[j].x, x[j].y += y1[j].y, x[j].z += y1[j].z, x[j].w += y1[j].w;
+          }
         }
         T* y = out + (m0 + r0) * ldo + nl;
 #pragma unroll
-        for (int j = 0; j < 4; ++j, y += split * ldo) {
+        for (int j = 0; j < kAt; ++j, y += split * ldo) {
           if (r0 + split * j >= rows) break;
           if (quads && left == 4) {
             if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(y) = make_uint2(bf16x2(x[j].x, x[j].y), bf16x2(x[j].z, x[j].w));
@@ -230,10 +238,10 @@ __global__ void __launch_bounds__(kThreads)
         }
       }
     }
-    cluster_meet();   // no CTA leaves while another reads its sums
   }
   tc::tc_fence_before();
   __syncthreads();
+  if (split > 1) cluster_meet();   // no CTA leaves while another reads its sums
   if (warp == 1) tc::tmem_dealloc(tmem, F::kTmem);
 }
 
@@ -265,13 +273,13 @@ cudaError_t launch_few(const MatmulProblem& p, int split, cudaStream_t stream) {
 }
 
 // How the product is cut, by the time in microseconds that it is expected to take.  The constants are fitted to 160
-// sizes (1 to 2,048 rows, N 512 to 16,416, K 512 to 12,288) with every cut timed, 1,900 times in all: they are within
-// 10 % of the times on average, and the cut that they pick is 0.8 % slower than the fastest on average, 10 % at most.
+// sizes (1 to 2,048 rows, N 512 to 16,416, K 512 to 12,288) with every cut timed, 905 times in all: they are within
+// 10 % of the times on average, and the cut that they pick is 0.9 % slower than the fastest on average, 11 % at most.
 //   few rows:  a fixed part; then waves of CTAs, a K block of each at so many KB through its SM, and its output; or the
 //              bytes of HBM if that takes longer; then the join of the parts of K.
-//   pairs:     a fixed part; waves of pairs, 0.3 us a K block; or the bytes.
+//   pairs:     a fixed part; waves of pairs, 0.29 us a K block; or the bytes.
 struct Cut {
-  int rows, split;   // rows 0: pairs
+  int rows, split;   // rows 0: the kernel of many rows
   bool deep;
 };
 Cut choose(const MatmulProblem& p, int sms) {
@@ -281,7 +289,7 @@ Cut choose(const MatmulProblem& p, int sms) {
   const auto waves = [](int64_t n, int64_t room) { return (float)((n + room - 1) / room); };
   const int64_t pairs = ((p.M + 255) / 256) * ((p.N + 239) / 240);
   Cut best{0, 1, true};
-  float least = 5.7f + std::max(hbm, waves(pairs, sms / 2) * std::max(0.3f * blocks, 0.9f));
+  float least = 4.6f + std::max(hbm, waves(pairs, sms / 2) * std::max(0.29f * blocks, 0.65f));
   for (int rows = 16; rows <= 256; rows *= 2) {
     const int64_t mt = (p.M + rows - 1) / rows;
     if (mt > 65535) continue;   // a grid's limit
@@ -290,9 +298,9 @@ Cut choose(const MatmulProblem& p, int sms) {
       if (ctas > INT32_MAX) continue;
       const bool deep = ctas <= sms, one = deep || rows == 256;   // one CTA an SM, or two
       const float kb = (float)std::min<int64_t>((int64_t)blocks, 4 * ((groups + split - 1) / split)), stage = 16.f + (float)rows / 8.f;
-      const float work = kb * (one ? 0.006f * stage + 0.056f : 0.0131f * stage + 0.052f) + 0.9f + 0.0065f * (float)rows;
-      const float join = split == 1 ? 0.f : 0.06f + 0.022f * (float)rows + 0.37f * (float)split;
-      const float t = 2.3f + std::max(hbm, waves(ctas, one ? sms : 2 * sms) * work) + join;
+      const float work = kb * (one ? 0.006f * stage + 0.038f : 0.0124f * stage + 0.063f) + 0.8f + 0.0118f * (float)rows;
+      const float join = split == 1 ? 0.f : 0.2f + 0.016f * (float)rows + 0.29f * (float)split;
+      const float t = 2.f + std::max(hbm, waves(ctas, one ? sms : 2 * sms) * work) + join;
       if (t < least) least = t, best = Cut{rows, split, deep};
     }
   }

@@ -35,28 +35,6 @@ constexpr int kGroupM = 8;              // tiles are taken in bands of so many r
 static_assert(kAlloc <= 227 * 1024 && 32 * kTurnRow * 4 <= 2 * kPiece && oOut % 128 == 0, "shared memory");
 
 // ------------------------------------------------------------- forms for a pair of CTAs
-// Arrival on an mbarrier of the cluster (address from mapa_shared), released at CTA scope: what it orders lies in
-// this CTA's own shared memory (behind a proxy fence) or TMEM.  (A release at cluster scope costs about 1,000 cycles.)
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// Arrive at this barrier of both CTAs once every MMA issued so far by the elected lane has completed.
-__device__ __forceinline__ void commit_both_w(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred pe;\n\t.reg .b16 m;\n\t"
-      "mov.b16 m, 3;\n\t"
-      "elect.sync _|pe, 0xffffffff;\n\t"
-      "@pe tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(tc::smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::smem_u32(dst)) : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_free_pair(uint32_t taddr) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
-}
-
 // 8 columns of TMEM, not there before tmem_ld_end has waited for them.
 __device__ __forceinline__ void tmem_ld8_begin(uint32_t taddr, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -153,7 +131,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 2) {
     load_words(pair, 0);
   } else if (warp == 3) {
-    tmem_alloc_pair(tmem_at);
+    tmem_alloc_pair(tmem_at, 512);
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -184,35 +162,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint64_t dS = desc_scales(tc::smem_u32(sm + oScales));
       int st = 0, it = 0;
       uint32_t phase = 0, g = 0;
-      for (uint32_t t = pair; t < tiles && ok; t += pairs, ++it) {
+      long long limit = kWaitLimit;
+      for (uint32_t t = pair; t < tiles; t += pairs, ++it) {
         const uint32_t acc = tmem + (it & 1) * kTN;
-        if (it >= 2 && !(ok = wait_w(tempty + (it & 1), ((it >> 1) - 1) & 1))) break;
-        tc::tc_fence_after();
-        for (int32_t k0 = 0; k0 < blocks && ok; k0 += 4, ++g) {   // four K blocks, a word of scales
+        if (it >= 2) wait_lane(tempty + (it & 1), ((it >> 1) - 1) & 1, limit);
+        for (int32_t k0 = 0; k0 < blocks; k0 += 4, ++g) {   // four K blocks, a word of scales
           const uint32_t slot = g % kScaleSlots, ca = tmem + cScales + (g & 1) * 12, cb = ca + 4;
           // the products that read these columns, two groups ago, are done
-          if (g >= 2 && !(ok = wait_w(sempty + (g - 2) % kScaleSlots, ((g - 2) / kScaleSlots) & 1))) break;
-          if (!(ok = wait_w(sfull + slot, (g / kScaleSlots) & 1))) break;
+          if (g >= 2) wait_lane(sempty + (g - 2) % kScaleSlots, ((g - 2) / kScaleSlots) & 1, limit);
+          wait_lane(sfull + slot, (g / kScaleSlots) & 1, limit);
           tc::tc_fence_after();
 #pragma unroll
           for (int s = 0; s < 3; ++s) scales_to_tmem_w<2>(ca + 4 * s, dS + ((slot * kScales + 512 * s) >> 4));
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
             if (k0 + b >= blocks) break;
-            if (!(ok = wait_w(full + st, phase))) break;
+            wait_lane(full + st, phase, limit);
             tc::tc_fence_after();
-            const uint64_t da = dA + (st * kStage >> 4), db = dB + (st * kStage >> 4);
-#pragma unroll
-            for (int k = 0; k < kStageK / 32; ++k)
-              mma_e4m3_w<2>(acc, da + 2 * k, db + 2 * k, idesc_e4m3(kTM, kTN) | scale_ids(b), ca, cb, (b > 0 || k > 0) ? 1u : (uint32_t)k0);
-            commit_both_w(empty + st);
+            mma_block_w<2>(acc, dA + (st * kStage >> 4), dB + (st * kStage >> 4), idesc_e4m3(kTM, kTN) | scale_ids(b), ca, cb,
+                           b > 0 ? 1u : (uint32_t)k0, empty + st, 3u);
             if (++st == kStages) st = 0, phase ^= 1;
           }
-          if (ok) commit_both_w(sempty + slot);
+          commit_both_w(sempty + slot, 3u);
         }
-        if (!ok) break;
-        commit_both_w(tfull + (it & 1));
+        commit_both_w(tfull + (it & 1), 3u);
       }
+      ok = __all_sync(0xffffffffu, limit != 0);
       for (int i = it > 2 ? it - 2 : 0; i < it; ++i) ok = wait_w(tempty + (i & 1), (i >> 1) & 1) && ok;
     }
   } else if (warp == 2) {
@@ -310,7 +285,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_meet();   // both CTAs are done with one another's barriers and TMEM
   tc::tc_fence_after();
-  if (warp == 3) tmem_free_pair(tmem);
+  if (warp == 3) tmem_free_pair(tmem, 512);
 }
 
 template <typename T>

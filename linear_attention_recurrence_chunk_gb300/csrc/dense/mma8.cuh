@@ -40,25 +40,43 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
   return d;
 }
 
-// Warp-level forms as in tc_ptx.cuh: all 32 lanes with uniform operands, one elected lane issues.
+// The products of a K block (four K = 32 steps, 32 bytes apart in both operands; the first adds to D when accumulate != 0,
+// the others always), then an arrival on `bar` when they are done (kGroup 2: of both CTAs, mask: their ranks in the
+// cluster).  Warp-level as in tc_ptx.cuh: all 32 lanes with uniform operands, one elected lane issues; one election for
+// all five, since each costs as much as an issue (400 -> 250 cycles a K block with the wait for it).
 template <int kGroup>
-__device__ __forceinline__ void mma_e4m3_w(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sa_tmem,
-                                           uint32_t sb_tmem, uint32_t accumulate) {
+__device__ __forceinline__ void mma_block_w(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sa_tmem, uint32_t sb_tmem,
+                                            uint32_t accumulate, uint64_t* bar, uint32_t mask) {
   if constexpr (kGroup == 1) {
     asm volatile(
-        "{\n\t.reg .pred p, pe;\n\t"
+        "{\n\t.reg .pred p, q, pe;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
+        "setp.eq.u32 q, 0, 0;\n\t"
+        "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+        "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
         "elect.sync _|pe, 0xffffffff;\n\t"
-        "@pe tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        "@pe tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t"
+        "@pe tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a1, b1, %3, [%4], [%5], q;\n\t"
+        "@pe tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a2, b2, %3, [%4], [%5], q;\n\t"
+        "@pe tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a3, b3, %3, [%4], [%5], q;\n\t"
+        "@pe tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%7];\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate), "r"(tc::smem_u32(bar))
         : "memory");
   } else {
     asm volatile(
-        "{\n\t.reg .pred p, pe;\n\t"
+        "{\n\t.reg .pred p, q, pe;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t.reg .b16 m;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
+        "setp.eq.u32 q, 0, 0;\n\t"
+        "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+        "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
         "elect.sync _|pe, 0xffffffff;\n\t"
-        "@pe tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        "@pe tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t"
+        "@pe tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a1, b1, %3, [%4], [%5], q;\n\t"
+        "@pe tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a2, b2, %3, [%4], [%5], q;\n\t"
+        "@pe tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a3, b3, %3, [%4], [%5], q;\n\t"
+        "cvt.u16.u32 m, %8;\n\t"
+        "@pe tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%7], m;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate), "r"(tc::smem_u32(bar)), "r"(mask)
         : "memory");
   }
 }
@@ -82,6 +100,11 @@ __device__ __forceinline__ void scales_to_tmem_w(uint32_t tmem, uint64_t desc) {
   }
 }
 
+// Wait of a warp whose next step brings it together again (an election): each lane asks and keeps its own answer.
+// After a wait that ran out the next ones do not wait (`limit` is 0 then), so that the warp comes to its end.
+__device__ __forceinline__ void wait_lane(uint64_t* bar, uint32_t parity, long long& limit) {
+  if (!tc::mbar_wait(bar, parity, limit)) limit = 0;
+}
 // Wait of a whole warp; every lane asks (a branch for one lane costs some 500 cycles before the warp is together again).
 __device__ __forceinline__ bool wait_w(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, kWaitLimit));
@@ -120,6 +143,29 @@ __device__ __forceinline__ void expect_w(uint32_t bar, uint32_t bytes) {
 // loads are on their way).
 __device__ __forceinline__ void cluster_meet() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// Arrival on an mbarrier of the cluster (address from mapa_shared), released at CTA scope: what it orders lies in
+// this CTA's own shared memory (behind a proxy fence) or TMEM.  (A release at cluster scope costs about 1,000 cycles.)
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Arrive at this barrier of both CTAs (mask: their ranks in the cluster) once every MMA issued so far by the elected lane has completed.
+__device__ __forceinline__ void commit_both_w(uint64_t* bar, uint32_t mask) {
+  asm volatile(
+      "{\n\t.reg .pred pe;\n\t.reg .b16 m;\n\t"
+      "cvt.u16.u32 m, %1;\n\t"
+      "elect.sync _|pe, 0xffffffff;\n\t"
+      "@pe tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(tc::smem_u32(bar)),
+      "r"(mask)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(dst)), "r"(cols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free_pair(uint32_t taddr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
 }
 
 constexpr int kScaleSlots = 4;   // groups of four K blocks whose scales are on their way (two of them in TMEM)
