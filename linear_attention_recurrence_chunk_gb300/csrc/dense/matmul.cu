@@ -274,10 +274,11 @@ cudaError_t launch_few(const MatmulProblem& p, int split, cudaStream_t stream) {
 
 // How the product is cut, by the time in microseconds that it is expected to take.  The constants are fitted to 160
 // sizes (1 to 2,048 rows, N 512 to 16,416, K 512 to 12,288) with every cut timed, 905 times in all: they are within
-// 10 % of the times on average, and the cut that they pick is 0.9 % slower than the fastest on average, 11 % at most.
-//   few rows:  a fixed part; then waves of CTAs, a K block of each at so many KB through its SM, and its output; or the
-//              bytes of HBM if that takes longer; then the join of the parts of K.
-//   pairs:     a fixed part; waves of pairs, 0.29 us a K block; or the bytes.
+// 7 % of the times on average, and the cut that they pick is 0.2 % slower than the fastest on average, 7 % at most.
+//   few rows:  a fixed part; waves of CTAs, a K block of each at so many KB through its SM, and its output; then the
+//              join of the parts of K.
+//   pairs:     a fixed part; waves of pairs, 0.255 us a K block.
+// The waves and the bytes of HBM overlap but for a part of the shorter.
 struct Cut {
   int rows, split;   // rows 0: the kernel of many rows
   bool deep;
@@ -285,22 +286,27 @@ struct Cut {
 Cut choose(const MatmulProblem& p, int sms) {
   const int64_t groups = (p.K + 4 * kStageK - 1) / (4 * kStageK), tiles = (p.N + 127) / 128;
   const float blocks = (float)((p.K + kStageK - 1) / kStageK), out = p.dt == KDA_F32 ? 4.f : 2.f;
-  const float hbm = (((float)p.M + (float)p.N) * (float)p.K + out * (float)p.M * (float)p.N) / 6.6e6f;
+  const float hbm = (((float)p.M + (float)p.N) * (float)p.K + out * (float)p.M * (float)p.N) / 6.82e6f;
   const auto waves = [](int64_t n, int64_t room) { return (float)((n + room - 1) / room); };
+  const auto both = [&](float work) { return std::max(hbm, work) + 0.272f * std::min(hbm, work); };
   const int64_t pairs = ((p.M + 255) / 256) * ((p.N + 239) / 240);
   Cut best{0, 1, true};
-  float least = 4.6f + std::max(hbm, waves(pairs, sms / 2) * std::max(0.29f * blocks, 0.65f));
+  float least = 4.97f + both(waves(pairs, sms / 2) * 0.255f * blocks);
   for (int rows = 16; rows <= 256; rows *= 2) {
     const int64_t mt = (p.M + rows - 1) / rows;
     if (mt > 65535) continue;   // a grid's limit
     for (int split = 1; split <= 8 && split <= groups; split *= 2) {
       const int64_t ctas = tiles * mt * split;
       if (ctas > INT32_MAX) continue;
-      const bool deep = ctas <= sms, one = deep || rows == 256;   // one CTA an SM, or two
+      // CTAs that run at once, one an SM or two, by clusters: 152, 152, 144, 120 and 304, 304, 296, 288 on GB300's 152 SMs
+      // (cudaOccupancyMaxActiveClusters)
+      const int room1 = split <= 2 ? sms : split == 4 ? sms * 18 / 19 : sms * 15 / 19;
+      const int room2 = split <= 2 ? 2 * sms : split == 4 ? 2 * sms * 37 / 38 : 2 * sms * 18 / 19;
+      const bool deep = ctas <= room1, one = deep || rows == 256;
       const float kb = (float)std::min<int64_t>((int64_t)blocks, 4 * ((groups + split - 1) / split)), stage = 16.f + (float)rows / 8.f;
-      const float work = kb * (one ? 0.006f * stage + 0.038f : 0.0124f * stage + 0.063f) + 0.8f + 0.0118f * (float)rows;
-      const float join = split == 1 ? 0.f : 0.2f + 0.016f * (float)rows + 0.29f * (float)split;
-      const float t = 2.f + std::max(hbm, waves(ctas, one ? sms : 2 * sms) * work) + join;
+      const float work = kb * (one ? 0.00563f * stage + 0.0378f : 0.0119f * stage + 0.0344f) + 0.422f + 0.0122f * (float)rows;
+      const float join = split == 1 ? 0.f : 0.148f + 0.017f * (float)rows + 0.278f * (float)split;
+      const float t = 2.22f + both(waves(ctas, one ? room1 : room2) * work) + join;
       if (t < least) least = t, best = Cut{rows, split, deep};
     }
   }

@@ -41,7 +41,8 @@ SIZES = [(1, 1, 16), (1, 128, 128), (1, 2052, 512), (3, 300, 1040), (8, 513, 409
          (4096, 4096, 528), (3000, 5000, 2048),
          # each way of cutting the product that the choice by sizes has: rows of a tile, parts of K, one or two CTAs an SM
          (2, 6188, 2624), (42, 21, 15280), (1122, 514, 64), (52, 561, 15056), (6687, 62, 2784), (159, 2068, 6912), (1363, 54, 8800),
-         (611, 16, 16048), (2357, 2519, 80), (6705, 108, 8864), (2749, 18, 11040), (1075, 7427, 2960), (10542, 19, 2496), (322, 8610, 48), (2657, 713, 14704), (1586, 400, 15472)]
+         (611, 16, 16048), (2357, 2519, 80), (6705, 108, 8864), (2749, 18, 11040), (1075, 7427, 2960), (10542, 19, 2496), (322, 8610, 48), (2657, 713, 14704), (1586, 400, 15472),
+         (131, 2192, 11472), (138, 17775, 10368), (3758, 579, 14768), (2243, 84, 4336), (66, 5494, 11264)]
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
