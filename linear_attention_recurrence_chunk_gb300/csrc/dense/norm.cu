@@ -118,6 +118,115 @@ __global__ void __launch_bounds__(kOneWarp ? 32 * kRowsPerBlock : 1024)
   }
 }
 
+// Rows of at most 128 values (a head's channels): the least power of two L of lanes that holds one at eight values a lane,
+// so 32 / L rows a warp, and two such sets of rows at once.  kWide: lane l of a row has columns 8 l ..; else l, l + L, ...
+constexpr int kNarrow = 128, kSets = 2;
+
+template <typename T, bool kAdd, bool kFp8, bool kWide>
+__global__ void __launch_bounds__(32 * kRowsPerBlock)
+    add_rmsnorm_narrow_kernel(const T* x, int64_t xs, const T* r, int64_t rs, const float* __restrict__ w, float eps0, int64_t rows, int32_t C,
+                              int32_t L, T* h, T* y, uint8_t* codes, uint8_t* scales) {
+  const int lane = threadIdx.x & 31, l = lane & (L - 1), per_warp = 32 / L;
+  const int64_t row0 = ((int64_t)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 5)) * (kSets * per_warp) + lane / L;
+  const auto column = [&](int i) { return kWide ? 8 * l + i : l + L * i; };
+  const auto load = [&](Eight<T, kWide>& v, const T* row) {
+    if constexpr (kWide) {
+      v.load(row, 0, C, l);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v.x[i] = column(i) < C ? row[column(i)] : from_f32<T>(0.f);
+    }
+  };
+  const auto store = [&](T* row, const float(&v)[8]) {
+    if constexpr (kWide) {
+      store8<T, true>(row, 0, C, l, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (column(i) < C) row[column(i)] = from_f32<T>(v[i]);
+    }
+  };
+  Eight<T, kWide> a[kSets], b[kAdd ? kSets : 1];
+#pragma unroll
+  for (int j = 0; j < kSets; ++j) {
+    const int64_t at = min(row0 + j * per_warp, rows - 1);   // (the last row again behind it: not stored)
+    load(a[j], x + at * xs);
+    if constexpr (kAdd) load(b[j], r + at * rs);
+  }
+  float g[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) g[i] = w && column(i) < C ? __ldg(w + column(i)) : 1.f;
+#pragma unroll
+  for (int j = 0; j < kSets; ++j) {
+    const int64_t row = row0 + j * per_warp;
+    const bool live = row < rows;
+    float v[8], eps = eps0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = kAdd ? a[j].at(i) + b[j].at(i) : a[j].at(i);
+    if constexpr (kAdd)
+      if (live) store(h + row * C, v);
+    const auto squares = [&]() {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s = fmaf(v[i], v[i], s);
+      for (int m = L >> 1; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+      return s;
+    };
+    float ss = squares();
+    // as in add_rmsnorm_kernel, each row for itself
+    const bool high = !(ss < __uint_as_float(0x7f800000u)), low = ss < 0x1p-60f && eps0 < 0x1p-100f;
+    if (__any_sync(0xffffffffu, high || low)) {
+      const float f = high ? 0x1p-80f : low ? 0x1p80f : 1.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= f;
+      eps = high ? 0.f : low ? eps0 * 0x1p80f * 0x1p80f : eps0;
+      ss = squares();
+    }
+    const float inv = 1.0f / sqrtf(ss / (float)C + eps);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = column(i) < C ? v[i] * inv * g[i] : 0.f;
+    if constexpr (kFp8) {
+      uint32_t top = __float_as_uint(top3(top3(v[0], v[1], v[2]), top3(v[3], v[4], v[5]), top2(v[6], v[7])));
+      for (int m = L >> 1; m > 0; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+      const uint32_t byte = scale_byte(top);
+      const uint2 c = codes8(v, byte, byte);
+      if (live) {
+        uint8_t* to = codes + row * C;
+        if constexpr (kWide) {
+          store_codes<true>(to, 0, C, l, c);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (column(i) < C) to[column(i)] = (uint8_t)((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
+        }
+        if (l == 0) scales[row] = (uint8_t)byte;
+      }
+    } else if (live) {
+      store(y + row * C, v);
+    }
+  }
+}
+
+template <typename T, bool kWide>
+cudaError_t launch_narrow(const NormProblem& p, cudaStream_t stream) {
+  int L = 1;
+  while (8 * L < p.C) L *= 2;
+  const int64_t per_block = (int64_t)kRowsPerBlock * kSets * (32 / L);
+  auto go = [&](auto add, auto fp8) {
+    add_rmsnorm_narrow_kernel<T, decltype(add)::value, decltype(fp8)::value, kWide>
+        <<<(unsigned)((p.T + per_block - 1) / per_block), 32 * kRowsPerBlock, 0, stream>>>(
+            static_cast<const T*>(p.x), p.xs, static_cast<const T*>(p.r), p.rs, p.w, p.eps, p.T, (int32_t)p.C, L, static_cast<T*>(p.h),
+            static_cast<T*>(p.y), p.codes, p.scales);
+  };
+  const std::true_type yes;
+  const std::false_type no;
+  prof_begin(stream, "add_rmsnorm_narrow_kernel");
+  if (p.r) p.codes ? go(yes, yes) : go(yes, no);
+  else p.codes ? go(no, yes) : go(no, no);
+  prof_end(stream);
+  return cudaGetLastError();
+}
+
 template <typename T, int J, bool kAdd, bool kFp8, bool kWide>
 cudaError_t launch4(const NormProblem& p, int warps, cudaStream_t stream) {
   auto go = [&](auto one) {
@@ -146,6 +255,7 @@ cudaError_t launch1(const NormProblem& p, cudaStream_t stream) {
   const int64_t step = 16 / sizeof(T);
   const bool wide = p.C % 8 == 0 && p.xs % step == 0 && at(p.x, 16) && (!p.r || (p.rs % step == 0 && at(p.r, 16) && at(p.h, 16))) &&
                     at(p.w, 16) && (p.codes ? at(p.codes, 8) : at(p.y, 16));
+  if (p.C <= kNarrow) return wide ? launch_narrow<T, true>(p, stream) : launch_narrow<T, false>(p, stream);
   const int chunks = (int)((p.C + 255) / 256);   // 256 columns each, at most 128
   // One or two chunks: a warp a row.  Else two a warp, four where 32 warps are not enough and for 8-bit output of
   // many rows (32,768 x 4,096: 157 us with two, 143 with four; 16,384 x 8,192: 182 and 147; but 1 x 4,096: 3.0 and

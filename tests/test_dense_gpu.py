@@ -97,7 +97,7 @@ def _norm_tol(y, dt):
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("add", [False, True])
-@pytest.mark.parametrize("T,C", [(1, 1), (1, 7), (9, 16), (6, 129), (5, 256), (3, 257), (17, 512), (64, 1001), (5, 4096), (3, 12288), (2, 16385),
+@pytest.mark.parametrize("T,C", [(1, 1), (1, 7), (9, 16), (33, 8), (70, 12), (300, 24), (129, 64), (1000, 100), (65, 128), (41, 127), (6, 129), (5, 256), (3, 257), (17, 512), (64, 1001), (5, 4096), (3, 12288), (2, 16385),
                                  (1, 32768)])
 def test_norm(T, C, add, dt):
     x, r = _rows(T, C, dt, T * C), _rows(T, C, dt, T * C + 1) if add else None
@@ -125,7 +125,7 @@ def test_norm(T, C, add, dt):
     assert kda.kda_device_error() == (0, 0)
 
 
-@pytest.mark.parametrize("C", [64, 300, 4096])
+@pytest.mark.parametrize("C", [64, 27, 300, 4096])
 def test_norm_range(C):
     """Squares beyond fp32's range and below it, rows of zeros, eps of 0, values that are not finite."""
     x = _rows(8, C, "f32", 9).numpy()
