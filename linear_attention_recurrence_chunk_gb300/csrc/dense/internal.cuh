@@ -12,6 +12,32 @@ namespace dense {
 
 constexpr int kBlock = 128;   // columns of a scale
 
+// -------------------------------------------------------------- launches one behind another
+// Every kernel here is launched so that it may start while the one before it in the stream ends (about 1 us less from
+// kernel to kernel; a product of one row, 16,416 x 4,096: 15.6 -> 13.0 us a call): it lets the next one start at once, and
+// touches no global memory before all that ran before it is complete and visible.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// cluster: CTAs of a cluster, 0 for none or what the kernel itself says.
+template <typename... P, typename... A>
+cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // ------------------------------------------------------------------ 8-bit values
 // Scale byte of a block whose largest |value| has the fp32 bits `top`: the exponent field b
 // of the least 2^(b - 127), b >= 1, with top <= 448 * 2^(b - 127); 255 for an inf or NaN.

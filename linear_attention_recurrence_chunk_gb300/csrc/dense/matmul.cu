@@ -86,14 +86,21 @@ __global__ void __launch_bounds__(kThreads)
       return r < kRows && m0 + r < M ? m0 + r : (int64_t)-1;
     });
   };
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_start();
   if (warp == 0) {
     if (lane < F::kBars) tc::mbar_init(full + lane, 1);
     tc::fence_mbar_init();
+    tc::tma_prefetch_desc(&mapW);
+    tc::tma_prefetch_desc(&mapX);
     __syncwarp();
-    for (int i = 0; i < first; ++i) load_tile(i, i);
   } else if (warp == 1) {
     tc::tmem_alloc(tmem_at, F::kTmem);
     tc::tmem_relinquish();
+  }
+  wait_for_previous();
+  if (warp == 0) {
+    for (int i = 0; i < first; ++i) load_tile(i, i);
   } else if (warp == 2) {
     load_words(0);
   }
@@ -252,22 +259,12 @@ cudaError_t launch_few(const MatmulProblem& p, int split, cudaStream_t stream) {
   if (!codes_map(&mw, p.w, p.N, p.K, p.ldw, 128) || !codes_map(&mx, p.a, p.M, p.K, p.lda, kRows)) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(fp8_matmul_few_kernel<kRows, kDeep, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F::kAlloc);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((p.N + 127) / 128 * split), (unsigned)((p.M + kRows - 1) / kRows));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = F::kAlloc;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)split;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
+  const int32_t blocks = (int32_t)((p.K + kStageK - 1) / kStageK);
   const bool quads = reinterpret_cast<uintptr_t>(p.out) % (4 * sizeof(T)) == 0 && p.ldo % 4 == 0;   // four columns a store
   prof_begin(stream, "fp8_matmul_few_kernel");
-  e = cudaLaunchKernelEx(&cfg, fp8_matmul_few_kernel<kRows, kDeep, T>, mw, mx, p.sw, p.sa, p.M, p.N, (int32_t)((p.K + kStageK - 1) / kStageK),
-                         static_cast<T*>(p.out), p.ldo, (int32_t)quads,
-                         (int32_t)scale_words(p.sa, p.sw, (p.K + kStageK - 1) / kStageK), (int32_t)split, p.dev_err);
+  e = launch_kernel(fp8_matmul_few_kernel<kRows, kDeep, T>,
+                    dim3((unsigned)((p.N + 127) / 128 * split), (unsigned)((p.M + kRows - 1) / kRows)), kThreads, F::kAlloc, split, stream, mw, mx,
+                    p.sw, p.sa, p.M, p.N, blocks, static_cast<T*>(p.out), p.ldo, quads, scale_words(p.sa, p.sw, blocks), split, p.dev_err);
   prof_end(stream);
   return e;
 }

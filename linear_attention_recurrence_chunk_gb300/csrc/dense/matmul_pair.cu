@@ -116,22 +116,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_load_w<2>(at + st * kStage + kA, &mapB, kb * kStageK, yb, lead + 8 * st);
   };
   const int early = rank == 0 ? min(blocks, kStages) : 0;   // of the first tile
+  let_next_start();
   if (warp == 0) {
     if (lane < kBars) {   // in the order of their declaration: full, empty, sfull, sempty, tfull, tempty
       const int i = lane - 2 * kStages - kScaleSlots;
       tc::mbar_init(full + lane, i < -kScaleSlots ? 1 : i < 0 ? 2 : i < kScaleSlots + 2 ? 1 : 8);
     }
     tc::fence_mbar_init();
+    tc::tma_prefetch_desc(&mapA);
+    tc::tma_prefetch_desc(&mapB);
     __syncwarp();
-    if (early > 0) {
-      uint32_t im, in;
-      place(pair, tm, tn, im, in);
-      for (int kb = 0; kb < early; ++kb) load_tile(kb, kb, (int32_t)(im * kTM), (int32_t)(in * kTN));
-    }
-  } else if (warp == 2) {
-    load_words(pair, 0);
   } else if (warp == 3) {
     tmem_alloc_pair(tmem_at, 512);
+  }
+  wait_for_previous();
+  if (warp == 0 && early > 0) {
+    uint32_t im, in;
+    place(pair, tm, tn, im, in);
+    for (int kb = 0; kb < early; ++kb) load_tile(kb, kb, (int32_t)(im * kTM), (int32_t)(in * kTN));
+  } else if (warp == 2) {
+    load_words(pair, 0);
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -294,6 +298,7 @@ cudaError_t launch(const MatmulProblem& p, int sms, cudaStream_t stream) {
   if (!codes_map(&ma, p.a, p.M, p.K, p.lda, 128) || !codes_map(&mb, p.w, p.N, p.K, p.ldw, kTN / 2)) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(fp8_matmul_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAlloc);
   if (e != cudaSuccess) return e;
+  const int32_t blocks = (int32_t)((p.K + kStageK - 1) / kStageK);
   const int64_t tm = (p.M + kTM - 1) / kTM, tn = (p.N + kTN - 1) / kTN;
   // rows that begin on 16-byte boundaries leave by tensor stores
   const bool wide = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && (size_t)p.ldo * sizeof(T) % 16 == 0;
@@ -302,11 +307,10 @@ cudaError_t launch(const MatmulProblem& p, int sms, cudaStream_t stream) {
   if (tm * tn > INT32_MAX) return cudaErrorInvalidValue;   // (2^44 products of a K: no memory holds them)
   const unsigned grid = 2 * (unsigned)std::min<int64_t>(tm * tn, sms / 2);
   prof_begin(stream, "fp8_matmul_pair_kernel");
-  fp8_matmul_pair_kernel<T><<<grid, kThreads, kAlloc, stream>>>(ma, mb, mo, p.sa, p.sw, p.M, p.N, (int32_t)((p.K + kStageK - 1) / kStageK), (uint32_t)tm, (uint32_t)tn,
-                                                               static_cast<T*>(p.out), p.ldo, (int32_t)wide,
-                                                               scale_words(p.sa, p.sw, (p.K + kStageK - 1) / kStageK), p.dev_err);
+  e = launch_kernel(fp8_matmul_pair_kernel<T>, dim3(grid), kThreads, kAlloc, 0, stream, ma, mb, mo, p.sa, p.sw, p.M, p.N, blocks, tm, tn,
+                    static_cast<T*>(p.out), p.ldo, wide, scale_words(p.sa, p.sw, blocks), p.dev_err);
   prof_end(stream);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace

@@ -40,6 +40,8 @@ __global__ void __launch_bounds__(kOneWarp ? 32 * kRowsPerBlock : 1024)
     add_rmsnorm_kernel(const T* x, int64_t xs, const T* r, int64_t rs, const float* __restrict__ w, float eps,
                        int64_t rows, int64_t C, T* h, T* y, uint8_t* codes, uint8_t* scales) {
   __shared__ float part[32];
+  let_next_start();
+  wait_for_previous();
   const int lane = threadIdx.x & 31, warp = kOneWarp ? 0 : threadIdx.x >> 5, W = kOneWarp ? 1 : blockDim.x >> 5;
   const int64_t row = kOneWarp ? (int64_t)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 5) : blockIdx.x;
   if (kOneWarp && row >= rows) return;
@@ -126,6 +128,8 @@ template <typename T, bool kAdd, bool kFp8, bool kWide>
 __global__ void __launch_bounds__(32 * kRowsPerBlock)
     add_rmsnorm_narrow_kernel(const T* x, int64_t xs, const T* r, int64_t rs, const float* __restrict__ w, float eps0, int64_t rows, int32_t C,
                               int32_t L, T* h, T* y, uint8_t* codes, uint8_t* scales) {
+  let_next_start();
+  wait_for_previous();
   const int lane = threadIdx.x & 31, l = lane & (L - 1), per_warp = 32 / L;
   const int64_t row0 = ((int64_t)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 5)) * (kSets * per_warp) + lane / L;
   const auto column = [&](int i) { return kWide ? 8 * l + i : l + L * i; };
@@ -213,34 +217,30 @@ cudaError_t launch_narrow(const NormProblem& p, cudaStream_t stream) {
   while (8 * L < p.C) L *= 2;
   const int64_t per_block = (int64_t)kRowsPerBlock * kSets * (32 / L);
   auto go = [&](auto add, auto fp8) {
-    add_rmsnorm_narrow_kernel<T, decltype(add)::value, decltype(fp8)::value, kWide>
-        <<<(unsigned)((p.T + per_block - 1) / per_block), 32 * kRowsPerBlock, 0, stream>>>(
-            static_cast<const T*>(p.x), p.xs, static_cast<const T*>(p.r), p.rs, p.w, p.eps, p.T, (int32_t)p.C, L, static_cast<T*>(p.h),
-            static_cast<T*>(p.y), p.codes, p.scales);
+    return launch_kernel(add_rmsnorm_narrow_kernel<T, decltype(add)::value, decltype(fp8)::value, kWide>, dim3((unsigned)((p.T + per_block - 1) / per_block)),
+                         32 * kRowsPerBlock, 0, 0, stream, static_cast<const T*>(p.x), p.xs, static_cast<const T*>(p.r), p.rs, p.w, p.eps, p.T, p.C, L,
+                         static_cast<T*>(p.h), static_cast<T*>(p.y), p.codes, p.scales);
   };
   const std::true_type yes;
   const std::false_type no;
   prof_begin(stream, "add_rmsnorm_narrow_kernel");
-  if (p.r) p.codes ? go(yes, yes) : go(yes, no);
-  else p.codes ? go(no, yes) : go(no, no);
+  const cudaError_t e = p.r ? (p.codes ? go(yes, yes) : go(yes, no)) : (p.codes ? go(no, yes) : go(no, no));
   prof_end(stream);
-  return cudaGetLastError();
+  return e;
 }
 
 template <typename T, int J, bool kAdd, bool kFp8, bool kWide>
 cudaError_t launch4(const NormProblem& p, int warps, cudaStream_t stream) {
   auto go = [&](auto one) {
     constexpr bool kOne = decltype(one)::value;
-    const unsigned grid = (unsigned)(kOne ? (p.T + kRowsPerBlock - 1) / kRowsPerBlock : p.T);
-    add_rmsnorm_kernel<T, J, kAdd, kFp8, kWide, kOne><<<grid, kOne ? 32 * kRowsPerBlock : 32 * warps, 0, stream>>>(
-        static_cast<const T*>(p.x), p.xs, static_cast<const T*>(p.r), p.rs, p.w, p.eps, p.T, p.C, static_cast<T*>(p.h),
-        static_cast<T*>(p.y), p.codes, p.scales);
+    return launch_kernel(add_rmsnorm_kernel<T, J, kAdd, kFp8, kWide, kOne>, dim3((unsigned)(kOne ? (p.T + kRowsPerBlock - 1) / kRowsPerBlock : p.T)),
+                         kOne ? 32 * kRowsPerBlock : 32 * warps, 0, 0, stream, static_cast<const T*>(p.x), p.xs, static_cast<const T*>(p.r), p.rs, p.w,
+                         p.eps, p.T, p.C, static_cast<T*>(p.h), static_cast<T*>(p.y), p.codes, p.scales);
   };
   prof_begin(stream, "add_rmsnorm_kernel");
-  if (warps == 1) go(std::true_type{});
-  else go(std::false_type{});
+  const cudaError_t e = warps == 1 ? go(std::true_type{}) : go(std::false_type{});
   prof_end(stream);
-  return cudaGetLastError();
+  return e;
 }
 
 template <typename T, int J, bool kWide>

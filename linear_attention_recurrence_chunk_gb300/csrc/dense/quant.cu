@@ -6,6 +6,8 @@
 // defined bit by bit.  Bound: HBM.  Blocks of 1 x 128: half a warp has a block (eight values a lane; any
 // alignment: a warp, four values a lane), four of them at once, whatever rows they lie in.  Blocks of 128 x 128: a CTA
 // holds one in registers between its maximum and its codes.
+#include <type_traits>
+
 #include "internal.cuh"
 
 namespace kda {
@@ -38,6 +40,8 @@ uint32_t walk_magic(int64_t d) { return d > 1 && d < 60000 ? (uint32_t)((0x10000
 template <typename T, bool kWide>
 __global__ void __launch_bounds__(32 * kWarps)
     fp8_quant_kernel(const T* __restrict__ x, int64_t xs, int64_t rows, int64_t C, uint32_t per_row, uint32_t magic, uint8_t* codes, uint8_t* scales) {
+  let_next_start();
+  wait_for_previous();
   const Walk<kWide> walk(C, per_row, magic);
   const int lane = threadIdx.x & 31;
   if constexpr (kWide) {
@@ -108,31 +112,45 @@ __global__ void __launch_bounds__(32 * kWarps)
   }
 }
 
-// Two blocks of 128 x 128 side by side (whole lines of 512 bytes of bf16 from each row: 256 each took 81 us for
-// 32,768 x 4,096): 16 warps, each with 256 columns of 8 rows.
-template <typename T, bool kWide>
+// Blocks of 128 x 128, kSide of them side by side, so that a row gives a line of 512 bytes: two of bf16 (one took 81 us
+// for 32,768 x 4,096, two 66), one of fp32 (4,096 x 4,096: two took 19.7 us); and one where there are no more.  16
+// warps have a row each at a time, or (kSide 1) two.
+template <typename T, bool kWide, int kSide>
 __global__ void __launch_bounds__(kSquareThreads)
     fp8_quant_square_kernel(const T* __restrict__ x, int64_t xs, int64_t rows, int64_t C, uint8_t* codes, uint8_t* scales) {
-  constexpr int W = kSquareThreads / 32, kRows = kBlock / W;
+  let_next_start();
+  wait_for_previous();
+  constexpr int W = kSquareThreads / 32, kAtOnce = 2 / kSide, kSteps = kBlock / (W * kAtOnce);
   __shared__ uint32_t part[2][W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t pairs = (C + 2 * kBlock - 1) / (2 * kBlock), br = blockIdx.x / pairs, bc = blockIdx.x - br * pairs;
-  const int64_t r0 = br * kBlock + warp, c0 = bc * 2 * kBlock;
-  Eight<T, kWide> v[kRows];
+  const int64_t across = (C + kSide * kBlock - 1) / (kSide * kBlock), br = blockIdx.x / across, bc = blockIdx.x - br * across;
+  const int64_t r0 = br * kBlock + kAtOnce * warp, c0 = bc * kSide * kBlock;
+  // kWide: lane `sub` of a row has eight columns; else value i lies in row_of(i), column_of(i)
+  const int sub = kSide == 2 ? lane : lane & 15, half = kSide == 2 ? 0 : lane >> 4;
+  const auto row_of = [&](int j, int i) { return r0 + W * kAtOnce * j + (kSide == 2 ? 0 : kWide ? half : i >> 2); };
+  const auto column_of = [&](int i) { return c0 + lane + 32 * (kSide == 2 ? i : i & 3); };
+  Eight<T, kWide> v[kSteps];
 #pragma unroll
-  for (int j = 0; j < kRows; ++j) {
-    const int64_t row = r0 + W * j;
-    v[j].load(x + (row < rows ? row : 0) * xs, c0, row < rows ? C : 0, lane);
+  for (int j = 0; j < kSteps; ++j) {
+    if constexpr (kWide) {
+      const int64_t row = row_of(j, 0);
+      v[j].load(x + (row < rows ? row : 0) * xs, c0, row < rows ? C : 0, sub);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[j].x[i] = row_of(j, i) < rows && column_of(i) < C ? x[row_of(j, i) * xs + column_of(i)] : from_f32<T>(0.f);
+    }
   }
+  // the largest of each half warp (kWide), or of values 0 .. 3 and 4 .. 7: of the first and the second block, or both of one
   uint32_t top[2] = {0, 0};
   if constexpr (kWide) {
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) top[0] = max(top[0], lane_top(v[j]));
-    top[0] = half_warp_max(top[0]);   // of the lane's block
+    for (int j = 0; j < kSteps; ++j) top[0] = max(top[0], lane_top(v[j]));
+    top[0] = half_warp_max(top[0]);
     if ((lane & 15) == 0) part[lane >> 4][warp] = top[0];
   } else {
 #pragma unroll
-    for (int j = 0; j < kRows; ++j)
+    for (int j = 0; j < kSteps; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) top[i >> 2] = max(top[i >> 2], __float_as_uint(top2(v[j].at(i), 0.f)));
 #pragma unroll
@@ -144,20 +162,25 @@ __global__ void __launch_bounds__(kSquareThreads)
   __syncthreads();
   uint32_t byte[2];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) byte[k] = scale_byte(__reduce_max_sync(0xffffffffu, part[k][lane & (W - 1)]));
-  if (threadIdx.x < 2 && c0 + kBlock * threadIdx.x < C)
+  for (int k = 0; k < 2; ++k) byte[k] = __reduce_max_sync(0xffffffffu, part[k][lane & (W - 1)]);
+  if constexpr (kSide == 1) byte[0] = byte[1] = max(byte[0], byte[1]);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) byte[k] = scale_byte(byte[k]);
+  if (threadIdx.x < kSide && c0 + kBlock * threadIdx.x < C)
     scales[br * ((C + kBlock - 1) / kBlock) + c0 / kBlock + threadIdx.x] = (uint8_t)(threadIdx.x ? byte[1] : byte[0]);
 #pragma unroll
-  for (int j = 0; j < kRows; ++j) {
-    const int64_t row = r0 + W * j;
-    if (row >= rows) break;
+  for (int j = 0; j < kSteps; ++j) {
     if constexpr (kWide) {
-      store_codes<true>(codes + row * C, c0, C, lane, codes8(v[j], lane < 16 ? byte[0] : byte[1]));
+      const int64_t row = row_of(j, 0);
+      if (row < rows) store_codes<true>(codes + row * C, c0, C, sub, codes8(v[j], lane < 16 ? byte[0] : byte[1]));
     } else {
       float f[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] = v[j].at(i);
-      store_codes<false>(codes + row * C, c0, C, lane, codes8(f, byte[0], byte[1]));
+      const uint2 w = codes8(f, byte[0], byte[1]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (row_of(j, i) < rows && column_of(i) < C) codes[row_of(j, i) * C + column_of(i)] = (uint8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
     }
   }
 }
@@ -166,6 +189,8 @@ template <typename T, bool kWide>
 __global__ void __launch_bounds__(32 * kWarps)
     fp8_values_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows, int64_t C, int32_t block_rows,
                       uint32_t per_row, uint32_t magic, T* y) {
+  let_next_start();
+  wait_for_previous();
   const Walk<kWide> walk(C, per_row, magic);
   const int lane = threadIdx.x & 31;
   constexpr int kN = kWide ? kJ : 2 * kJ, kPer = kWide ? 2 : 1;   // blocks of a lane; half a warp or a warp each
@@ -216,31 +241,37 @@ template <typename T>
 cudaError_t quant(const QuantProblem& p, cudaStream_t stream) {
   const bool wide = p.C % 8 == 0 && p.stride % (16 / sizeof(T)) == 0 && at(p.x, 16) && at(p.codes, 8);
   const T* x = static_cast<const T*>(p.x);
+  cudaError_t e;
   prof_begin(stream, "fp8_quant_kernel");
   if (p.rows == 1) {
-    const uint32_t per_row = (uint32_t)((p.C + kBlock - 1) / kBlock), magic = walk_magic(per_row);
+    const uint32_t per_row = (uint32_t)((p.C + kBlock - 1) / kBlock);
     const unsigned grid = (unsigned)((p.T * per_row + 2 * kJ * kWarps - 1) / (2 * kJ * kWarps));
-    if (wide) fp8_quant_kernel<T, true><<<grid, 32 * kWarps, 0, stream>>>(x, p.stride, p.T, p.C, per_row, magic, p.codes, p.scales);
-    else fp8_quant_kernel<T, false><<<grid, 32 * kWarps, 0, stream>>>(x, p.stride, p.T, p.C, per_row, magic, p.codes, p.scales);
+    e = launch_kernel(wide ? fp8_quant_kernel<T, true> : fp8_quant_kernel<T, false>, dim3(grid), 32 * kWarps, 0, 0, stream, x, p.stride, p.T, p.C, per_row,
+                      walk_magic(per_row), p.codes, p.scales);
   } else {
-    const unsigned grid = (unsigned)(((p.T + kBlock - 1) / kBlock) * ((p.C + 2 * kBlock - 1) / (2 * kBlock)));
-    if (wide) fp8_quant_square_kernel<T, true><<<grid, kSquareThreads, 0, stream>>>(x, p.stride, p.T, p.C, p.codes, p.scales);
-    else fp8_quant_square_kernel<T, false><<<grid, kSquareThreads, 0, stream>>>(x, p.stride, p.T, p.C, p.codes, p.scales);
+    const auto go = [&](auto side) {
+      constexpr int kSide = decltype(side)::value;
+      const unsigned grid = (unsigned)(((p.T + kBlock - 1) / kBlock) * ((p.C + kSide * kBlock - 1) / (kSide * kBlock)));
+      return launch_kernel(wide ? fp8_quant_square_kernel<T, true, kSide> : fp8_quant_square_kernel<T, false, kSide>, dim3(grid), kSquareThreads, 0, 0,
+                           stream, x, p.stride, p.T, p.C, p.codes, p.scales);
+    };
+    if constexpr (sizeof(T) == 4) e = go(std::integral_constant<int, 1>{});
+    else e = p.C <= kBlock ? go(std::integral_constant<int, 1>{}) : go(std::integral_constant<int, 2>{});
   }
   prof_end(stream);
-  return cudaGetLastError();
+  return e;
 }
 
 template <typename T>
 cudaError_t values(const ValuesProblem& p, cudaStream_t stream) {
   const bool wide = p.C % 8 == 0 && at(p.codes, 8) && at(p.y, 16);
-  const uint32_t per_row = (uint32_t)((p.C + kBlock - 1) / kBlock), magic = walk_magic(per_row);
+  const uint32_t per_row = (uint32_t)((p.C + kBlock - 1) / kBlock);
   const unsigned grid = (unsigned)((p.T * per_row + 2 * kJ * kWarps - 1) / (2 * kJ * kWarps));
   prof_begin(stream, "fp8_values_kernel");
-  if (wide) fp8_values_kernel<T, true><<<grid, 32 * kWarps, 0, stream>>>(p.codes, p.scales, p.T, p.C, p.rows, per_row, magic, static_cast<T*>(p.y));
-  else fp8_values_kernel<T, false><<<grid, 32 * kWarps, 0, stream>>>(p.codes, p.scales, p.T, p.C, p.rows, per_row, magic, static_cast<T*>(p.y));
+  const cudaError_t e = launch_kernel(wide ? fp8_values_kernel<T, true> : fp8_values_kernel<T, false>, dim3(grid), 32 * kWarps, 0, 0, stream, p.codes,
+                                      p.scales, p.T, p.C, p.rows, per_row, walk_magic(per_row), static_cast<T*>(p.y));
   prof_end(stream);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace

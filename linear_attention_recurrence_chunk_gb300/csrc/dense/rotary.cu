@@ -70,6 +70,8 @@ struct Values {
 template <typename T, int kE, bool kNext, bool kInverse, bool kMany>
 __global__ void __launch_bounds__(32 * kWarps, 2) rotary_kernel(const Shape s) {
   extern __shared__ uint64_t sm[];
+  let_next_start();
+  wait_for_previous();
   uint64_t* turn = sm;   // [half] turns per position, 2^-64 each
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // its tokens' (cos, sin), of each kE / 2 blocks of [turned][2 pairs] (kE = 1: [half]): lanes of neighbouring parts read neighbouring banks
@@ -203,8 +205,7 @@ cudaError_t launch(const RotaryProblem& p, cudaStream_t stream) {
   const int64_t units = s.split == 1 ? (p.T + s.tokens - 1) / s.tokens : p.T * s.split;
   const dim3 grid((unsigned)std::min<int64_t>(2 * sms, (units + kWarps - 1) / kWarps));
   auto go = [&](auto kernel) -> cudaError_t {
-    kernel<<<grid, 32 * kWarps, smem, stream>>>(s);
-    return cudaGetLastError();
+    return launch_kernel(kernel, grid, 32 * kWarps, smem, 0, stream, s);
   };
   prof_begin(stream, "rotary_kernel");
   auto pick = [&](auto many) -> cudaError_t {
