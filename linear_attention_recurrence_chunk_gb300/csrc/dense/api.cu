@@ -38,7 +38,7 @@ bool dtype_ok(kda_dtype dt) { return dt == KDA_F32 || dt == KDA_BF16; }
 int64_t blocks_of(int64_t n) { return (n + kBlock - 1) / kBlock; }
 
 constexpr int64_t kMost = (int64_t)INT32_MAX - 511;   // rows or columns
-constexpr int64_t kMostStride = (int64_t)1 << 40;     // elements
+constexpr int64_t kMostStride = (int64_t)1 << 37;     // elements (a tensor map's strides are below 2^40 bytes)
 
 // Rows of a strided [rows][C] matrix (rows, C at least 1), its bytes from first to last.
 Range span(const void* p, int64_t rows, int64_t C, int64_t stride, size_t eb) {
@@ -151,8 +151,9 @@ kda_status kda_rotary(const void* q, int64_t q_token_stride, int64_t q_head_stri
     const int64_t st[] = {p.xt, p.xh, p.yt, p.yh};
     for (int64_t s : st)
       if (s < 0 || s > kMostStride) return KDA_ERR_INVALID_ARG;
-    // the heads of a token, and the tokens of an output, do not lie over one another
+    // an output's heads and tokens do not lie over one another: the heads of a token side by side, or the tokens of a head
     if ((p.H > 1 && p.yh < D) || (T > 1 && p.yt < D)) return KDA_ERR_INVALID_ARG;
+    if (p.H > 1 && T > 1 && p.yt < (p.H - 1) * p.yh + D && p.yh < (T - 1) * p.yt + D) return KDA_ERR_INVALID_ARG;
     in[i] = {p.x, (size_t)((T - 1) * p.xt + (p.H - 1) * p.xh + D) * eb};
     out[i] = {p.y, (size_t)((T - 1) * p.yt + (p.H - 1) * p.yh + D) * eb};
     place[i] = p.x == p.y && p.xt == p.yt && p.xh == p.yh;

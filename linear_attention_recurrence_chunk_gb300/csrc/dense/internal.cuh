@@ -15,7 +15,8 @@ constexpr int kBlock = 128;   // columns of a scale
 // -------------------------------------------------------------- launches one behind another
 // Every kernel here is launched so that it may start while the one before it in the stream ends (about 1 us less from
 // kernel to kernel; a product of one row, 16,416 x 4,096: 15.6 -> 13.0 us a call): it lets the next one start at once, and
-// touches no global memory before all that ran before it is complete and visible.
+// touches no global memory before all that ran before it is complete and visible.  (No loads by the read-only path, or
+// through __restrict__ pointers: what they read may be written while the kernel is waiting.)
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -54,8 +54,8 @@ __device__ __forceinline__ uint32_t cluster_address(uint32_t shared, uint32_t ra
 
 template <int kRows, bool kDeep, typename T>
 __global__ void __launch_bounds__(kThreads)
-    fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapX, const uint8_t* __restrict__ sw,
-                          const uint8_t* __restrict__ sx, int64_t M, int64_t N, int32_t blocks, T* out, int64_t ldo, int32_t quads,
+    fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapX, const uint8_t* sw,
+                          const uint8_t* sx, int64_t M, int64_t N, int32_t blocks, T* out, int64_t ldo, int32_t quads,
                           int32_t words, int32_t split, int32_t* dev_err) {
   using F = Few<kRows, kDeep>;
   extern __shared__ uint8_t raw[];

@@ -76,8 +76,8 @@ __device__ __forceinline__ void place(uint32_t t, uint32_t tm, uint32_t tn, uint
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fp8_matmul_pair_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB, const __grid_constant__ CUtensorMap mapO,
-                           const uint8_t* __restrict__ sa,
-                           const uint8_t* __restrict__ sw, int64_t M, int64_t N, int32_t blocks, uint32_t tm, uint32_t tn, T* out, int64_t ldo,
+                           const uint8_t* sa,
+                           const uint8_t* sw, int64_t M, int64_t N, int32_t blocks, uint32_t tm, uint32_t tn, T* out, int64_t ldo,
                            int32_t wide, int32_t words, int32_t* dev_err) {
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);

@@ -174,7 +174,7 @@ constexpr int kScaleSlots = 4;   // groups of four K blocks whose scales are on 
 // row(i) gives a row's number, negative for none (any word then).  No branch stands between the loads, so
 // that all are on their way together, and nothing here waits for whole words.  `words`: rows of whole 32-bit words.
 template <int kWords, typename F>
-__device__ __forceinline__ void load_scales(const uint8_t* __restrict__ scales, int32_t blocks, int32_t kb, bool words, uint32_t (&w)[kWords],
+__device__ __forceinline__ void load_scales(const uint8_t* scales, int32_t blocks, int32_t kb, bool words, uint32_t (&w)[kWords],
                                             F row) {
   int64_t r[kWords];
 #pragma unroll
@@ -184,13 +184,13 @@ __device__ __forceinline__ void load_scales(const uint8_t* __restrict__ scales, 
   }
   if (words) {
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(scales + r[i] * blocks + kb));
+    for (int i = 0; i < kWords; ++i) w[i] = __ldcg(reinterpret_cast<const uint32_t*>(scales + r[i] * blocks + kb));
   } else {
     uint32_t b[kWords][4];
 #pragma unroll
     for (int i = 0; i < kWords; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) b[i][j] = __ldg(scales + r[i] * blocks + (kb + j < blocks ? kb + j : blocks - 1));
+      for (int j = 0; j < 4; ++j) b[i][j] = __ldcg(scales + r[i] * blocks + (kb + j < blocks ? kb + j : blocks - 1));
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       w[i] = 0;

@@ -37,7 +37,7 @@ __device__ __forceinline__ float row_sum(float x, float* part, int warp, int lan
 
 template <typename T, int J, bool kAdd, bool kFp8, bool kWide, bool kOneWarp>
 __global__ void __launch_bounds__(kOneWarp ? 32 * kRowsPerBlock : 1024)
-    add_rmsnorm_kernel(const T* x, int64_t xs, const T* r, int64_t rs, const float* __restrict__ w, float eps,
+    add_rmsnorm_kernel(const T* x, int64_t xs, const T* r, int64_t rs, const float* w, float eps,
                        int64_t rows, int64_t C, T* h, T* y, uint8_t* codes, uint8_t* scales) {
   __shared__ float part[32];
   let_next_start();
@@ -93,13 +93,13 @@ __global__ void __launch_bounds__(kOneWarp ? 32 * kRowsPerBlock : 1024)
       if constexpr (kWide) {
         const int64_t c = c0 + 8 * lane;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-        if (c < C) a = __ldg(reinterpret_cast<const float4*>(w + c)), b = __ldg(reinterpret_cast<const float4*>(w + c) + 1);
+        if (c < C) a = reinterpret_cast<const float4*>(w + c)[0], b = reinterpret_cast<const float4*>(w + c)[1];
         g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w, g[4] = b.x, g[5] = b.y, g[6] = b.z, g[7] = b.w;
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int64_t c = c0 + lane + 32 * i;
-          g[i] = c < C ? __ldg(w + c) : 0.f;
+          g[i] = c < C ? w[c] : 0.f;
         }
       }
 #pragma unroll
@@ -126,7 +126,7 @@ constexpr int kNarrow = 128, kSets = 2;
 
 template <typename T, bool kAdd, bool kFp8, bool kWide>
 __global__ void __launch_bounds__(32 * kRowsPerBlock)
-    add_rmsnorm_narrow_kernel(const T* x, int64_t xs, const T* r, int64_t rs, const float* __restrict__ w, float eps0, int64_t rows, int32_t C,
+    add_rmsnorm_narrow_kernel(const T* x, int64_t xs, const T* r, int64_t rs, const float* w, float eps0, int64_t rows, int32_t C,
                               int32_t L, T* h, T* y, uint8_t* codes, uint8_t* scales) {
   let_next_start();
   wait_for_previous();
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(32 * kRowsPerBlock)
   }
   float g[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) g[i] = w && column(i) < C ? __ldg(w + column(i)) : 1.f;
+  for (int i = 0; i < 8; ++i) g[i] = w && column(i) < C ? w[column(i)] : 1.f;
 #pragma unroll
   for (int j = 0; j < kSets; ++j) {
     const int64_t row = row0 + j * per_warp;

@@ -39,7 +39,7 @@ uint32_t walk_magic(int64_t d) { return d > 1 && d < 60000 ? (uint32_t)((0x10000
 
 template <typename T, bool kWide>
 __global__ void __launch_bounds__(32 * kWarps)
-    fp8_quant_kernel(const T* __restrict__ x, int64_t xs, int64_t rows, int64_t C, uint32_t per_row, uint32_t magic, uint8_t* codes, uint8_t* scales) {
+    fp8_quant_kernel(const T* x, int64_t xs, int64_t rows, int64_t C, uint32_t per_row, uint32_t magic, uint8_t* codes, uint8_t* scales) {
   let_next_start();
   wait_for_previous();
   const Walk<kWide> walk(C, per_row, magic);
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(32 * kWarps)
 // warps have a row each at a time, or (kSide 1) two.
 template <typename T, bool kWide, int kSide>
 __global__ void __launch_bounds__(kSquareThreads)
-    fp8_quant_square_kernel(const T* __restrict__ x, int64_t xs, int64_t rows, int64_t C, uint8_t* codes, uint8_t* scales) {
+    fp8_quant_square_kernel(const T* x, int64_t xs, int64_t rows, int64_t C, uint8_t* codes, uint8_t* scales) {
   let_next_start();
   wait_for_previous();
   constexpr int W = kSquareThreads / 32, kAtOnce = 2 / kSide, kSteps = kBlock / (W * kAtOnce);
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kSquareThreads)
 
 template <typename T, bool kWide>
 __global__ void __launch_bounds__(32 * kWarps)
-    fp8_values_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows, int64_t C, int32_t block_rows,
+    fp8_values_kernel(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t C, int32_t block_rows,
                       uint32_t per_row, uint32_t magic, T* y) {
   let_next_start();
   wait_for_previous();

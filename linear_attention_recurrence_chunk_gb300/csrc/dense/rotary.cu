@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) rotary_kernel(const Shape s) {
   auto token = [&](int64_t unit) { return s.split == 1 ? unit * s.tokens : unit / s.split; };
   auto position = [&](int64_t unit) {
     const int64_t t = token(unit) + lane;
-    return unit < units && lane < s.tokens && t < s.T ? __ldg(s.pos + t) : -1;
+    return unit < units && lane < s.tokens && t < s.T ? s.pos[t] : -1;
   };
   int32_t next = position(u);
   for (; u < units; u += step) {

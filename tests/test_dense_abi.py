@@ -82,7 +82,8 @@ def _matmul(lib, **kw):
     (dict(N=-1), 1), (dict(K=0), 1), (dict(K=-16), 1), (dict(K=500, lda=512), 2), (dict(M=1 << 31), 2), (dict(N=1 << 31), 2),
     (dict(lda=496), 1), (dict(lda=520), 1), (dict(ldw=504), 1), (dict(a=FAKE + 8), 1), (dict(w=FAKE + 2 * G + 4), 1),
     (dict(out=FAKE + 4 * G + 1), 1), (dict(out=FAKE + 4 * G + 2, dt=0), 1), (dict(ldo=299), 1), (dict(out=FAKE), 1),
-    (dict(out=FAKE + G + 8), 1), (dict(out=FAKE + 2 * G), 1), (dict(out=FAKE + 3 * G), 1), (dict(lda=-512), 1)])
+    (dict(out=FAKE + G + 8), 1), (dict(out=FAKE + 2 * G), 1), (dict(out=FAKE + 3 * G), 1), (dict(lda=-512), 1),
+    (dict(ldw=1 << 38), 1), (dict(ldo=1 << 38), 1)])
 def test_matmul_refusals(lib, kw, want):
     assert _matmul(lib, **kw) == want
     assert _matmul(lib, M=0, a=None) == 0 and _matmul(lib, N=0, w=None) == 0
@@ -104,6 +105,8 @@ def _rotary(lib, **kw):
     (dict(qo=FAKE), 1),                                     # over its input, with other strides
     (dict(qo=FAKE + 256, qot=1280), 1),                     # shifted by a head
     (dict(qo=FAKE + 4 * G), 1),                             # over k_out
+    (dict(qot=128, qoh=128), 1), (dict(qot=512), 1), (dict(kot=128), 1),   # tokens over the heads of others
+    (dict(qot=1 << 38), 1),
     (dict(ko=FAKE + 2048), 1), (dict(ko=FAKE + G), 1), (dict(qo=FAKE + 2 * G), 1)])
 def test_rotary_refusals(lib, kw, want):
     assert _rotary(lib, **kw) == want

@@ -150,3 +150,29 @@ def test_calls_in_flight_at_once():
         for outs, ws in zip(round_, want):
             for a, b in zip(outs, ws):
                 assert torch.equal(a, b)
+
+
+def test_one_behind_another():
+    """300 dependent steps without a wait between them (a residual stream updated in place, an input that each step's
+    product writes) give the bits that they give with the GPU waited for after every call."""
+    def run(wait):
+        g = torch.Generator(device="cuda").manual_seed(5)
+        res = torch.randn(200, 512, device="cuda", generator=g).bfloat16()
+        w = kda.kda_fp8_quant(torch.randn(512, 512, device="cuda", generator=g) * 0.05, 128)
+        x, pos = torch.zeros_like(res), torch.arange(200, device="cuda", dtype=torch.int32)
+        freqs, _ = kda.kda_rotary_freqs(64)
+        for i in range(300):
+            codes, scales, _ = kda.kda_add_rmsnorm_fp8(x, res, residual_out=res)
+            wait()
+            kda.kda_fp8_matmul(codes, scales, *w, out=x)
+            wait()
+            heads = x.view(200, 8, 64)
+            kda.kda_rotary(heads, None, pos, freqs, q_out=heads)
+            wait()
+            if i % 7 == 0:
+                x.copy_(kda.kda_fp8_values(*kda.kda_fp8_quant(x, 128), 128))
+                wait()
+        return res, x
+
+    for a, b in zip(run(lambda: None), run(torch.cuda.synchronize)):
+        assert torch.isfinite(a.float()).all() and torch.equal(a, b)

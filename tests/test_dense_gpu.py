@@ -179,6 +179,30 @@ def test_no_rows_and_no_columns():
         assert kda.kda_fp8_quant(x, 128)[1].shape == (0, 1) if T == 0 else True
 
 
+def test_matrices_beyond_2_31_elements():
+    """The last rows of 2.2e9 values: norm, 8 bits and back, and the rotation."""
+    T, C = 1100000, 2048
+    x = torch.zeros(T, C, device="cuda", dtype=torch.bfloat16)
+    x[-3:] = _rows(3, C, "bf16", 4).cuda()
+    want, _ = kda.kda_add_rmsnorm(x[-3:].contiguous())
+    y, h = kda.kda_add_rmsnorm(x, x)
+    assert torch.equal(h[-3:], 2 * x[-3:]) and (y[-3:] - want).abs().max() <= 2.0 ** -7 * want.abs().max() and not h[:-3].any()
+    del y, h
+    for rows in (1, 128):
+        codes, scales = kda.kda_fp8_quant(x, rows)
+        tail = T - T % 128 if rows == 128 else T - 3
+        c, s = kda.kda_fp8_quant(x[tail:], rows)
+        assert torch.equal(codes[tail:].view(torch.uint8), c.view(torch.uint8)) and torch.equal(scales[-s.shape[0]:], s)
+        v = kda.kda_fp8_values(codes, scales, rows)
+        assert torch.equal(v[tail:], kda.kda_fp8_values(c, s, rows)) and not v[:tail].any()
+        del codes, v
+    freqs, _ = kda.kda_rotary_freqs(128)
+    pos = torch.arange(T, device="cuda", dtype=torch.int32)
+    q = x.view(T, 16, 128)
+    yq, _ = kda.kda_rotary(q, None, pos, freqs)
+    assert torch.equal(yq[-3:], kda.kda_rotary(q[-3:].contiguous(), None, pos[-3:].contiguous(), freqs)[0]) and not yq[:-3].any()
+
+
 # ------------------------------------------------------------------ rotary
 def _rot_tol(x, want, amp, dt):
     """Each product: the angle to 2^-25 of a turn (2e-7 rad) and sine and cosine to 2^-23, the amplitude, the product and

@@ -111,10 +111,10 @@ def test_values_that_are_not_finite(M):
 
 @pytest.mark.parametrize("M", [3, 129, 1030])
 def test_scales_over_the_range(M):
-    """Bytes from 1 to 254 that leave the product in fp32's normal range."""
+    """Bytes from 0 to 254 that leave the product in fp32's normal range."""
     N, K = 200, 256
     a, sa, w, sw = _exact_operands(M, N, K, 11)
-    for b in (1, 40, 127, 200, 254):
+    for b in (0, 1, 40, 127, 200, 253, 254):
         sa[:], sw[:] = b, 254 - b
         got = kda.kda_fp8_matmul(a.cuda(), sa.cuda(), w.cuda(), sw.cuda(), torch.float32)
         want = (a.double() @ w.double().t()).cuda()   # 2^(b - 127) 2^(127 - b)
@@ -158,3 +158,22 @@ def test_refuses_on_the_gpu():
         kda.kda_fp8_matmul(a[:, :120], sa, w[:, :120], sw)    # K not a multiple of 16
     with pytest.raises(kda.KdaError):
         kda.kda_fp8_matmul(a[:, 8:], sa, w[:, 8:], sw)        # begins inside 16 bytes
+
+
+@pytest.mark.parametrize("M,N", [(70000, 33000), (66000, 32769)])
+def test_outputs_beyond_2_31_elements(M, N):
+    """Both ends of an output of 2.2e9 values, by tensor stores and by rows that begin anywhere."""
+    K = 144
+    a, sa, w, sw = (t.cuda() for t in _exact_operands(M, N, K, 3))
+    got = kda.kda_fp8_matmul(a, sa, w, sw)
+    for rows in (slice(0, 300), slice(M - 300, M)):
+        want = _dense(a[rows], sa[rows], 1) @ _dense(w, sw, 128).t()
+        assert torch.equal(got[rows], want.bfloat16())
+
+
+def test_many_rows_of_few_columns():
+    """More rows than a grid's second dimension has blocks of 16."""
+    M, N, K = 1100000, 24, 32
+    a, sa, w, sw = (t.cuda() for t in _exact_operands(M, N, K, 5))
+    got = kda.kda_fp8_matmul(a, sa, w, sw)
+    assert torch.equal(got, (_dense(a, sa, 1) @ _dense(w, sw, 128).t()).bfloat16())
