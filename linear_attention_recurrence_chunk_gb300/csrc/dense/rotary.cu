@@ -203,9 +203,9 @@ cudaError_t launch(const RotaryProblem& p, cudaStream_t stream) {
   s.m_token = magic((uint32_t)(s.heads * s.parts));
   const size_t smem = (size_t)s.half * 8 * (1 + kWarps * s.tokens);   // 36 KB at most
   const int64_t units = s.split == 1 ? (p.T + s.tokens - 1) / s.tokens : p.T * s.split;
-  const dim3 grid((unsigned)std::min<int64_t>(2 * sms, (units + kWarps - 1) / kWarps));
+  const unsigned grid = (unsigned)std::min<int64_t>(2 * sms, (units + kWarps - 1) / kWarps);
   auto go = [&](auto kernel) -> cudaError_t {
-    return launch_kernel(kernel, grid, 32 * kWarps, smem, 0, stream, s);
+    return launch_kernel(kernel, dim3(grid), 32 * kWarps, smem, 0, stream, s);
   };
   prof_begin(stream, "rotary_kernel");
   auto pick = [&](auto many) -> cudaError_t {
