@@ -30,7 +30,7 @@ extern "C" {
 
 /*
  * x [T][C] dtype dt (row stride in elements, at least C) to 8 bits: codes [T][C] dense, scales
- * [ceil(T / block_rows)][ceil(C / 128)], block_rows 1 or 128.  Any T, C up to 2^31 - 129; rows that
+ * [ceil(T / block_rows)][ceil(C / 128)], block_rows 1 or 128.  Any T, C up to 2^31 - 512; rows that
  * begin on 16-byte boundaries (8 bytes for codes) take wide loads and stores.
  */
 KDA_API kda_status kda_fp8_quant(const void* x, int64_t x_stride, int64_t T, int64_t C, int32_t block_rows,
@@ -68,9 +68,9 @@ KDA_API kda_status kda_add_rmsnorm(const void* x, int64_t x_stride, const void* 
  *  out          [M][N] dtype dt, row stride out_stride in elements, at least N
  * K and the row strides of a and w are multiples of 16, a and w 16-byte aligned, out aligned to
  * its type.  Products are exact, sums fp32 in the tensor core's order, which depends on the
- * sizes alone: the same call gives the same bits.  A NaN of a row of A reaches that row of
- * out, one of W that column.
- * KDA_ERR_UNSUPPORTED: K not a multiple of 16; M, N or K beyond 2^31 - 512.
+ * sizes alone: the same call gives the same bits.  A NaN code of a row of A reaches that row of
+ * out, one of W that column; a scale byte 255 its row, or its 128 columns.
+ * KDA_ERR_UNSUPPORTED: K not a multiple of 16 or beyond 2^27; M or N beyond 2^31 - 512.
  */
 KDA_API kda_status kda_fp8_matmul(const uint8_t* a, int64_t a_stride, const uint8_t* a_scales, const uint8_t* w,
                                   int64_t w_stride, const uint8_t* w_scales, int64_t M, int64_t N, int64_t K,
@@ -88,12 +88,14 @@ enum { KDA_ROTARY_INTERLEAVED = 1, KDA_ROTARY_INVERSE = 2 };
  *
  *  q [T][Hq][D], k [T][Hk][D] dtype dt, and q_out, k_out of the same shapes: strides from token to
  *             token and head to head in elements, channels contiguous.  A part with no heads (0) may be
- *             NULL.  An output is its input (the same pointer and strides: in place) or overlaps no input.
+ *             NULL.  An output is its input (the same pointer and strides: in place) or overlaps no input;
+ *             its heads and tokens do not lie over one another.
  *  positions  int32[T] (kda_page_map's); a token with a negative one is not turned
  *  freqs      fp64[rot / 2]: radians per position, finite
  * Angles are reduced to a fraction of a turn in 64 bits of fixed point: at any position they are
- * right to 2^-24 of a turn, and sines and cosines to fp32's rounding.  rot is even, at most D; D at most
- * 1024 (else KDA_ERR_UNSUPPORTED).  16-byte steps throughout take wide loads and stores.
+ * right to 2^-24 of a turn, and sines and cosines to fp32's rounding.  rot is even, at most D.
+ * 16-byte steps throughout (and rot a multiple of 16) take wide loads and stores.
+ * KDA_ERR_UNSUPPORTED: D beyond 1024, or Hq + Hk.
  */
 KDA_API kda_status kda_rotary(const void* q, int64_t q_token_stride, int64_t q_head_stride, int32_t Hq, const void* k,
                               int64_t k_token_stride, int64_t k_head_stride, int32_t Hk, const int32_t* positions,

@@ -38,6 +38,7 @@ bool dtype_ok(kda_dtype dt) { return dt == KDA_F32 || dt == KDA_BF16; }
 int64_t blocks_of(int64_t n) { return (n + kBlock - 1) / kBlock; }
 
 constexpr int64_t kMost = (int64_t)INT32_MAX - 511;   // rows or columns
+constexpr int64_t kMostK = (int64_t)1 << 27;           // (a tile's 2^20 K blocks end well inside a bounded wait)
 constexpr int64_t kMostStride = (int64_t)1 << 37;     // elements (a tensor map's strides are below 2^40 bytes)
 
 // Rows of a strided [rows][C] matrix (rows, C at least 1), its bytes from first to last.
@@ -110,7 +111,7 @@ kda_status kda_fp8_matmul(const uint8_t* a, int64_t a_stride, const uint8_t* a_s
                           const uint8_t* w_scales, int64_t M, int64_t N, int64_t K, kda_dtype dt, void* out, int64_t out_stride,
                           cudaStream_t stream) {
   if (!dtype_ok(dt) || M < 0 || N < 0 || K < 1) return KDA_ERR_INVALID_ARG;
-  if (K % 16 != 0 || M > kMost || N > kMost || K > kMost) return KDA_ERR_UNSUPPORTED;
+  if (K % 16 != 0 || M > kMost || N > kMost || K > kMostK) return KDA_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return KDA_OK;
   const auto up16 = [](int64_t v) { return (v + 15) / 16 * 16; };
   if (M == 1) a_stride = K, out_stride = N;   // a stride over one row has no meaning

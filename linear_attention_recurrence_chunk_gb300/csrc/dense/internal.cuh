@@ -40,6 +40,7 @@ cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, int threads, size_t s
   cfg.numAttrs = cluster > 0 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
+
 // ------------------------------------------------------------------ 8-bit values
 // Scale byte of a block whose largest |value| has the fp32 bits `top`: the exponent field b
 // of the least 2^(b - 127), b >= 1, with top <= 448 * 2^(b - 127); 255 for an inf or NaN.

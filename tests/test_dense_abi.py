@@ -79,7 +79,7 @@ def _matmul(lib, **kw):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(a=None), 1), (dict(sa=None), 1), (dict(w=None), 1), (dict(sw=None), 1), (dict(out=None), 1), (dict(dt=9), 1), (dict(M=-1), 1),
-    (dict(N=-1), 1), (dict(K=0), 1), (dict(K=-16), 1), (dict(K=500, lda=512), 2), (dict(M=1 << 31), 2), (dict(N=1 << 31), 2),
+    (dict(N=-1), 1), (dict(K=0), 1), (dict(K=-16), 1), (dict(K=500, lda=512), 2), (dict(M=1 << 31), 2), (dict(N=1 << 31), 2), (dict(K=(1 << 27) + 16, lda=1 << 28, ldw=1 << 28), 2),
     (dict(lda=496), 1), (dict(lda=520), 1), (dict(ldw=504), 1), (dict(a=FAKE + 8), 1), (dict(w=FAKE + 2 * G + 4), 1),
     (dict(out=FAKE + 4 * G + 1), 1), (dict(out=FAKE + 4 * G + 2, dt=0), 1), (dict(ldo=299), 1), (dict(out=FAKE), 1),
     (dict(out=FAKE + G + 8), 1), (dict(out=FAKE + 2 * G), 1), (dict(out=FAKE + 3 * G), 1), (dict(lda=-512), 1),

@@ -64,6 +64,18 @@ def test_edges_of_the_format(rows):
     assert v[0 if rows == 128 else 5, 130].isnan()
 
 
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("C", [256, 131])
+def test_subnormal_bf16(C, rows):
+    """Every subnormal bf16 and its neighbours, alone in their blocks and beside larger values."""
+    x = torch.arange(0, 512, dtype=torch.int16).view(torch.bfloat16)[:, None].repeat(1, C)
+    x[:, 1::2] *= -1
+    x[256:, 3] = torch.arange(256).to(torch.bfloat16) * 2.0 ** -120
+    codes, scales = kda.kda_fp8_quant(x.cuda(), rows)
+    c, b = ref.stored(_np(x), rows)
+    assert np.array_equal(scales.cpu().numpy(), b) and np.array_equal(_bytes(codes), c)
+
+
 def test_every_code_and_scale_byte_reads_back():
     codes = torch.arange(256, dtype=torch.uint8).repeat(256, 1)
     scales = torch.arange(256, dtype=torch.uint8)[:, None].repeat(1, 2)
@@ -150,6 +162,16 @@ def test_norm_range(C):
     codes, scales, _ = kda.kda_add_rmsnorm_fp8(torch.from_numpy(x).cuda(), None, None, 1e-6)
     b = scales.cpu().numpy()
     assert (b[:6] < 255).all() and b[6, 0] == 255 and (b[6, 1:] == 1).all() and (b[7] == 255).all()
+
+
+@pytest.mark.parametrize("C", [64, 4096])
+def test_norm_with_a_large_eps(C):
+    """An eps beside squares beyond fp32's range, and one far above them."""
+    x = _rows(4, C, "f32", 2).numpy() * np.float32(1e19)
+    for eps in (1e30, 1e38, 3e38):
+        y, _ = kda.kda_add_rmsnorm(torch.from_numpy(x).cuda(), None, None, eps)
+        _, want = ref.norm(x.astype(np.float64), None, None, np.float64(np.float32(eps)))
+        assert (np.abs(_np(y) - want) <= _norm_tol(want, "f32")).all()
 
 
 def test_norm_in_place_and_strided():
@@ -309,6 +331,20 @@ def test_rotary_many_tokens(T, Hq, Hk, D, rot, interleaved, dt):
     size = 2 * x.double().abs().amax(-1, keepdim=True)
     assert ((y.double() - want).abs() <= 2.0 ** -20 * size + (2.0 ** -8 if dt == "bf16" else 0) * want.abs()).all()
     assert torch.equal(y[pos < 0], x[pos < 0])
+
+
+def test_rotary_many_heads_at_any_alignment():
+    """66,560 single pairs a token, more tokens than warps: each as in a call of its own."""
+    T, H, D = 4900, 1024, 130
+    x = torch.randn(T, H * D + 1, device="cuda").bfloat16()[:, 1:].unflatten(1, (H, D))
+    pos = torch.arange(T, device="cuda", dtype=torch.int32)
+    freqs, _ = kda.kda_rotary_freqs(D)
+    yq, yk = kda.kda_rotary(x[:, :1000], x[:, 1000:], pos, freqs)
+    for t in (0, 1, 2500, T - 1):
+        want, _ = kda.kda_rotary(x[t:t + 1, 3:].contiguous(), None, pos[t:t + 1].contiguous(), freqs)
+        assert torch.equal(torch.cat([yq[t:t + 1, 3:], yk[t:t + 1]], 1), want)
+    want = ref.rotate(_np(x[-1:, -2:]), pos[-1:].cpu().numpy(), freqs.cpu().numpy(), 1.0, False, False)
+    assert (np.abs(_np(yk[-1:, -2:]) - want) <= _rot_tol(_np(x[-1:, -2:]), want, 1.0, "bf16")).all()
 
 
 def test_rotary_no_tokens():
