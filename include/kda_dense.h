@@ -66,7 +66,7 @@ KDA_API kda_status kda_add_rmsnorm(const void* x, int64_t x_stride, const void* 
  *  a, a_scales  codes [M][K], row stride a_stride in bytes; scales [M][ceil(K / 128)] (R = 1)
  *  w, w_scales  codes [N][K], row stride w_stride in bytes; scales [ceil(N / 128)][ceil(K / 128)] (R = 128)
  *  out          [M][N] dtype dt, row stride out_stride in elements, at least N
- * K and the row strides of a and w are multiples of 16, a and w 16-byte aligned, out aligned to
+ * K (at least 16) and the row strides of a and w are multiples of 16, a and w 16-byte aligned, out aligned to
  * its type.  Products are exact, sums fp32 in the tensor core's order, which depends on the
  * sizes alone: the same call gives the same bits.  A NaN code of a row of A reaches that row of
  * out, one of W that column; a scale byte 255 its row, or its 128 columns.
@@ -89,7 +89,9 @@ enum { KDA_ROTARY_INTERLEAVED = 1, KDA_ROTARY_INVERSE = 2 };
  *  q [T][Hq][D], k [T][Hk][D] dtype dt, and q_out, k_out of the same shapes: strides from token to
  *             token and head to head in elements, channels contiguous.  A part with no heads (0) may be
  *             NULL.  An output is its input (the same pointer and strides: in place) or overlaps no input;
- *             its heads and tokens do not lie over one another.
+ *             its heads and tokens do not lie over one another.  In place, the other part lies apart, or
+ *             between the tokens (the same token stride) or heads (the same head stride) of this one, as
+ *             parts of one projection do.
  *  positions  int32[T] (kda_page_map's); a token with a negative one is not turned
  *  freqs      fp64[rot / 2]: radians per position, finite
  * Angles are reduced to a fraction of a turn in 64 bits of fixed point: at any position they are

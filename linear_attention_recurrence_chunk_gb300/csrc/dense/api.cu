@@ -3,6 +3,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "internal.cuh"
 
 namespace {
@@ -49,6 +51,22 @@ bool shape_ok(int64_t rows, int64_t C) {
   return rows >= 0 && C >= 0 && rows <= kMost && C <= kMost && (rows == 0 || C <= ((int64_t)1 << 42) / rows);
 }
 bool stride_ok(int64_t stride, int64_t C) { return stride >= C && stride <= kMostStride; }
+
+// Whether the values that two parts read may be the same ones.  Parts whose bytes lie over one another are told apart
+// as parts of one projection are: between one another's tokens (the same token stride), or heads (the same head stride,
+// which divides the tokens').
+bool share(const kda::dense::RotaryPart& a, const kda::dense::RotaryPart& b, const Range& ra, const Range& rb, int64_t T, int32_t D, size_t eb) {
+  if (!overlaps(ra, rb)) return false;
+  if (T > 1 && a.xt != b.xt) return true;
+  const int64_t d = (int64_t)(reinterpret_cast<intptr_t>(b.x) - reinterpret_cast<intptr_t>(a.x)) / (int64_t)eb;
+  const auto beside = [d](int64_t step, int64_t na, int64_t nb) {   // na and nb values of each `step`, d apart
+    const int64_t r = step > 0 ? (d % step + step) % step : 0;
+    return step > 0 && r >= na && r + nb <= step;
+  };
+  if (T > 1 && beside(a.xt, (a.H - 1) * a.xh + D, (b.H - 1) * b.xh + D)) return false;
+  const int64_t h = std::max(a.xh, b.xh);   // of one head: 0
+  return !((a.H == 1 || a.xh == h) && (b.H == 1 || b.xh == h) && h > 0 && (T == 1 || a.xt % h == 0) && beside(h, D, D));
+}
 
 kda_status done(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
 
@@ -161,9 +179,10 @@ kda_status kda_rotary(const void* q, int64_t q_token_stride, int64_t q_head_stri
   }
   for (int i = 0; i < 2; ++i) {
     if (overlaps(out[i], in[2]) || overlaps(out[i], in[3])) return KDA_ERR_INVALID_ARG;
-    // In place, the other part may lie between the heads or tokens of this one (parts of one projection).
+    // In place, the other part may lie between the tokens or heads of this one (parts of one projection).
     if (!place[i] && (overlaps(out[i], in[0]) || overlaps(out[i], in[1]) || overlaps(out[i], out[1 - i]))) return KDA_ERR_INVALID_ARG;
   }
+  if ((place[0] || place[1]) && part[0].H > 0 && part[1].H > 0 && share(part[0], part[1], in[0], in[1], T, D, eb)) return KDA_ERR_INVALID_ARG;
   return done(kda::dense::launch_rotary({part[0], part[1], positions, freqs, T, D, rot, amplitude, flags, dt}, stream));
 }
 

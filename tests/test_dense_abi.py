@@ -113,6 +113,20 @@ def test_rotary_refusals(lib, kw, want):
     assert _rotary(lib, T=0, q=None) == 0 and _rotary(lib, Hq=0, Hk=0, q=None, k=None) == 0
 
 
+_IN = dict(qo=FAKE, qot=1280, qoh=128)   # the queries in place
+
+
+@pytest.mark.parametrize("kw", [
+    dict(k=FAKE, kt=1280, kh=128, Hk=8), dict(k=FAKE + 2046), dict(k=FAKE + 256), dict(k=FAKE + 2560 - 256 + 2),   # keys over the queries
+    dict(k=FAKE + 2560 * 7 + 512), dict(k=FAKE + 2560 * 7 - 256), dict(k=FAKE + 2048, kt=640),                # rows on; another stride
+    dict(k=FAKE, ko=FAKE, kt=1280, kot=1280), dict(k=FAKE, T=1), dict(k=FAKE + 2 * 128 * 7, T=1, Hk=1),
+    dict(k=FAKE + 128, qt=2048, qh=256, qot=2048, qoh=256, kt=2048, kh=256, Hk=8),                            # half a head on
+    dict(k=FAKE + 256, qt=2100, qh=256, qot=2100, qoh=256, kt=2100, kh=256, Hk=8)])                           # head steps that miss the tokens'
+def test_rotary_in_place_over_the_other_part(lib, kw):
+    """What one part reads while the other is turned where it lies."""
+    assert _rotary(lib, **{**_IN, **kw}) == 1
+
+
 def test_python_binding_refuses():
     x = torch.zeros(4, 256)
     c, s = torch.zeros(4, 256, dtype=torch.float8_e4m3fn), torch.zeros(4, 2, dtype=torch.uint8)

@@ -281,6 +281,37 @@ def test_rotary_in_place_and_strided(D, rot, extra, dt):
         kda.kda_rotary(q, k, pos, freqs, q_out=p[:, D:(Hq + 1) * D].unflatten(1, (Hq, D)))
 
 
+@pytest.mark.parametrize("T", [1, 2, 37])
+@pytest.mark.parametrize("order", ["tokens", "heads", "heads and more", "apart"])
+def test_rotary_one_part_in_place(T, order):
+    """Queries where they lie with keys between their tokens or heads, into new memory and in place."""
+    H, D = 4, 64
+    p = _rows(T, 2 * H * D + 64, "bf16", T).cuda()
+    if order == "tokens":
+        q, k = p[:, :H * D].unflatten(1, (H, D)), p[:, H * D:(H + 2) * D].unflatten(1, (2, D))
+    elif order == "heads":
+        both = p[:, :2 * H * D].contiguous().view(T, 2 * H, D)
+        q, k = both[:, 0::2], both[:, 1::2]
+    elif order == "heads and more":   # the head stride does not divide the tokens', but the tokens do not reach one another
+        both = p[:, :2 * H * D].unflatten(1, (2 * H, D))
+        q, k = both[:, :H], both[:, H:]
+    else:
+        q, k = p[:, :H * D].contiguous().view(T, H, D), p[:, H * D:2 * H * D].contiguous().view(T, H, D)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") * 991 - 1
+    freqs, _ = kda.kda_rotary_freqs(D)
+    yq, yk = kda.kda_rotary(q, k, pos, freqs)
+    keys = k.clone()
+    a, b = kda.kda_rotary(q, k, pos, freqs, q_out=q)
+    assert a is q and torch.equal(q, yq) and torch.equal(b, yk) and torch.equal(k, keys)
+    queries = q.clone()
+    kda.kda_rotary(q, k, pos, freqs, k_out=k)
+    assert torch.equal(q, queries) and torch.equal(k, yk)
+    with pytest.raises(kda.KdaError):
+        kda.kda_rotary(q, q, pos, freqs, q_out=q, k_out=q)
+    with pytest.raises(kda.KdaError):
+        kda.kda_rotary(q, q[:, 1:], pos, freqs, q_out=q)
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_rotary_inverse_is_the_gradient(interleaved):
     """The rotation is linear: <inverse(g), x> = <g, rotation(x)> for any x, the gradient by its definition."""
