@@ -24,7 +24,7 @@ namespace kda {
 namespace dense {
 namespace {
 
-constexpr int kThreads = 128;   // warp 0 loads tiles, 1 issues products, 2 loads scales; all store
+constexpr int kThreads = 128;   // warp 0 loads tiles, 1 issues products, 2 and 3 load scales in turn; all store
 
 // kDeep: one CTA an SM with all of its shared memory, else two.  (256 tokens: one.)
 template <int kRows, bool kDeep>
@@ -78,15 +78,16 @@ __global__ void __launch_bounds__(kThreads)
   // Before the CTA meets: the first loads go out, and the first scales are read.
   const uint32_t at = tc::smem_u32(sm), bar = tc::smem_u32(full);
   const int first = min(nb, F::kStages);
-  uint32_t ww[1], wx[4 * F::kSets];
+  Scales<1> ww;
+  Scales<4 * F::kSets> wx;
   auto load_tile = [&](int i, int st) {
     expect_w(bar + 8 * st, F::kStage);
     tma_load_w<1>(at + st * F::kStage, &mapW, (kb0 + i) * kStageK, (int32_t)n0, bar + 8 * st);
     tma_load_w<1>(at + st * F::kStage + F::kW, &mapX, (kb0 + i) * kStageK, (int32_t)m0, bar + 8 * st);
   };
   auto load_words = [&](int g) {
-    load_scales(sw, blocks, kb0 + 4 * g, words, ww, [&](int) { return (int64_t)tile; });
-    load_scales(sx, blocks, kb0 + 4 * g, words, wx, [&](int i) {
+    ww.load(sw, (N + 127) / 128 * blocks, blocks, kb0 + 4 * g, words, [&](int) { return (int64_t)tile; });
+    wx.load(sx, M * blocks, blocks, kb0 + 4 * g, words, [&](int i) {
       const int r = 32 * i + lane;
       return r < kRows && m0 + r < M ? m0 + r : (int64_t)-1;
     });
@@ -105,8 +106,8 @@ __global__ void __launch_bounds__(kThreads)
   wait_for_previous();
   if (warp == 0) {
     for (int i = 0; i < first; ++i) load_tile(i, i);
-  } else if (warp == 2) {
-    load_words(0);
+  } else if (warp >= 2 && 4 * (warp - 2) < nb) {
+    load_words(warp - 2);
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -152,22 +153,23 @@ __global__ void __launch_bounds__(kThreads)
     }
     ok = __all_sync(0xffffffffu, limit != 0);
     tc::mma_commit_w(done);
-  } else if (warp == 2) {
-    for (int g = 0; 4 * g < nb && ok; ++g) {
+  } else {
+    for (int g = warp - 2; 4 * g < nb; g += 2) {
       const int slot = g % kScaleSlots;
       if (g >= kScaleSlots) ok = wait_w(sempty + slot, (g / kScaleSlots - 1) & 1);
       if (!ok) break;
       uint4* to = reinterpret_cast<uint4*>(sm + F::oScales + slot * F::kScales) + lane;
-      to[0] = make_uint4(ww[0], ww[0], ww[0], ww[0]);
+      const uint32_t w = ww.word(0);
+      to[0] = make_uint4(w, w, w, w);
+      uint32_t x[4 * F::kSets];
 #pragma unroll
-      for (int i = 0; i < 4 * F::kSets; ++i)
-        if (32 * i + lane >= min((int64_t)kRows, M - m0)) wx[i] = kOnes;
+      for (int i = 0; i < 4 * F::kSets; ++i) x[i] = 32 * i + lane < min((int64_t)kRows, M - m0) ? wx.word(i) : kOnes;
 #pragma unroll
-      for (int s = 0; s < F::kSets; ++s) to[32 * (1 + s)] = make_uint4(wx[4 * s], wx[4 * s + 1], wx[4 * s + 2], wx[4 * s + 3]);
+      for (int s = 0; s < F::kSets; ++s) to[32 * (1 + s)] = make_uint4(x[4 * s], x[4 * s + 1], x[4 * s + 2], x[4 * s + 3]);
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(sfull + slot);
-      if (4 * (g + 1) < nb) load_words(g + 1);
+      if (4 * (g + 2) < nb) load_words(g + 2);
     }
   }
   // every product done: the sums are in TMEM, and nothing reads or writes the stages any more

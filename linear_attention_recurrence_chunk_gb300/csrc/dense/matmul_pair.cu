@@ -15,8 +15,9 @@
 // eight storing warps); parts of K in clusters of four and six CTAs for few tiles (256 x 4,096 x 12,288: 21.7 us against the
 // other kernel's 20.9); barriers arrived at with a release at cluster scope, 1,000 cycles each (780 us).
 //
-// Warps of a CTA: 0 loads tiles, 1 issues products (of the leading CTA alone), 2 loads scales, 3 TMEM,
-// 4 to 7 store.
+// Warps of a CTA: 0 loads tiles, 1 issues products (of the leading CTA alone), 2 and 3 load scales, a group of four K
+// blocks each in turn (of rows that are not whole words one warp's loads take longer than a group's products: 4,813 x
+// 1,920 x 10,304 62 us with one, 54 with two), 4 to 7 store.
 #include <limits.h>
 
 #include <algorithm>
@@ -32,8 +33,8 @@ constexpr int kTM = 256, kTN = 240, kThreads = 256, kStages = 6;
 constexpr uint32_t kA = 128 * kStageK, kB = kTN / 2 * kStageK, kStage = kA + kB;
 constexpr uint32_t kScales = 3 * 512;   // one slot: 128 rows of A, twice 128 of W
 constexpr uint32_t oScales = kStages * kStage, oOut = oScales + kScaleSlots * kScales;
-// Per storing warp two pieces of 32 rows by 96 bytes of the output; or 32 rows of 16 sums (17 words apart).
-constexpr uint32_t kPiece = 32 * 96, kTurnRow = 17;
+// Per storing warp two pieces of 32 rows by 96 bytes of the output; or 32 rows of 32 sums (33 words apart).
+constexpr uint32_t kPiece = 32 * 96, kTurnRow = 33;
 constexpr uint32_t oBars = oOut + 4 * 2 * kPiece;
 constexpr int kBars = 2 * kStages + 2 * kScaleSlots + 4;
 constexpr uint32_t kAlloc = oBars + kBars * 8 + 8 + 1024;
@@ -98,18 +99,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   // Before the cluster meets: the first scales are read, and the leading CTA's own first loads go out.
   const uint32_t at = tc::smem_u32(sm), lead = tc::mapa_shared(full, 0);
-  uint32_t wa[4], wb[8];
+  Scales<4> wa;
+  Scales<8> wb;
   int left_a = 0, left_b = 0;   // rows of A, and of W, from this lane's first one on
   auto load_words = [&](uint32_t t, int gg) {   // of group gg of tile t
     uint32_t im, in;
     place(t, tm, tn, im, in);
     left_a = (int)min(M - (int64_t)im * kTM - 128 * rank - lane, (int64_t)128);
     left_b = (int)min(N - (int64_t)in * kTN - lane, (int64_t)256);
-    load_scales(sa, blocks, 4 * gg, words, wa, [&](int i) {
+    wa.load(sa, M * blocks, blocks, 4 * gg, words, [&](int i) {
       const int64_t m = (int64_t)im * kTM + 128 * rank + 32 * i + lane;
       return m < M ? m : -1;
     });
-    load_scales(sw, blocks, 4 * gg, words, wb, [&](int i) {
+    wb.load(sw, (N + kBlock - 1) / kBlock * blocks, blocks, 4 * gg, words, [&](int i) {
       const int64_t c = (int64_t)in * kTN + 32 * i + lane;
       return c < N ? c / kBlock : -1;
     });
@@ -139,8 +141,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t im, in;
     place(pair, tm, tn, im, in);
     for (int kb = 0; kb < early; ++kb) load_tile(kb, kb, (int32_t)(im * kTM), (int32_t)(in * kTN));
-  } else if (warp == 2) {
-    load_words(pair, 0);
+  } else if (warp == 2 || warp == 3) {
+    if (warp == 2 || groups > 1) load_words(pair, warp - 2);
+    else if (pair + pairs < tiles) load_words(pair + pairs, 0);
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -199,30 +202,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, limit != 0);
       for (int i = it > 2 ? it - 2 : 0; i < it; ++i) ok = wait_w(tempty + (i & 1), (i >> 1) & 1) && ok;
     }
-  } else if (warp == 2) {
-    uint32_t g = 0, t = pair;
-    int gg = 0;
+  } else if (warp < 4) {
+    const uint32_t first = warp - 2;
+    uint32_t g = first, t = pair;
+    int gg = (int)first;
+    if (gg == groups) gg = 0, t += pairs;
     while (t < tiles) {
       const uint32_t slot = g % kScaleSlots;
       if (g >= kScaleSlots && !(ok = wait_w(sempty + slot, (g / kScaleSlots - 1) & 1))) break;
       uint4* to = reinterpret_cast<uint4*>(sm + oScales + slot * kScales) + lane;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) wa[i] = 32 * i < left_a ? wa[i] : kOnes;   // rows behind the last: a factor 1
-#pragma unroll
-      for (int i = 0; i < 8; ++i) wb[i] = 32 * i < left_b ? wb[i] : kOnes;
-      to[0] = make_uint4(wa[0], wa[1], wa[2], wa[3]);
-      to[32] = make_uint4(wb[0], wb[1], wb[2], wb[3]);
-      to[64] = make_uint4(wb[4], wb[5], wb[6], wb[7]);
+      const auto a_word = [&](int i) { return 32 * i < left_a ? wa.word(i) : kOnes; };   // rows behind the last: a factor 1
+      const auto b_word = [&](int i) { return 32 * i < left_b ? wb.word(i) : kOnes; };
+      to[0] = make_uint4(a_word(0), a_word(1), a_word(2), a_word(3));
+      to[32] = make_uint4(b_word(0), b_word(1), b_word(2), b_word(3));
+      to[64] = make_uint4(b_word(4), b_word(5), b_word(6), b_word(7));
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) arrive_cluster(tc::mapa_shared(sfull + slot, 0));
-      if (++gg == groups) gg = 0, t += pairs;
+      for (int i = 0; i < 2; ++i)
+        if (++gg == groups) gg = 0, t += pairs;
       if (t < tiles) load_words(t, gg);
-      ++g;
+      g += 2;
     }
-    for (uint32_t i = g > kScaleSlots ? g - kScaleSlots : 0; i < g; ++i)
-      ok = wait_w(sempty + i % kScaleSlots, (i / kScaleSlots) & 1) && ok;
-  } else if (warp >= 4) {
+    for (uint32_t i = 2; i <= kScaleSlots && g >= first + i; i += 2) ok = wait_w(sempty + (g - i) % kScaleSlots, ((g - i) / kScaleSlots) & 1) && ok;
+  } else {
     const int q = warp - 4;
     uint8_t* mine = sm + oOut + q * 2 * kPiece;
     constexpr int kCols = 96 / sizeof(T);   // of a piece
@@ -270,19 +273,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else {   // through shared memory: a row's columns next to one another
         float* turn = reinterpret_cast<float*>(mine);
 #pragma unroll 1
-        for (int c = 0; c < cols; c += 16) {
-          float v[16];
-          tc::tmem_ld16(acc + c, v);
-          if (c + 16 >= cols) freed();
+        for (int c = 0; c < cols; c += 32) {   // (the last 32 of 240 reach into the next columns of TMEM: not stored)
+          uint32_t v[32];
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) tmem_ld8_begin(acc + c + i, v + i);
+          tmem_ld_end(v);
+          if (c + 32 >= cols) freed();
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) turn[lane * kTurnRow + i] = v[i];
+          for (int i = 0; i < 32; ++i) turn[lane * kTurnRow + i] = __uint_as_float(v[i]);
           __syncwarp();
-          const int cc = c + (lane & 15);
-          if (cc < cols) {
-            T* o = out + (m0 + (lane >> 4)) * ldo + n0 + cc;
+          if (c + lane < cols) {
+            T* o = out + m0 * ldo + n0 + c + lane;
+            if (rows == 32) {
+#pragma unroll
+              for (int r = 0; r < 32; ++r, o += ldo) *o = from_f32<T>(turn[r * kTurnRow + lane]);
+            } else {
 #pragma unroll 4
-            for (int r = lane >> 4; r < rows; r += 2, o += 2 * ldo) *o = from_f32<T>(turn[r * kTurnRow + (lane & 15)]);
+              for (int r = 0; r < rows; ++r, o += ldo) *o = from_f32<T>(turn[r * kTurnRow + lane]);
+            }
           }
         }
       }

@@ -170,36 +170,60 @@ __device__ __forceinline__ void tmem_free_pair(uint32_t taddr, uint32_t cols) {
 
 constexpr int kScaleSlots = 4;   // groups of four K blocks whose scales are on their way (two of them in TMEM)
 
-// Scale words of four K blocks, kb .. kb + 3 of `blocks` (bytes behind the last: 127, a factor 1), for kWords rows:
-// row(i) gives a row's number, negative for none (any word then).  No branch stands between the loads, so
-// that all are on their way together, and nothing here waits for whole words.  `words`: rows of whole 32-bit words.
-template <int kWords, typename F>
-__device__ __forceinline__ void load_scales(const uint8_t* scales, int32_t blocks, int32_t kb, bool words, uint32_t (&w)[kWords],
-                                            F row) {
-  int64_t r[kWords];
-#pragma unroll
-  for (int i = 0; i < kWords; ++i) {
-    r[i] = row(i);
-    r[i] = r[i] < 0 ? 0 : r[i];
-  }
-  if (words) {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = __ldcg(reinterpret_cast<const uint32_t*>(scales + r[i] * blocks + kb));
-  } else {
-    uint32_t b[kWords][4];
-#pragma unroll
-    for (int i = 0; i < kWords; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) b[i][j] = __ldcg(scales + r[i] * blocks + (kb + j < blocks ? kb + j : blocks - 1));
+// Scale words of four K blocks, kb .. kb + 3 of `blocks` (bytes behind the last: 127, a factor 1), for kWords rows of a
+// matrix's `size` scales: row(i) gives a row's number, negative for none (any word then).  No branch stands between the
+// loads, so that all are on their way together, and nothing waits for them before word() takes them.  Rows of whole
+// 32-bit words (`words`) take one load each.  Others take the two words around their four bytes (the same
+// one twice where it holds all that are there), each with a byte of the row in it; and byte after byte where such a word reaches over
+// the scales' ends.  (With bytes alone 4,813 x 1,920 x 10,304 took 66 us against 54, 331 x 2,688 x 4,992 12.1 against 9.5.)
+constexpr uint32_t kOnes = 0x7f7f7f7fu;   // four factors of 1
+template <int kWords>
+struct Scales {
+  uint32_t lo[kWords], hi[kWords], shift[kWords];
+  uint32_t kept;   // the bytes of blocks that are there
+  template <typename F>
+  __device__ __forceinline__ void load(const uint8_t* scales, int64_t size, int32_t blocks, int32_t kb, bool words, F row) {
+    const uint8_t* p[kWords];
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
-      w[i] = 0;
+      const int64_t r = row(i);
+      p[i] = scales + (r < 0 ? 0 : r) * blocks + kb;
+      hi[i] = shift[i] = 0;   // (a copy of lo would wait for it)
+    }
+    const int n = min(blocks - kb, 4);
+    kept = 0xffffffffu >> (32 - 8 * n);
+    if (words) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[i] |= (kb + j < blocks ? b[i][j] : 127u) << (8 * j);
+      for (int i = 0; i < kWords; ++i) lo[i] = __ldcg(reinterpret_cast<const uint32_t*>(p[i]));
+      return;
+    }
+    const uintptr_t from = reinterpret_cast<uintptr_t>(scales), to = from + size;
+    uintptr_t a[kWords], b[kWords];
+    bool inside = true;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      a[i] = reinterpret_cast<uintptr_t>(p[i]) & ~(uintptr_t)3, b[i] = (reinterpret_cast<uintptr_t>(p[i]) + n - 1) & ~(uintptr_t)3;
+      inside = inside && a[i] >= from && b[i] + 4 <= to;
+    }
+    if (__all_sync(0xffffffffu, inside)) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        lo[i] = __ldcg(reinterpret_cast<const uint32_t*>(a[i]));
+        hi[i] = __ldcg(reinterpret_cast<const uint32_t*>(b[i]));
+        shift[i] = 8 * (uint32_t)(reinterpret_cast<uintptr_t>(p[i]) & 3);
+      }
+    } else {
+      uint32_t c[kWords][4];
+#pragma unroll
+      for (int i = 0; i < kWords; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[i][j] = __ldcg(p[i] + min(j, n - 1));
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) lo[i] = c[i][0] | c[i][1] << 8 | c[i][2] << 16 | c[i][3] << 24;
     }
   }
-}
-constexpr uint32_t kOnes = 0x7f7f7f7fu;   // four factors of 1
+  __device__ __forceinline__ uint32_t word(int i) const { return (__funnelshift_r(lo[i], hi[i], shift[i]) & kept) | (kOnes & ~kept); }
+};
 inline bool scale_words(const void* a, const void* b, int64_t blocks) {
   return blocks % 4 == 0 && reinterpret_cast<uintptr_t>(a) % 4 == 0 && reinterpret_cast<uintptr_t>(b) % 4 == 0;
 }
@@ -217,7 +241,9 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encode() {
   return fn;
 }
 
-// Boxes of 128 bytes of K (zeros behind K) by box_rows rows (zeros behind the last), 128-byte swizzle.
+// Boxes of 128 bytes of K (zeros behind K) by box_rows rows (zeros behind the last), 128-byte swizzle.  L2 takes 256 bytes
+// at a time of rows that begin on 128-byte boundaries (128: 1 x 16,416 x 4,096 13.8 us against 13.6), else 128 (331 x 2,688 x
+// 4,976 13.5 us against 14.7).
 inline bool codes_map(CUtensorMap* m, const uint8_t* base, int64_t rows, int64_t K, int64_t stride, int box_rows) {
   const auto fn = tensor_map_encode();
   if (!fn) return false;
@@ -225,8 +251,10 @@ inline bool codes_map(CUtensorMap* m, const uint8_t* base, int64_t rows, int64_t
   const cuuint64_t strides[1] = {(cuuint64_t)stride};
   const cuuint32_t box[2] = {kStageK, (cuuint32_t)box_rows};
   const cuuint32_t es[2] = {1, 1};
+  const bool lines = stride % 128 == 0 && reinterpret_cast<uintptr_t>(base) % 128 == 0;
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_SWIZZLE_128B, lines ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Boxes of box_cols x box_rows of an output of elements of eb bytes, for stores.

@@ -177,3 +177,19 @@ def test_many_rows_of_few_columns():
     a, sa, w, sw = (t.cuda() for t in _exact_operands(M, N, K, 5))
     got = kda.kda_fp8_matmul(a, sa, w, sw)
     assert torch.equal(got, (_dense(a, sa, 1) @ _dense(w, sw, 128).t()).bfloat16())
+
+
+@pytest.mark.parametrize("pairs", ["0", "1"])
+@pytest.mark.parametrize("M,N,K", [(130, 300, 16), (257, 500, 272), (129, 300, 656), (70, 900, 1296)])
+def test_scales_at_any_address(M, N, K, pairs, monkeypatch):
+    """Scale bytes that begin and end between 32-bit words, with other bytes around them."""
+    monkeypatch.setenv("KDA_FP8_PAIR", pairs)
+    a, sa, w, sw = (t.cuda() for t in _exact_operands(M, N, K, 7))
+    want = kda.kda_fp8_matmul(a, sa, w, sw, torch.float32)
+    assert torch.equal(want, (_dense(a, sa, 1) @ _dense(w, sw, 128).t()).float())
+    for i in range(1, 8):
+        def moved(t, by):
+            room = torch.full((t.numel() + 8,), 255, dtype=torch.uint8, device="cuda")
+            room[by:by + t.numel()] = t.flatten()
+            return room[by:by + t.numel()].view(t.shape)
+        assert torch.equal(kda.kda_fp8_matmul(a, moved(sa, i % 4), w, moved(sw, i // 2), torch.float32), want)
