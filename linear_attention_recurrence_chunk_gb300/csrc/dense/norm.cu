@@ -8,7 +8,7 @@
 // the same registers, so that nothing is read twice.  Rows of a head's size share a warp.
 // Measured (replayed from a graph): 32,768 x 4,096 of bf16 with a residual 156 us (6.9 TB/s), in 8 bits 142 us (6.6 TB/s;
 // DRAM 80 %, issue slots 73 %); 1,000,000 x 128 153 us (6.7 TB/s); 16,384 x 2,001 of fp32 79 us (6.7 TB/s); bf16 rows of odd
-// width by 2-byte accesses 4.4 TB/s (8,192 x 8,001).  256 x 4,096: 3.7 us, one row 2.1 us: launch and latency.  Slower: a
+// width by 2-byte accesses 4.4 TB/s (8,192 x 8,001); 32,000 x 768 of bf16 with a residual 33 us (5.9 TB/s).  256 x 4,096: 3.7 us, one row 2.1 us: launch and latency.  Slower: a
 // block with row after row and the next one's loads ahead (32,768 x 4,096 172 us: half the warps an SM).
 #include <type_traits>
 
@@ -261,10 +261,15 @@ cudaError_t launch1(const NormProblem& p, cudaStream_t stream) {
                     at(p.w, 16) && (p.codes ? at(p.codes, 8) : at(p.y, 16));
   if (p.C <= kNarrow) return wide ? launch_narrow<T, true>(p, stream) : launch_narrow<T, false>(p, stream);
   const int chunks = (int)((p.C + 255) / 256);   // 256 columns each, at most 128
-  // One or two chunks: a warp a row.  Else two a warp, four where 32 warps are not enough and for 8-bit output of
+  // One or two chunks: a warp a row; three or four too where there are many rows of at most 3,584 bytes to read (32,000 x
+  // 520 of bf16: 14 us, 34 with two warps, whose blocks start too slowly; 32,000 x 768 with a residual 33 and 37; but
+  // 1,024 with a residual 43 and 42, of fp32 83 and 79, and 500 x 768 2.4 and 2.3).  Else two chunks a warp, four where
+  // 32 warps are not enough and for 8-bit output of
   // many rows (32,768 x 4,096: 157 us with two, 143 with four; 16,384 x 8,192: 182 and 147; but 1 x 4,096: 3.0 and
   // 3.6, 256 x 8,192: 5.5 and 5.9; in the input's type the two differ by 1 %).
   if (chunks <= 1) return wide ? launch2<T, 1, true>(p, 1, stream) : launch2<T, 1, false>(p, 1, stream);
+  if (chunks > 2 && chunks <= 4 && p.T >= 4096 && p.C * (int64_t)sizeof(T) * (p.r ? 2 : 1) <= 3584)
+    return wide ? launch2<T, 4, true>(p, 1, stream) : launch2<T, 4, false>(p, 1, stream);
   const int J = chunks > 64 || (p.codes && chunks > 8 && p.T >= 1024) ? 4 : 2, warps = (chunks + J - 1) / J;
   if (J == 2) return wide ? launch2<T, 2, true>(p, warps, stream) : launch2<T, 2, false>(p, warps, stream);
   return wide ? launch2<T, 4, true>(p, warps, stream) : launch2<T, 4, false>(p, warps, stream);

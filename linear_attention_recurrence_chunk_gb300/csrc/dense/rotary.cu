@@ -44,7 +44,7 @@ struct Shape {
   int32_t split, heads;   // warps of a token, heads of each
   int32_t tokens;         // of a warp at a time (1 where split > 1)
   int32_t parts, turned;  // items of a head: of pairs first, then of channels that stay
-  uint32_t m_parts, m_token;   // (tokens > 1: a token has at most 96 items)
+  uint32_t m_parts, m_token;   // (tokens > 1: a token has at most 128 items)
 };
 
 // kE consecutive values of one side of kE pairs.
@@ -195,14 +195,21 @@ cudaError_t launch(const RotaryProblem& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   // Two blocks an SM.  With fewer tokens than warps, several warps a token, each with an item a lane at least;
-  // with many tokens of few heads, several tokens a warp, three items a lane (2 + 1 heads of 64, 65,536 tokens:
-  // 16 us, 34 with one token at a time).
+  // with few items a token (a round of a warp has 96), as many tokens a warp as fill its rounds, and the rounds of all
+  // warps, best (2 + 1 heads of 64, 65,536 tokens: 16 us, 34 with one token at a time; 12 + 1 heads of 64, 43,045 tokens:
+  // 31 and 37 us; of 24 + 2 heads of 128 in fp32, 208 items, 65 and 61).
   const int64_t warps = (int64_t)2 * sms * kWarps, items = (int64_t)H * s.parts;
   const int64_t split = std::min<int64_t>(std::max<int64_t>(1, warps / p.T), std::max<int64_t>(1, items / 32));
   s.heads = (int)((H + split - 1) / split);
   s.split = (H + s.heads - 1) / s.heads;
-  if (s.split == 1)
-    s.tokens = (int)std::max<int64_t>(1, std::min<int64_t>({8, 32 * kItems / items, 512 / std::max(s.half, 1), p.T / warps}));
+  if (s.split == 1 && items <= 128) {
+    double most = 0;   // of the places in all rounds, those with an item
+    for (int64_t k = 1; k <= std::min<int64_t>(8, 512 / std::max(s.half, 1)); ++k) {
+      const int64_t rounds = (k * items + 32 * kItems - 1) / (32 * kItems), turns = ((p.T + k - 1) / k + warps - 1) / warps;
+      const double full = (double)(p.T * items) / (double)(turns * warps * rounds * 32 * kItems);
+      if (full > 1.03 * most) most = full, s.tokens = (int)k;
+    }
+  }
   if (s.tokens > 1) s.m_token = magic((uint32_t)(s.heads * s.parts));
   const size_t smem = (size_t)s.half * 8 * (1 + kWarps * s.tokens);   // 36 KB at most
   const int64_t units = s.split == 1 ? (p.T + s.tokens - 1) / s.tokens : p.T * s.split;

@@ -110,7 +110,7 @@ def _norm_tol(y, dt):
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("add", [False, True])
 @pytest.mark.parametrize("T,C", [(1, 1), (1, 7), (9, 16), (33, 8), (70, 12), (300, 24), (129, 64), (1000, 100), (65, 128), (41, 127), (6, 129), (5, 256), (3, 257), (17, 512), (64, 1001), (5, 4096), (3, 12288), (2, 16385),
-                                 (1, 32768)])
+                                 (1, 32768), (4100, 600), (4099, 777), (5000, 513), (4097, 896)])
 def test_norm(T, C, add, dt):
     x, r = _rows(T, C, dt, T * C), _rows(T, C, dt, T * C + 1) if add else None
     w = torch.randn(C, generator=torch.Generator().manual_seed(3))
@@ -340,7 +340,8 @@ def test_rotary_far_positions_of_fast_pairs():
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("interleaved", [False, True])
-@pytest.mark.parametrize("T,Hq,Hk,D,rot", [(9731, 1, 1, 64, 64), (20000, 2, 1, 64, 32), (10007, 1, 0, 6, 4), (40001, 4, 2, 128, 128)])
+@pytest.mark.parametrize("T,Hq,Hk,D,rot", [(9731, 1, 1, 64, 64), (20000, 2, 1, 64, 32), (10007, 1, 0, 6, 4), (40001, 4, 2, 128, 128),
+                                             (20000, 12, 1, 64, 64), (9000, 8, 8, 128, 64), (15001, 9, 3, 20, 12)])
 def test_rotary_many_tokens(T, Hq, Hk, D, rot, interleaved, dt):
     """Few heads and more tokens than the chip holds warps, the formula in fp64 on the GPU (angles below 2^31 * 1e-4, so
     that fp64's own error in them stays below 2^-30)."""
