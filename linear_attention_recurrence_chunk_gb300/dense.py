@@ -77,11 +77,6 @@ def _dtype(dt: torch.dtype) -> int:
     return code
 
 
-def _e4m3(name: str, t: torch.Tensor):
-    if t.dtype is not _E4M3:
-        raise TypeError(f"{name}: {_E4M3} expected, got {t.dtype}")
-
-
 def _matrix(name: str, t: torch.Tensor, dev: int) -> Tuple[int, int, int]:
     """(rows, columns, row stride) of [rows, columns] with contiguous columns."""
     if t.dim() != 2 or t.get_device() != dev:
@@ -93,12 +88,20 @@ def _matrix(name: str, t: torch.Tensor, dev: int) -> Tuple[int, int, int]:
     return T, C, s if T > 1 else C   # a stride over one row has no meaning
 
 
-def _scales(name: str, t: torch.Tensor, rows: int, cols: int, dev: int) -> int:
-    if t.dtype is not _U8:
-        raise TypeError(f"{name}: uint8 expected, got {t.dtype}")
-    if t.get_device() != dev or not t.is_contiguous() or t.shape != (rows, cols):
-        raise ValueError(f"{name}: a contiguous [{rows}, {cols}] tensor on cuda:{dev} expected, got {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+def _stored(name: str, codes: torch.Tensor, scales: torch.Tensor, block_rows: int, dev: int) -> Tuple[int, int, int, int]:
+    """(rows, columns, row stride, pointer of the scales) of a matrix in 8 bits."""
+    if scales.dtype is not _U8:
+        raise TypeError(f"scales of {name}: uint8 expected, got {scales.dtype}")
+    if codes.dim() != 2 or codes.get_device() != dev or scales.get_device() != dev or not scales.is_contiguous():
+        raise ValueError(f"{name}: a matrix of codes and contiguous scales on cuda:{dev} expected, got {tuple(codes.shape)} on {codes.device}, "
+                         f"{tuple(scales.shape)} on {scales.device}")
+    T, C = codes.shape
+    s, c = codes.stride()
+    if c != 1 and C > 1:
+        raise ValueError(f"{name}: contiguous columns expected")
+    if scales.shape != (T if block_rows == 1 else (T + 127) // 128, (C + 127) // 128):
+        raise ValueError(f"{name}: a scale for each {block_rows} x 128 values of {tuple(codes.shape)} expected, got {tuple(scales.shape)}")
+    return T, C, s if T > 1 else C, scales.data_ptr()
 
 
 def _block_rows(n: int):
@@ -117,7 +120,7 @@ def kda_fp8_quant(x: torch.Tensor, block_rows: int = 1, stream=None) -> Tuple[to
     _block_rows(block_rows)
     codes = _empty((T, C), dtype=_E4M3, device=x.device)
     scales = _empty((T if block_rows == 1 else (T + 127) // 128, (C + 127) // 128), dtype=_U8, device=x.device)
-    st = _lib().kda_fp8_quant(x.data_ptr(), xs, T, C, block_rows, dt, codes.data_ptr(), scales.data_ptr(), _current_raw_stream(dev))
+    st = (_fns or _lib()).kda_fp8_quant(x.data_ptr(), xs, T, C, block_rows, dt, codes.data_ptr(), scales.data_ptr(), _current_raw_stream(dev))
     if st:
         _fail(st, "kda_fp8_quant")
     return codes, scales
@@ -127,17 +130,18 @@ def kda_fp8_values(codes: torch.Tensor, scales: torch.Tensor, block_rows: int = 
                    stream=None) -> torch.Tensor:
     """The values ``[T, C]`` of ``dtype`` that codes ``[T, C]`` (contiguous) and their scale
     bytes stand for."""
-    _e4m3("codes", codes)
+    if codes.dtype is not _E4M3:
+        raise TypeError(f"codes: {_E4M3} expected, got {codes.dtype}")
     dev = _device("codes", codes)
     if stream is not None or dev != _current_device():
         return _run(dev, stream, lambda _: kda_fp8_values(codes, scales, block_rows, dtype))
-    T, C, _ = _matrix("codes", codes, dev)
+    _block_rows(block_rows)
+    T, C, _, sp = _stored("codes", codes, scales, block_rows, dev)
     if not codes.is_contiguous():
         raise ValueError("codes: a contiguous matrix is expected")
-    _block_rows(block_rows)
-    dt, sp = _dtype(dtype), _scales("scales", scales, T if block_rows == 1 else (T + 127) // 128, (C + 127) // 128, dev)
+    dt = _dtype(dtype)
     y = _empty((T, C), dtype=dtype, device=codes.device)
-    st = _lib().kda_fp8_values(codes.data_ptr(), sp, T, C, block_rows, dt, y.data_ptr(), _current_raw_stream(dev))
+    st = (_fns or _lib()).kda_fp8_values(codes.data_ptr(), sp, T, C, block_rows, dt, y.data_ptr(), _current_raw_stream(dev))
     if st:
         _fail(st, "kda_fp8_values")
     return y
@@ -151,9 +155,12 @@ def _norm(x, residual, weight, eps, h, fp8, stream):
     dtype = x.dtype
     dt, rp, rs, wp, hp, device = _dtype(dtype), None, 0, None, None, x.device
     if residual is not None:
-        if residual.dtype is not dtype or residual.shape != x.shape:
-            raise ValueError(f"residual: {dtype} {tuple(x.shape)} expected, got {residual.dtype} {tuple(residual.shape)}")
-        rs, rp = _matrix("residual", residual, dev)[2], residual.data_ptr()
+        if residual.dtype is not dtype or residual.shape != x.shape or residual.get_device() != dev:
+            raise ValueError(f"residual: {dtype} {tuple(x.shape)} on cuda:{dev} expected, got {residual.dtype} {tuple(residual.shape)} on {residual.device}")
+        rs, c = residual.stride()
+        if c != 1 and C > 1:
+            raise ValueError("residual: contiguous columns expected")
+        rp = residual.data_ptr()
     if weight is not None:
         if weight.dtype is not torch.float32:
             raise TypeError(f"weight: torch.float32 expected, got {weight.dtype}")
@@ -169,11 +176,11 @@ def _norm(x, residual, weight, eps, h, fp8, stream):
         hp = h.data_ptr()
     if fp8:
         y, scales = _empty((T, C), dtype=_E4M3, device=device), _empty((T, (C + 127) // 128), dtype=_U8, device=device)
-        st = _lib().kda_add_rmsnorm(x.data_ptr(), xs, rp, rs, wp, eps, T, C, dt, hp, None, y.data_ptr(), scales.data_ptr(),
+        st = (_fns or _lib()).kda_add_rmsnorm(x.data_ptr(), xs, rp, rs, wp, eps, T, C, dt, hp, None, y.data_ptr(), scales.data_ptr(),
                                     _current_raw_stream(dev))
     else:
         y, scales = _empty((T, C), dtype=dtype, device=device), None
-        st = _lib().kda_add_rmsnorm(x.data_ptr(), xs, rp, rs, wp, eps, T, C, dt, hp, y.data_ptr(), None, None, _current_raw_stream(dev))
+        st = (_fns or _lib()).kda_add_rmsnorm(x.data_ptr(), xs, rp, rs, wp, eps, T, C, dt, hp, y.data_ptr(), None, None, _current_raw_stream(dev))
     if st:
         _fail(st, "kda_add_rmsnorm")
     return (y, scales, h) if fp8 else (y, h)
@@ -200,17 +207,15 @@ def kda_fp8_matmul(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_s
     """``a w^T``, ``[M, N]`` of ``dtype``: a ``[M, K]`` with scales ``[M, ceil(K / 128)]`` and w ``[N, K]``
     with scales ``[ceil(N / 128), ceil(K / 128)]``.  K and the row strides are multiples of 16;
     ``out`` (whose type counts then) may have any row stride."""
-    _e4m3("a", a)
-    _e4m3("w", w)
+    if a.dtype is not _E4M3 or w.dtype is not _E4M3:
+        raise TypeError(f"a and w: {_E4M3} expected, got {a.dtype} and {w.dtype}")
     dev = _device("a", a)
     if stream is not None or dev != _current_device():
         return _run(dev, stream, lambda _: kda_fp8_matmul(a, a_scales, w, w_scales, dtype, out))
-    M, K, lda = _matrix("a", a, dev)
-    N, KW, ldw = _matrix("w", w, dev)
+    M, K, lda, sa = _stored("a", a, a_scales, 1, dev)
+    N, KW, ldw, sw = _stored("w", w, w_scales, 128, dev)
     if KW != K:
         raise ValueError(f"w: [N, {K}] expected, got {tuple(w.shape)}")
-    kb = (K + 127) // 128
-    sa, sw = _scales("a_scales", a_scales, M, kb, dev), _scales("w_scales", w_scales, (N + 127) // 128, kb, dev)
     if out is None:
         dt, ldo = _dtype(dtype), N
         out = _empty((M, N), dtype=dtype, device=a.device)
@@ -218,7 +223,7 @@ def kda_fp8_matmul(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_s
         if out.shape != (M, N):
             raise ValueError(f"out: [{M}, {N}] expected, got {tuple(out.shape)}")
         dt, ldo = _dtype(out.dtype), _matrix("out", out, dev)[2]
-    st = _lib().kda_fp8_matmul(a.data_ptr(), lda, sa, w.data_ptr(), ldw, sw, M, N, K, dt, out.data_ptr(), ldo, _current_raw_stream(dev))
+    st = (_fns or _lib()).kda_fp8_matmul(a.data_ptr(), lda, sa, w.data_ptr(), ldw, sw, M, N, K, dt, out.data_ptr(), ldo, _current_raw_stream(dev))
     if st:
         _fail(st, "kda_fp8_matmul")
     return out
@@ -315,7 +320,7 @@ def kda_rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tens
         kop = k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
-    st = _lib().kda_rotary(q.data_ptr(), qt, qh, Hq, kp, kt, kh, Hk, pp, T, D, 2 * n, fp, amplitude, (1 if interleaved else 0) | (2 if inverse else 0),
+    st = (_fns or _lib()).kda_rotary(q.data_ptr(), qt, qh, Hq, kp, kt, kh, Hk, pp, T, D, 2 * n, fp, amplitude, (1 if interleaved else 0) | (2 if inverse else 0),
                            dt, q_out.data_ptr(), qot, qoh, kop, kot, koh, _current_raw_stream(dev))
     if st:
         _fail(st, "kda_rotary")
