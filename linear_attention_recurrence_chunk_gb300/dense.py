@@ -295,7 +295,9 @@ def kda_rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tens
     if q.dim() != 3:
         raise ValueError(f"q: [tokens, heads, channels] expected, got {tuple(q.shape)}")
     T, Hq, D = q.shape
-    qt, qh = _heads("q", q, T, D, dev, dtype)
+    qt, qh, qc = q.stride()
+    if qc != 1 and D > 1:
+        raise ValueError("q: contiguous channels are expected")
     n = freqs.numel()
     pp, fp = _vector("positions", positions, T, torch.int32, dev), _vector("freqs", freqs, n, torch.float64, dev)
     if q_out is None:
