@@ -5,13 +5,15 @@
 // Bound: the weights' bytes from HBM.  So the weights are the 128-row operand of the tensor core and
 // the tokens (kRows of them, 16 to 256) its columns: no row of the instruction is padding however
 // few tokens there are.  A cluster of CTAs splits K of one tile, so that few tiles still
-// fill the chip; its partial sums meet in distributed shared memory in a fixed order, with no scratch memory
-// and one launch.
-// Measured (replayed from a graph): 1 x 16,416 x 4,096 13.0 us (the bytes' floor 9.9; DRAM is busy 57 % of it, the first
-// bytes come after 3 us), 8 x 2,052 x 512 2.4 us, 64 x 4,096 x 12,288 13.7 us (7.6), 256 x 4,096 x 12,288 17.3 us (8.2: a
+// fill the chip; each sends the others the sums that they join, through distributed shared memory, and adds its own
+// share in a fixed order, with no scratch memory and one launch.
+// Measured (replayed from a graph): 1 x 16,416 x 4,096 13.0 us (the bytes' floor 9.9; DRAM is busy 56 % of it, the first
+// bytes come after 3 us), 8 x 2,052 x 512 2.4 us, 64 x 4,096 x 12,288 12.2 us (7.6), 256 x 4,096 x 12,288 16.7 us (8.2: a
 // K block takes some 400 cycles, 256 of them products, and the join 2 us).  In a loop of K blocks the issue counts
 // as much as the products: see mma_block_w and wait_lane.  Not faster: pairs of CTAs on 256 rows of W (256 x
-// 4,096 x 12,288 18.4 us against 18.5), eight-CTA clusters beyond 15 of them (two waves).
+// 4,096 x 12,288 18.4 us against 18.5), eight-CTA clusters beyond 15 of them (two waves).  Joining by loads from the other
+// CTAs took 14.9 us for 128 x 4,096 x 12,288, stores to them 13.4; stores of four tokens of a weight, whose
+// lanes lie apart, 17.2; a CTA's own share stored by its own address 14.0.
 #include <limits.h>
 
 #include <algorithm>
@@ -45,10 +47,8 @@ struct Few {
   static_assert(kStages * kStage >= kRows * 512 && kBars <= 32 && kAlloc <= 227 * 1024, "shared memory; partial sums take the stages' place");
 };
 
-__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
-  float4 x;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(addr) : "memory");
-  return x;
+__device__ __forceinline__ void st_cluster(uint32_t addr, float x) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
 }
 
 __device__ __forceinline__ uint32_t cluster_address(uint32_t shared, uint32_t rank) {
@@ -201,44 +201,43 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
   } else {
-    float* sums = reinterpret_cast<float*>(sm);   // [kRows][128]
+    // This CTA joins the tile's tokens part, part + split, ...: the others send it their sums of these, a token's 32 weights
+    // of a warp side by side, to [part][token / split][128].
+    const int R = kRows / split, down = __ffs(split) - 1;
+    const uint32_t to = at + (part * R * 128 + threadIdx.x) * 4;
+    cluster_meet();   // all products of the cluster are done: the sums take the stages' place
     if (ok) {
 #pragma unroll 1
       for (int c = 0; c < rows; c += 16) {
         float v[16];
         tc::tmem_ld16(td + c, v);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) sums[(c + e) * 128 + threadIdx.x] = v[e];
+        for (int e = 0; e < 16; ++e) st_cluster(cluster_address(to, e & (split - 1)) + ((c + e) >> down) * 512, v[e]);
       }
     }
     tc::cluster_sync_all();
     if (ok) {
-      // this CTA's rows are part, part + split, ...: a warp takes eight at a time, a lane four columns of each
+      // a warp takes eight tokens at a time, a lane four columns of each
       constexpr int kAt = kRows < 64 ? 4 : 8;
       const int64_t nl = n0 + 4 * lane;
       const int left = (int)(N - nl < 4 ? N - nl : 4);   // columns of this lane
-      const uint32_t from = tc::smem_u32(sums + 4 * lane);
-      for (int r0 = part + split * kAt * warp; r0 < rows; r0 += split * kAt * (kThreads / 32)) {
-        float4 x[kAt] = {};
+      const float4* sums = reinterpret_cast<const float4*>(sm) + lane;
+      for (int i0 = kAt * warp; part + split * i0 < rows; i0 += kAt * (kThreads / 32)) {
+        float4 x[kAt];
+#pragma unroll
+        for (int j = 0; j < kAt; ++j) x[j] = sums[min(i0 + j, R - 1) * 32];
 #pragma unroll 1
-        for (int s = 0; s < split; s += 2) {   // in the order of K, two parts on their way
-          const uint32_t p0 = cluster_address(from, s), p1 = cluster_address(from, min(s + 1, split - 1));
-          float4 y0[kAt], y1[kAt];
+        for (int s = 1; s < split; ++s) {   // in the order of K
+          float4 y[kAt];
 #pragma unroll
-          for (int j = 0; j < kAt; ++j) y0[j] = ld_cluster(p0 + min(r0 + split * j, rows - 1) * 512);
+          for (int j = 0; j < kAt; ++j) y[j] = sums[(s * R + min(i0 + j, R - 1)) * 32];
 #pragma unroll
-          for (int j = 0; j < kAt; ++j) y1[j] = ld_cluster(p1 + min(r0 + split * j, rows - 1) * 512);
-#pragma unroll
-          for (int j = 0; j < kAt; ++j) x[j].x += y0[j].x, x[j].y += y0[j].y, x[j].z += y0[j].z, x[j].w += y0[j].w;
-          if (s + 1 < split) {
-#pragma unroll
-            for (int j = 0; j < kAt; ++j) x[j].x += y1[j].x, x[j].y += y1[j].y, x[j].z += y1[j].z, x[j].w += y1[j].w;
-          }
+          for (int j = 0; j < kAt; ++j) x[j].x += y[j].x, x[j].y += y[j].y, x[j].z += y[j].z, x[j].w += y[j].w;
         }
-        T* y = out + (m0 + r0) * ldo + nl;
+        T* y = out + (m0 + part + split * i0) * ldo + nl;
 #pragma unroll
         for (int j = 0; j < kAt; ++j, y += split * ldo) {
-          if (r0 + split * j >= rows) break;
+          if (part + split * (i0 + j) >= rows) break;
           if (quads && left == 4) {
             if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(y) = make_uint2(bf16x2(x[j].x, x[j].y), bf16x2(x[j].z, x[j].w));
             else *reinterpret_cast<float4*>(y) = x[j];
@@ -254,7 +253,6 @@ __global__ void __launch_bounds__(kThreads)
   }
   tc::tc_fence_before();
   __syncthreads();
-  if (split > 1) cluster_meet();   // no CTA leaves while another reads its sums
   if (warp == 1) tc::tmem_dealloc(tmem, F::kTmem);
 }
 
@@ -277,10 +275,10 @@ cudaError_t launch_few(const MatmulProblem& p, int split, cudaStream_t stream) {
 
 // How the product is cut, by the time in microseconds that it is expected to take.  The constants are fitted to 160
 // sizes (1 to 2,048 rows, N 512 to 16,416, K 512 to 12,288) with every cut timed, 905 times in all: they are within
-// 7 % of the times on average, and the cut that they pick is 0.2 % slower than the fastest on average, 7 % at most.
+// 7 % of the times on average, and the cut that they pick is 0.3 % slower than the fastest on average, 10 % at most.
 //   few rows:  a fixed part; waves of CTAs, a K block of each at so many KB through its SM, and its output; then the
 //              join of the parts of K.
-//   pairs:     a fixed part; waves of pairs, 0.255 us a K block.
+//   pairs:     a fixed part; waves of pairs, 0.236 us a K block.
 // The waves and the bytes of HBM overlap but for a part of the shorter.
 struct Cut {
   int rows, split;   // rows 0: the kernel of many rows
@@ -289,12 +287,12 @@ struct Cut {
 Cut choose(const MatmulProblem& p, int sms) {
   const int64_t groups = (p.K + 4 * kStageK - 1) / (4 * kStageK), tiles = (p.N + 127) / 128;
   const float blocks = (float)((p.K + kStageK - 1) / kStageK), out = p.dt == KDA_F32 ? 4.f : 2.f;
-  const float hbm = (((float)p.M + (float)p.N) * (float)p.K + out * (float)p.M * (float)p.N) / 6.82e6f;
+  const float hbm = (((float)p.M + (float)p.N) * (float)p.K + out * (float)p.M * (float)p.N) / 7.13e6f;
   const auto waves = [](int64_t n, int64_t room) { return (float)((n + room - 1) / room); };
-  const auto both = [&](float work) { return std::max(hbm, work) + 0.272f * std::min(hbm, work); };
+  const auto both = [&](float work) { return std::max(hbm, work) + 0.501f * std::min(hbm, work); };
   const int64_t pairs = ((p.M + 255) / 256) * ((p.N + 239) / 240);
   Cut best{0, 1, true};
-  float least = 4.97f + both(waves(pairs, sms / 2) * 0.255f * blocks);
+  float least = 4.29f + both(waves(pairs, sms / 2) * 0.236f * blocks);
   for (int rows = 16; rows <= 256; rows *= 2) {
     const int64_t mt = (p.M + rows - 1) / rows;
     if (mt > 65535) continue;   // a grid's limit
@@ -307,9 +305,9 @@ Cut choose(const MatmulProblem& p, int sms) {
       const int room2 = split <= 2 ? 2 * sms : split == 4 ? 2 * sms * 37 / 38 : 2 * sms * 18 / 19;
       const bool deep = ctas <= room1, one = deep || rows == 256;
       const float kb = (float)std::min<int64_t>((int64_t)blocks, 4 * ((groups + split - 1) / split)), stage = 16.f + (float)rows / 8.f;
-      const float work = kb * (one ? 0.00563f * stage + 0.0378f : 0.0119f * stage + 0.0344f) + 0.422f + 0.0122f * (float)rows;
-      const float join = split == 1 ? 0.f : 0.148f + 0.017f * (float)rows + 0.278f * (float)split;
-      const float t = 2.22f + both(waves(ctas, one ? room1 : room2) * work) + join;
+      const float work = kb * (one ? 0.00535f * stage + 0.0211f : 0.0111f * stage + 0.0197f) + 0.594f + 0.0109f * (float)rows;
+      const float join = split == 1 ? 0.f : 0.175f + 0.013f * (float)rows + 0.117f * (float)split;
+      const float t = 1.38f + both(waves(ctas, one ? room1 : room2) * work) + join;
       if (t < least) least = t, best = Cut{rows, split, deep};
     }
   }

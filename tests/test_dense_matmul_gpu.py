@@ -42,7 +42,9 @@ SIZES = [(1, 1, 16), (1, 128, 128), (1, 2052, 512), (3, 300, 1040), (8, 513, 409
          # each way of cutting the product that the choice by sizes has: rows of a tile, parts of K, one or two CTAs an SM
          (2, 6188, 2624), (42, 21, 15280), (1122, 514, 64), (52, 561, 15056), (6687, 62, 2784), (159, 2068, 6912), (1363, 54, 8800),
          (611, 16, 16048), (2357, 2519, 80), (6705, 108, 8864), (2749, 18, 11040), (1075, 7427, 2960), (10542, 19, 2496), (322, 8610, 48), (2657, 713, 14704), (1586, 400, 15472),
-         (131, 2192, 11472), (138, 17775, 10368), (3758, 579, 14768), (2243, 84, 4336), (66, 5494, 11264)]
+         (131, 2192, 11472), (138, 17775, 10368), (3758, 579, 14768), (2243, 84, 4336), (66, 5494, 11264),
+         (5, 48, 1792), (655, 17, 3424), (11480, 258, 2000), (13258, 529, 3600), (5351, 16, 13632), (1, 4748, 15584), (2353, 36, 10080), (4683, 22, 11280),
+         (2, 19561, 16160), (13994, 501, 7872)]
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
