@@ -74,20 +74,20 @@ __global__ void __launch_bounds__(kOneWarp ? 32 * kRowsPerBlock : 1024)
       for (int i = 0; i < 8; ++i) s = fmaf(v[j][i], v[j][i], s);
     return row_sum<kOneWarp>(s, part, warp, lane, W);
   };
-  float ss = squares();
-  // Squares beyond fp32's range, or below it with an eps that does not cover them: the row once more, scaled
-  // by a power of two (every thread of the row has the same ss).
-  const bool high = !(ss < __uint_as_float(0x7f800000u)), low = ss < 0x1p-60f && eps < 0x1p-100f;
+  const float ss = squares();
+  float mean = ss / (float)C + eps;
+  // Squares beyond fp32's range, alone or with eps, or below it with an eps that does not cover them: the row once more,
+  // scaled by a power of two (every thread of the row has the same ss).
+  const bool high = !(mean < __uint_as_float(0x7f800000u)), low = ss < 0x1p-60f && eps < 0x1p-100f;
   if (high || low) {
     const float f = high ? 0x1p-80f : 0x1p80f;
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[j][i] *= f;
-    eps = eps * f * f;   // (what underflows beside squares of 2^113 and more does not count there)
-    ss = squares();
+    mean = squares() / (float)C + eps * f * f;   // (what underflows beside a mean or an eps of 2^113 and more does not count there)
   }
-  const float inv = 1.0f / sqrtf(ss / (float)C + eps);
+  const float inv = 1.0f / sqrtf(mean);
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int64_t c0 = 256 * (int64_t)(warp + W * j);
@@ -130,7 +130,7 @@ constexpr int kNarrow = 128, kSets = 2;
 
 template <typename T, bool kAdd, bool kFp8, bool kWide>
 __global__ void __launch_bounds__(32 * kRowsPerBlock)
-    add_rmsnorm_narrow_kernel(const T* x, int64_t xs, const T* r, int64_t rs, const float* w, float eps0, int64_t rows, int32_t C,
+    add_rmsnorm_narrow_kernel(const T* x, int64_t xs, const T* r, int64_t rs, const float* w, float eps, int64_t rows, int32_t C,
                               int32_t L, T* h, T* y, uint8_t* codes, uint8_t* scales) {
   let_next_start();
   wait_for_previous();
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(32 * kRowsPerBlock)
   for (int j = 0; j < kSets; ++j) {
     const int64_t row = row0 + j * per_warp;
     const bool live = row < rows;
-    float v[8], eps = eps0;
+    float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = kAdd ? a[j].at(i) + b[j].at(i) : a[j].at(i);
     if constexpr (kAdd)
@@ -180,17 +180,17 @@ __global__ void __launch_bounds__(32 * kRowsPerBlock)
       for (int m = L >> 1; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
       return s;
     };
-    float ss = squares();
+    const float ss = squares();
+    float mean = ss / (float)C + eps;
     // as in add_rmsnorm_kernel, each row for itself
-    const bool high = !(ss < __uint_as_float(0x7f800000u)), low = ss < 0x1p-60f && eps0 < 0x1p-100f;
+    const bool high = !(mean < __uint_as_float(0x7f800000u)), low = ss < 0x1p-60f && eps < 0x1p-100f;
     if (__any_sync(0xffffffffu, high || low)) {
       const float f = high ? 0x1p-80f : low ? 0x1p80f : 1.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] *= f;
-      eps = eps0 * f * f;
-      ss = squares();
+      mean = squares() / (float)C + eps * f * f;
     }
-    const float inv = 1.0f / sqrtf(ss / (float)C + eps);
+    const float inv = 1.0f / sqrtf(mean);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = column(i) < C ? v[i] * inv * g[i] : 0.f;
     if constexpr (kFp8) {
