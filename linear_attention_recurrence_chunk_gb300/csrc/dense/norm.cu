@@ -66,28 +66,29 @@ __global__ void __launch_bounds__(kOneWarp ? 32 * kRowsPerBlock : 1024)
 #pragma unroll
     for (int j = 0; j < J; ++j) store8<T, kWide>(h + row * C, 256 * (int64_t)(warp + W * j), C, lane, v[j]);
   }
-  auto squares = [&]() {
+  auto squares = [&](float t) {
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s = fmaf(v[j][i], v[j][i], s);
+      for (int i = 0; i < 8; ++i) s = fmaf(v[j][i] * t, v[j][i] * t, s);
     return row_sum<kOneWarp>(s, part, warp, lane, W);
   };
-  const float ss = squares();
-  float mean = ss / (float)C + eps;
+  const float ss = squares(1.f);
+  const float mean = ss / (float)C + eps;
+  float inv = 1.f / sqrtf(mean);
   // Squares beyond fp32's range, alone or with eps, or below it with an eps that does not cover them: the row once more,
-  // scaled by a power of two (every thread of the row has the same ss).
+  // scaled by a power of two (every thread of the row has the same ss).  The values of a large row take half of its
+  // scaling, their squares and the factor the rest: those 2^126 below its largest would lose bits as subnormal numbers.
   const bool high = !(mean < __uint_as_float(0x7f800000u)), low = ss < 0x1p-60f && eps < 0x1p-100f;
   if (high || low) {
-    const float f = high ? 0x1p-80f : 0x1p80f;
+    const float f = high ? 0x1p-40f : 0x1p80f, t = high ? f : 1.f;
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[j][i] *= f;
-    mean = squares() / (float)C + eps * f * f;   // (what underflows beside a mean or an eps of 2^113 and more does not count there)
+    inv = t / sqrtf(squares(t) / (float)C + eps * (f * t) * (f * t));   // (what underflows beside a mean or an eps of 2^113 and more does not count there)
   }
-  const float inv = 1.0f / sqrtf(mean);
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int64_t c0 = 256 * (int64_t)(warp + W * j);
@@ -173,24 +174,24 @@ __global__ void __launch_bounds__(32 * kRowsPerBlock)
     for (int i = 0; i < 8; ++i) v[i] = kAdd ? a[j].at(i) + b[j].at(i) : a[j].at(i);
     if constexpr (kAdd)
       if (live) store(h + row * C, v);
-    const auto squares = [&]() {
+    const auto squares = [&](float t) {
       float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s = fmaf(v[i], v[i], s);
+      for (int i = 0; i < 8; ++i) s = fmaf(v[i] * t, v[i] * t, s);
       for (int m = L >> 1; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
       return s;
     };
-    const float ss = squares();
-    float mean = ss / (float)C + eps;
+    const float ss = squares(1.f);
+    const float mean = ss / (float)C + eps;
+    float inv = 1.f / sqrtf(mean);
     // as in add_rmsnorm_kernel, each row for itself
     const bool high = !(mean < __uint_as_float(0x7f800000u)), low = ss < 0x1p-60f && eps < 0x1p-100f;
     if (__any_sync(0xffffffffu, high || low)) {
-      const float f = high ? 0x1p-80f : low ? 0x1p80f : 1.f;
+      const float f = high ? 0x1p-40f : low ? 0x1p80f : 1.f, t = high ? f : 1.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] *= f;
-      mean = squares() / (float)C + eps * f * f;
+      inv = t / sqrtf(squares(t) / (float)C + eps * (f * t) * (f * t));
     }
-    const float inv = 1.0f / sqrtf(mean);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = column(i) < C ? v[i] * inv * g[i] : 0.f;
     if constexpr (kFp8) {

@@ -39,3 +39,20 @@ def test_eps_beside_finite_squares(C, top):
         _, want = ref.norm(x.double().numpy(), None, w.double().numpy(), eps)
         # E4M3: half a step of 2^-4, or of the least step under the block's scale (2^-10 of it, 448 of which hold the largest)
         assert (np.abs(v - want) <= (2.0 ** -4 + 2.0 ** -19) * np.abs(want) + 2.0 ** -10 * np.abs(want).max(1, keepdims=True) / 224).all()
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("C", [4, 27, 64, 128, 130, 300, 520, 4096, 12290])
+def test_small_values_beside_squares_beyond_the_range(C, dt):
+    """Rows whose squares overflow through one value: the others, up to 2^128 below it, keep their precision (bf16's subnormal
+    results are off by 2^-134 at most)."""
+    g = torch.Generator().manual_seed(C)
+    x = torch.randn(6, C, generator=g, dtype=torch.float64)
+    for i, e in enumerate((0, -20, -50, -60, -62, -63)):
+        x[i] *= 2.0 ** e
+    x[:, C // 2] = 2.0 ** 64 * C ** 0.5
+    x = x.to(dt)
+    _, want = ref.norm(x.double().numpy(), None, None, 1e-6)
+    y, _ = kda.kda_add_rmsnorm(x.cuda())
+    half, least = (2.0 ** -8, 2.0 ** -134) if dt is torch.bfloat16 else (0.0, 0.0)
+    assert (np.abs(y.double().cpu().numpy() - want) <= _tol(want, half) + least).all()
