@@ -70,6 +70,32 @@ bool share(const kda::dense::RotaryPart& a, const kda::dense::RotaryPart& b, con
 
 kda_status done(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
 
+// kda_fp8_matmul, by the cut that the sizes ask for or by a given one.
+kda_status matmul(kda::dense::MatmulProblem p, const kda::dense::Cut* cut, cudaStream_t stream) {
+  const int64_t M = p.M, N = p.N, K = p.K;
+  if (!dtype_ok(p.dt) || M < 0 || N < 0 || K < 1) return KDA_ERR_INVALID_ARG;
+  if (K % 16 != 0 || M > kMost || N > kMost || K > kMostK) return KDA_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return KDA_OK;
+  const auto up16 = [](int64_t v) { return (v + 15) / 16 * 16; };
+  if (M == 1) p.lda = K, p.ldo = N;   // a stride over one row has no meaning
+  if (N == 1) p.ldw = up16(K);
+  if (!p.a || !p.w || !p.sa || !p.sw || !p.out) return KDA_ERR_INVALID_ARG;
+  if (!aligned(p.a, 16) || !aligned(p.w, 16) || !aligned(p.out, elem(p.dt)) || p.lda % 16 != 0 || p.ldw % 16 != 0) return KDA_ERR_INVALID_ARG;
+  if (!stride_ok(p.lda, K) || !stride_ok(p.ldw, K) || !stride_ok(p.ldo, N)) return KDA_ERR_INVALID_ARG;
+  const Range in[] = {span(p.a, M, K, p.lda, 1), span(p.w, N, K, p.ldw, 1), {p.sa, (size_t)(M * blocks_of(K))},
+                      {p.sw, (size_t)(blocks_of(N) * blocks_of(K))}};
+  const Range res[] = {span(p.out, M, N, p.ldo, elem(p.dt))};
+  if (!apart(in, res)) return KDA_ERR_INVALID_ARG;
+  if (cut) {
+    const int r = cut->rows, s = cut->split;
+    const bool is_few = (r == 16 || r == 32 || r == 64 || r == 128 || r == 256) && (s == 1 || s == 2 || s == 4 || s == 8);
+    if (!(r == 0 && s == 1) && !(is_few && s <= (blocks_of(K) + 3) / 4)) return KDA_ERR_INVALID_ARG;
+    if (!kda::dense::cut_fits(p, *cut)) return KDA_ERR_UNSUPPORTED;
+  }
+  if (kda::device_error_ptr(&p.dev_err) != cudaSuccess) return KDA_ERR_CUDA;
+  return done(kda::dense::launch_matmul(p, cut, stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -128,22 +154,21 @@ kda_status kda_add_rmsnorm(const void* x, int64_t x_stride, const void* residual
 kda_status kda_fp8_matmul(const uint8_t* a, int64_t a_stride, const uint8_t* a_scales, const uint8_t* w, int64_t w_stride,
                           const uint8_t* w_scales, int64_t M, int64_t N, int64_t K, kda_dtype dt, void* out, int64_t out_stride,
                           cudaStream_t stream) {
-  if (!dtype_ok(dt) || M < 0 || N < 0 || K < 1) return KDA_ERR_INVALID_ARG;
-  if (K % 16 != 0 || M > kMost || N > kMost || K > kMostK) return KDA_ERR_UNSUPPORTED;
-  if (M == 0 || N == 0) return KDA_OK;
-  const auto up16 = [](int64_t v) { return (v + 15) / 16 * 16; };
-  if (M == 1) a_stride = K, out_stride = N;   // a stride over one row has no meaning
-  if (N == 1) w_stride = up16(K);
-  if (!a || !w || !a_scales || !w_scales || !out) return KDA_ERR_INVALID_ARG;
-  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(out, elem(dt)) || a_stride % 16 != 0 || w_stride % 16 != 0) return KDA_ERR_INVALID_ARG;
-  if (!stride_ok(a_stride, K) || !stride_ok(w_stride, K) || !stride_ok(out_stride, N)) return KDA_ERR_INVALID_ARG;
-  const Range in[] = {span(a, M, K, a_stride, 1), span(w, N, K, w_stride, 1), {a_scales, (size_t)(M * blocks_of(K))},
-                      {w_scales, (size_t)(blocks_of(N) * blocks_of(K))}};
-  const Range res[] = {span(out, M, N, out_stride, elem(dt))};
-  if (!apart(in, res)) return KDA_ERR_INVALID_ARG;
-  kda::dense::MatmulProblem p{a, a_scales, w, w_scales, a_stride, w_stride, M, N, K, dt, out, out_stride, nullptr};
-  if (kda::device_error_ptr(&p.dev_err) != cudaSuccess) return KDA_ERR_CUDA;
-  return done(kda::dense::launch_matmul(p, stream));
+  return matmul({a, a_scales, w, w_scales, a_stride, w_stride, M, N, K, dt, out, out_stride, nullptr}, nullptr, stream);
+}
+
+kda_status kda_fp8_matmul_cut(const uint8_t* a, int64_t a_stride, const uint8_t* a_scales, const uint8_t* w, int64_t w_stride,
+                              const uint8_t* w_scales, int64_t M, int64_t N, int64_t K, kda_dtype dt, void* out, int64_t out_stride,
+                              int32_t rows, int32_t split, int32_t deep, cudaStream_t stream) {
+  const kda::dense::Cut cut{rows, split, deep != 0};
+  return matmul({a, a_scales, w, w_scales, a_stride, w_stride, M, N, K, dt, out, out_stride, nullptr}, &cut, stream);
+}
+
+kda_status kda_fp8_matmul_choice(int64_t M, int64_t N, int64_t K, kda_dtype dt, int32_t sms, int32_t* cut) {
+  if (!dtype_ok(dt) || M < 1 || N < 1 || K < 16 || M > kMost || N > kMost || K > kMostK || sms < 2 || !cut) return KDA_ERR_INVALID_ARG;
+  const kda::dense::Cut c = kda::dense::choose_cut({nullptr, nullptr, nullptr, nullptr, K, K, M, N, K, dt, nullptr, N, nullptr}, sms);
+  cut[0] = c.rows, cut[1] = c.split, cut[2] = c.deep;
+  return KDA_OK;
 }
 
 kda_status kda_rotary(const void* q, int64_t q_token_stride, int64_t q_head_stride, int32_t Hq, const void* k, int64_t k_token_stride,

@@ -269,7 +269,15 @@ struct MatmulProblem {
   int64_t ldo;
   int32_t* dev_err;
 };
-cudaError_t launch_matmul(const MatmulProblem& p, cudaStream_t stream);
+// How a product is cut: tiles of `rows` rows of A (a power of two from 16 to 256; 0: the kernel of many rows), the parts of
+// K of a tile (1, 2, 4 or 8, each with a group of four K blocks at least), and one CTA an SM or two.
+struct Cut {
+  int32_t rows, split;
+  bool deep;
+};
+Cut choose_cut(const MatmulProblem& p, int sms);
+bool cut_fits(const MatmulProblem& p, const Cut& c);   // a grid's limits
+cudaError_t launch_matmul(const MatmulProblem& p, const Cut* cut, cudaStream_t stream);   // cut NULL: the one chosen by sizes
 cudaError_t launch_matmul_pair(const MatmulProblem& p, int sms, cudaStream_t stream);   // many rows
 
 struct RotaryPart {   // queries or keys
@@ -292,3 +300,13 @@ cudaError_t launch_rotary(const RotaryProblem& p, cudaStream_t stream);
 
 }  // namespace dense
 }  // namespace kda
+
+// For tests, and no part of the headers that a user includes: the cut {rows, split, deep} that kda_fp8_matmul takes on a device
+// of so many SMs, and kda_fp8_matmul with a given one.  KDA_ERR_INVALID_ARG for a cut that there is not,
+// KDA_ERR_UNSUPPORTED for one beyond a grid's limits.
+extern "C" {
+KDA_API kda_status kda_fp8_matmul_choice(int64_t M, int64_t N, int64_t K, kda_dtype dt, int32_t sms, int32_t* cut);
+KDA_API kda_status kda_fp8_matmul_cut(const uint8_t* a, int64_t a_stride, const uint8_t* a_scales, const uint8_t* w, int64_t w_stride,
+                                      const uint8_t* w_scales, int64_t M, int64_t N, int64_t K, kda_dtype dt, void* out, int64_t out_stride,
+                                      int32_t rows, int32_t split, int32_t deep, cudaStream_t stream);
+}

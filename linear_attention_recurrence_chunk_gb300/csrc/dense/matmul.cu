@@ -17,7 +17,6 @@
 #include <limits.h>
 
 #include <algorithm>
-#include <cstdlib>
 
 #include "internal.cuh"
 #include "mma8.cuh"
@@ -273,6 +272,25 @@ cudaError_t launch_few(const MatmulProblem& p, int split, cudaStream_t stream) {
   return e;
 }
 
+template <typename T>
+cudaError_t launch(const MatmulProblem& p, const Cut& c, cudaStream_t stream) {
+  switch (c.rows) {
+    case 16: return c.deep ? launch_few<16, true, T>(p, c.split, stream) : launch_few<16, false, T>(p, c.split, stream);
+    case 32: return c.deep ? launch_few<32, true, T>(p, c.split, stream) : launch_few<32, false, T>(p, c.split, stream);
+    case 64: return c.deep ? launch_few<64, true, T>(p, c.split, stream) : launch_few<64, false, T>(p, c.split, stream);
+    case 128: return c.deep ? launch_few<128, true, T>(p, c.split, stream) : launch_few<128, false, T>(p, c.split, stream);
+    default: return launch_few<256, true, T>(p, c.split, stream);
+  }
+}
+
+}  // namespace
+
+bool cut_fits(const MatmulProblem& p, const Cut& c) {
+  if (c.rows == 0) return true;
+  const int64_t mt = (p.M + c.rows - 1) / c.rows;
+  return mt <= 65535 && (p.N + 127) / 128 * mt * c.split <= INT32_MAX;
+}
+
 // How the product is cut, by the time in microseconds that it is expected to take.  The constants are fitted to 160
 // sizes (1 to 2,048 rows, N 512 to 16,416, K 512 to 12,288) with every cut timed, 905 times in all: they are within
 // 7 % of the times on average, and the cut that they pick is 0.3 % slower than the fastest on average, 10 % at most.
@@ -280,11 +298,7 @@ cudaError_t launch_few(const MatmulProblem& p, int split, cudaStream_t stream) {
 //              join of the parts of K.
 //   pairs:     a fixed part; waves of pairs, 0.236 us a K block.
 // The waves and the bytes of HBM overlap but for a part of the shorter.
-struct Cut {
-  int rows, split;   // rows 0: the kernel of many rows
-  bool deep;
-};
-Cut choose(const MatmulProblem& p, int sms) {
+Cut choose_cut(const MatmulProblem& p, int sms) {
   const int64_t groups = (p.K + 4 * kStageK - 1) / (4 * kStageK), tiles = (p.N + 127) / 128;
   const float blocks = (float)((p.K + kStageK - 1) / kStageK), out = p.dt == KDA_F32 ? 4.f : 2.f;
   const float hbm = (((float)p.M + (float)p.N) * (float)p.K + out * (float)p.M * (float)p.N) / 7.13e6f;
@@ -295,10 +309,9 @@ Cut choose(const MatmulProblem& p, int sms) {
   float least = 4.29f + both(waves(pairs, sms / 2) * 0.236f * blocks);
   for (int rows = 16; rows <= 256; rows *= 2) {
     const int64_t mt = (p.M + rows - 1) / rows;
-    if (mt > 65535) continue;   // a grid's limit
     for (int split = 1; split <= 8 && split <= groups; split *= 2) {
+      if (!cut_fits(p, {rows, split, true})) continue;
       const int64_t ctas = tiles * mt * split;
-      if (ctas > INT32_MAX) continue;
       // CTAs that run at once, one an SM or two, by clusters: 152, 152, 144, 120 and 304, 304, 296, 288 on GB300's 152 SMs
       // (cudaOccupancyMaxActiveClusters)
       const int room1 = split <= 2 ? sms : split == 4 ? sms * 18 / 19 : sms * 15 / 19;
@@ -314,30 +327,12 @@ Cut choose(const MatmulProblem& p, int sms) {
   return best;
 }
 
-template <typename T>
-cudaError_t launch(const MatmulProblem& p, const Cut& c, cudaStream_t stream) {
-  switch (c.rows) {
-    case 16: return c.deep ? launch_few<16, true, T>(p, c.split, stream) : launch_few<16, false, T>(p, c.split, stream);
-    case 32: return c.deep ? launch_few<32, true, T>(p, c.split, stream) : launch_few<32, false, T>(p, c.split, stream);
-    case 64: return c.deep ? launch_few<64, true, T>(p, c.split, stream) : launch_few<64, false, T>(p, c.split, stream);
-    case 128: return c.deep ? launch_few<128, true, T>(p, c.split, stream) : launch_few<128, false, T>(p, c.split, stream);
-    default: return launch_few<256, true, T>(p, c.split, stream);
-  }
-}
-
-}  // namespace
-
-cudaError_t launch_matmul(const MatmulProblem& p, cudaStream_t stream) {
+cudaError_t launch_matmul(const MatmulProblem& p, const Cut* cut, cudaStream_t stream) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  Cut c = choose(p, sms);
-  // KDA_FP8_PAIR=1 takes pairs whatever the sizes, KDA_FP8_PAIR=0 never (tests).
-  if (const char* env = std::getenv("KDA_FP8_PAIR")) {
-    if (std::atoi(env) != 0) c.rows = 0;
-    else if (c.rows == 0) c = Cut{256, 1, true};
-  }
+  const Cut c = cut ? *cut : choose_cut(p, sms);
   if (c.rows == 0) return launch_matmul_pair(p, sms, stream);
   return p.dt == KDA_F32 ? launch<float>(p, c, stream) : launch<__nv_bfloat16>(p, c, stream);
 }

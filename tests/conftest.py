@@ -13,6 +13,15 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "slow: full-size workloads (minutes)")
 
 
+@pytest.fixture(autouse=True)
+def _fp8_kernel_by_environment(request, monkeypatch):
+    """The tests of the 8-bit product choose between its kernels by KDA_FP8_PAIR (1: pairs of CTAs, 0: single ones).  The
+    library has no such switch: their calls go through its entry that takes a given cut."""
+    if request.module.__name__ == "test_dense_matmul_gpu":
+        import dense_testutil
+        dense_testutil.cuts_by_environment(monkeypatch)
+
+
 def pytest_terminal_summary(terminalreporter, exitstatus, config):
     """Error margins of the parity tests that recorded them: the bare
     max|dO|/rms(o_ref), the same after each stored value's own rounding

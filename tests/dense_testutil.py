@@ -2,6 +2,9 @@
 every level, norms and rotations row by row.  They share no code with the library."""
 from __future__ import annotations
 
+import ctypes
+import os
+
 import numpy as np
 
 
@@ -90,3 +93,48 @@ def rotate(x, pos, freqs, amplitude, interleaved, inverse):
 def half_step(t):
     """Half a step of bf16 or fp32 values, relative."""
     return 2.0 ** -8 if t == "bf16" else 2.0 ** -24
+
+
+# ------------------------------------------------------------------ cuts of the 8-bit product
+def cut_library():
+    """The library, with the two entries that no header has: the cut of a product, and a product by a given cut."""
+    from linear_attention_recurrence_chunk_gb300 import dense
+    lib = dense._lib()
+    vp, i32, i64, c = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int
+    lib.kda_fp8_matmul_choice.argtypes = [i64, i64, i64, c, i32, ctypes.POINTER(i32)]
+    lib.kda_fp8_matmul_cut.argtypes = [vp, i64, vp, vp, i64, vp, i64, i64, i64, c, vp, i64, i32, i32, i32, vp]
+    return lib
+
+
+def choice(M, N, K, dt, sms=152):
+    """(rows, split, deep) of a product with output type dt (0: fp32, 1: bf16); rows 0: pairs of CTAs."""
+    cut = (ctypes.c_int32 * 3)()
+    status = cut_library().kda_fp8_matmul_choice(M, N, K, dt, sms, cut)
+    assert status == 0, status
+    return tuple(cut)
+
+
+def force_cut(monkeypatch, cut_of):
+    """kda_fp8_matmul by the cut that cut_of(M, N, K, dt) gives (None: the library's own choice)."""
+    lib = cut_library()
+    plain = lib.kda_fp8_matmul
+
+    def call(*args):
+        cut = cut_of(*args[6:10])
+        return plain(*args) if cut is None else lib.kda_fp8_matmul_cut(*args[:-1], *cut, args[-1])
+
+    monkeypatch.setattr(lib, "kda_fp8_matmul", call)
+
+
+def cuts_by_environment(monkeypatch):
+    def cut_of(M, N, K, dt):
+        pair = os.environ.get("KDA_FP8_PAIR")
+        if pair is None or min(M, N, K) < 1 or K % 16:
+            return None
+        if pair != "0":
+            return 0, 1, 1
+        import torch
+        cut = choice(M, N, K, dt, torch.cuda.get_device_properties(0).multi_processor_count)
+        return cut if cut[0] else (256, 1, 1)
+
+    force_cut(monkeypatch, cut_of)
