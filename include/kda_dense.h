@@ -67,8 +67,8 @@ KDA_API kda_status kda_add_rmsnorm(const void* x, int64_t x_stride, const void* 
  *  w, w_scales  codes [N][K], row stride w_stride in bytes; scales [ceil(N / 128)][ceil(K / 128)] (R = 128)
  *  out          [M][N] dtype dt, row stride out_stride in elements, at least N
  * K (at least 16) and the row strides of a and w are multiples of 16, a and w 16-byte aligned, out aligned to
- * its type.  Products are exact, sums fp32 in the tensor core's order, which depends on the
- * sizes alone: the same call gives the same bits.  A NaN code of a row of A reaches that row of
+ * its type.  Products are exact, sums fp32 in an order that depends on M, N, K and the number of the device's SMs
+ * alone: the same call gives the same bits, and a bf16 output is the fp32 output rounded.  A NaN code of a row of A reaches that row of
  * out, one of W that column; a scale byte 255 its row, or its 128 columns.
  * KDA_ERR_UNSUPPORTED: K not a multiple of 16 or beyond 2^27; M or N beyond 2^31 - 512.
  */

@@ -14,6 +14,7 @@
 // 4,096 x 12,288 18.4 us against 18.5), eight-CTA clusters beyond 15 of them (two waves).  Joining by loads from the other
 // CTAs took 14.9 us for 128 x 4,096 x 12,288, stores to them 13.4; stores of four tokens of a weight, whose
 // lanes lie apart, 17.2; a CTA's own share stored by its own address 14.0.
+#include <float.h>
 #include <limits.h>
 
 #include <algorithm>
@@ -298,19 +299,20 @@ bool cut_fits(const MatmulProblem& p, const Cut& c) {
 //              join of the parts of K.
 //   pairs:     a fixed part; waves of pairs, 0.236 us a K block.
 // The waves and the bytes of HBM overlap but for a part of the shorter.
-Cut choose_cut(const MatmulProblem& p, int sms) {
+// `out` bytes an output value; only: the one number of parts of K to look at (0: any).
+static Cut least_time(const MatmulProblem& p, int sms, float out, int only) {
   const int64_t groups = (p.K + 4 * kStageK - 1) / (4 * kStageK), tiles = (p.N + 127) / 128;
-  const float blocks = (float)((p.K + kStageK - 1) / kStageK), out = p.dt == KDA_F32 ? 4.f : 2.f;
+  const float blocks = (float)((p.K + kStageK - 1) / kStageK);
   const float hbm = (((float)p.M + (float)p.N) * (float)p.K + out * (float)p.M * (float)p.N) / 7.13e6f;
   const auto waves = [](int64_t n, int64_t room) { return (float)((n + room - 1) / room); };
   const auto both = [&](float work) { return std::max(hbm, work) + 0.501f * std::min(hbm, work); };
   const int64_t pairs = ((p.M + 255) / 256) * ((p.N + 239) / 240);
   Cut best{0, 1, true};
-  float least = 4.29f + both(waves(pairs, sms / 2) * 0.236f * blocks);
+  float least = only > 1 ? FLT_MAX : 4.29f + both(waves(pairs, sms / 2) * 0.236f * blocks);
   for (int rows = 16; rows <= 256; rows *= 2) {
     const int64_t mt = (p.M + rows - 1) / rows;
     for (int split = 1; split <= 8 && split <= groups; split *= 2) {
-      if (!cut_fits(p, {rows, split, true})) continue;
+      if ((only && split != only) || !cut_fits(p, {rows, split, true})) continue;
       const int64_t ctas = tiles * mt * split;
       // CTAs that run at once, one an SM or two, by clusters: 152, 152, 144, 120 and 304, 304, 296, 288 on GB300's 152 SMs
       // (cudaOccupancyMaxActiveClusters)
@@ -325,6 +327,14 @@ Cut choose_cut(const MatmulProblem& p, int sms) {
     }
   }
   return best;
+}
+
+// The order of a sum is that of its parts of K, whatever the tiles: fp32 outputs take as many parts as bf16 ones, which
+// are then the same sums, rounded.  (One size in 10,000 would take others of its own: 39 x 6,169 x 7,184 with fp32 outputs 14.5
+// us and 16.1 by its own, 61 x 4,955 x 9,888 16.8 and 14.3.)
+Cut choose_cut(const MatmulProblem& p, int sms) {
+  const Cut c = least_time(p, sms, 2.f, 0);
+  return p.dt == KDA_F32 ? least_time(p, sms, 4.f, c.split) : c;
 }
 
 cudaError_t launch_matmul(const MatmulProblem& p, const Cut* cut, cudaStream_t stream) {

@@ -32,6 +32,16 @@ def test_choices_at_a_grids_limits(M, N, K):
         assert _fits(M, N, ref.choice(M, N, K, dt))
 
 
+@pytest.mark.parametrize("sms", [148, 152])
+def test_parts_of_k_do_not_depend_on_the_output_type(sms):
+    """They set the order of the sums."""
+    rng = random.Random(3)
+    sizes = [(39, 6169, 7184), (55, 4345, 6448), (61, 4955, 9888)]
+    sizes += [(int(2 ** rng.uniform(0, 13)), int(2 ** rng.uniform(4, 14)), 16 * int(2 ** rng.uniform(2, 10))) for _ in range(5000)]
+    for size in sizes:
+        assert ref.choice(*size, 0, sms)[1] == ref.choice(*size, 1, sms)[1], size
+
+
 @pytest.mark.parametrize("bad", [dict(M=0), dict(N=0), dict(K=15), dict(dt=2), dict(sms=1), dict(M=2 ** 31), dict(cut=None)])
 def test_choice_refuses(bad):
     a = dict(M=10, N=20, K=512, dt=1, sms=152, cut=(ctypes.c_int32 * 3)())

@@ -40,3 +40,31 @@ def test_the_environment_does_not_choose(monkeypatch):
     one = torch.full((1, 16), 1.0, device="cuda").to(torch.float8_e4m3fn)
     got = kda.kda_fp8_matmul(a, torch.full((M, 1), 127, dtype=torch.uint8, device="cuda"), one, torch.full((1, 1), 127, dtype=torch.uint8, device="cuda"))
     assert torch.equal(got[:, 0], a[:, 0].to(torch.bfloat16))
+
+
+def _operands(M, N, K):
+    """Rows and columns over some powers of two, so that the order of a sum shows in its bits."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x = torch.randn(M, K, device="cuda", generator=g) * torch.exp(2 * torch.randn(M, K, device="cuda", generator=g))
+    return (*kda.kda_fp8_quant(x), *kda.kda_fp8_quant(torch.randn(N, K, device="cuda", generator=g), 128))
+
+
+@pytest.mark.parametrize("M,N,K", [(39, 6169, 7184), (55, 4345, 6448), (61, 4955, 9888), (1, 16416, 4096), (228, 16300, 4096), (974, 4516, 912),
+                                   (64, 4096, 12288)])
+def test_bf16_is_fp32_rounded(M, N, K):
+    """Sizes at which the two types would be cut differently among them."""
+    ops = _operands(M, N, K)
+    f, h = kda.kda_fp8_matmul(*ops, torch.float32), kda.kda_fp8_matmul(*ops)
+    assert torch.equal(f.bfloat16(), h)
+
+
+@pytest.mark.parametrize("split", [1, 2, 4, 8])
+def test_bits_depend_on_the_parts_of_k_alone(split, monkeypatch):
+    ops = _operands(130, 513, 4112)
+    got = []
+    for cut in CUTS:
+        if cut[1] == split:
+            with monkeypatch.context() as m:
+                ref.force_cut(m, lambda *_: cut)
+                got.append(kda.kda_fp8_matmul(*ops, torch.float32))
+    assert len(got) >= 9 and all(torch.equal(got[0], f) for f in got)
