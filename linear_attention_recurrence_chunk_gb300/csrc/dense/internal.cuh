@@ -14,8 +14,10 @@ constexpr int kBlock = 128;   // columns of a scale
 
 // -------------------------------------------------------------- launches one behind another
 // Every kernel here is launched so that it may start while the one before it in the stream ends, and lets the next one
-// do so at once.  It touches no global memory before all that ran before it is complete and visible; it loads nothing
-// by the read-only path or through __restrict__ pointers, since what they read may be written while it waits.  Taken in
+// do so at once (one thread of a CTA says so for it); a product only when it has its tensor memory.  CTAs of the next
+// product take theirs before they wait and give it back after this one has ended: were this one still without its own,
+// each could wait for the other.  No kernel touches global memory before all that ran before it is complete and visible, or
+// loads by the read-only path or through __restrict__ pointers, since what they read may be written while it waits.  Taken in
 // turn with plain launches: a product of one row, 16,416 x 4,096, 13.0 us a call against 15.6, 8 x 2,052 x 512 in
 // a graph 2.4 against 3.2, 8,192 x 12,288 to 8 bits and back 92.6 against 96.9, 256 x 4,096 normed (host time) 14.0
 // against 14.6.

@@ -92,7 +92,6 @@ __global__ void __launch_bounds__(kThreads)
       return r < kRows && m0 + r < M ? m0 + r : (int64_t)-1;
     });
   };
-  let_next_start();
   if (warp == 0) {
     if (lane < F::kBars) tc::mbar_init(full + lane, 1);
     tc::fence_mbar_init();
@@ -102,6 +101,7 @@ __global__ void __launch_bounds__(kThreads)
   } else if (warp == 1) {
     tc::tmem_alloc(tmem_at, F::kTmem);
     tc::tmem_relinquish();
+    let_next_start();   // not before: see there
   }
   wait_for_previous();
   if (warp == 0) {

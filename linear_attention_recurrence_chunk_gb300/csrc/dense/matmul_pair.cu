@@ -125,7 +125,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_load_w<2>(at + st * kStage + kA, &mapB, kb * kStageK, yb, lead + 8 * st);
   };
   const int early = rank == 0 ? min(blocks, kStages) : 0;   // of the first tile
-  let_next_start();
   if (warp == 0) {
     if (lane < kBars) {   // in the order of their declaration: full, empty, sfull, sempty, tfull, tempty
       const int i = lane - 2 * kStages - kScaleSlots;
@@ -137,6 +136,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 3) {
     tmem_alloc_pair(tmem_at, 512);
+    let_next_start();   // not before: see there
   }
   wait_for_previous();
   if (warp == 0 && early > 0) {
