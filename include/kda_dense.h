@@ -88,10 +88,11 @@ enum { KDA_ROTARY_INTERLEAVED = 1, KDA_ROTARY_INVERSE = 2 };
  *
  *  q [T][Hq][D], k [T][Hk][D] dtype dt, and q_out, k_out of the same shapes: strides from token to
  *             token and head to head in elements, channels contiguous.  A part with no heads (0) may be
- *             NULL.  An output is its input (the same pointer and strides: in place) or overlaps no input;
- *             its heads and tokens do not lie over one another.  In place, the other part lies apart, or
- *             between the tokens (the same token stride) or heads (the same head stride) of this one, as
- *             parts of one projection do.
+ *             NULL.  An output is its input (the same pointer and strides: in place), or none of its values is
+ *             one of an input's; its heads and tokens do not lie over one another, or over the other output's.
+ *             Inputs and outputs may lie between one another's tokens (with the same token stride) or heads
+ *             (with the same head stride, a divisor of the token stride), as parts of one projection do;
+ *             other ones lie apart from first to last byte.
  *  positions  int32[T] (kda_page_map's); a token with a negative one is not turned
  *  freqs      fp64[rot / 2]: radians per position, finite
  * Angles are reduced to a fraction of a turn in 64 bits of fixed point: at any position they are

@@ -52,20 +52,28 @@ bool shape_ok(int64_t rows, int64_t C) {
 }
 bool stride_ok(int64_t stride, int64_t C) { return stride >= C && stride <= kMostStride; }
 
-// Whether the values that two parts read may be the same ones.  Parts whose bytes lie over one another are told apart
-// as parts of one projection are: between one another's tokens (the same token stride), or heads (the same head stride,
-// which divides the tokens').
-bool share(const kda::dense::RotaryPart& a, const kda::dense::RotaryPart& b, const Range& ra, const Range& rb, int64_t T, int32_t D, size_t eb) {
-  if (!overlaps(ra, rb)) return false;
-  if (T > 1 && a.xt != b.xt) return true;
-  const int64_t d = (int64_t)(reinterpret_cast<intptr_t>(b.x) - reinterpret_cast<intptr_t>(a.x)) / (int64_t)eb;
+// Heads of D values, T tokens of them: what a rotation reads of a part, or writes of it.
+struct Heads {
+  const void* p;
+  int64_t t, h;   // strides in elements from token to token (T = 1: 0) and head to head (H = 1: 0)
+  int32_t H;
+  int64_t token(int32_t D) const { return (H - 1) * h + D; }
+  Range bytes(int64_t T, int32_t D, size_t eb) const { return {p, H > 0 ? (size_t)((T - 1) * t + token(D)) * eb : 0}; }
+};
+// Whether two of these may have a value in common.  Parts whose bytes lie over one another are told apart as parts of one
+// projection are: between one another's tokens (the same token stride), or heads (the same head stride, which divides the
+// tokens').
+bool share(const Heads& a, const Heads& b, int64_t T, int32_t D, size_t eb) {
+  if (!overlaps(a.bytes(T, D, eb), b.bytes(T, D, eb))) return false;
+  if (T > 1 && a.t != b.t) return true;
+  const int64_t d = (int64_t)(reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p)) / (int64_t)eb;
   const auto beside = [d](int64_t step, int64_t na, int64_t nb) {   // na and nb values of each `step`, d apart
     const int64_t r = step > 0 ? (d % step + step) % step : 0;
     return step > 0 && r >= na && r + nb <= step;
   };
-  if (T > 1 && beside(a.xt, (a.H - 1) * a.xh + D, (b.H - 1) * b.xh + D)) return false;
-  const int64_t h = std::max(a.xh, b.xh);   // of one head: 0
-  return !((a.H == 1 || a.xh == h) && (b.H == 1 || b.xh == h) && h > 0 && (T == 1 || a.xt % h == 0) && beside(h, D, D));
+  if (T > 1 && beside(a.t, a.token(D), b.token(D))) return false;
+  const int64_t h = std::max(a.h, b.h);   // of one head: 0
+  return !((a.H == 1 || a.h == h) && (b.H == 1 || b.h == h) && h > 0 && (T == 1 || a.t % h == 0) && beside(h, D, D));
 }
 
 kda_status done(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
@@ -184,7 +192,7 @@ kda_status kda_rotary(const void* q, int64_t q_token_stride, int64_t q_head_stri
   const size_t eb = elem(dt);
   kda::dense::RotaryPart part[2] = {{q, q_out, q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride, Hq},
                                     {k, k_out, k_token_stride, k_head_stride, k_out_token_stride, k_out_head_stride, Hk}};
-  Range in[4] = {{nullptr, 0}, {nullptr, 0}, {positions, (size_t)T * 4}, {freqs, (size_t)rot / 2 * 8}}, out[2] = {{nullptr, 0}, {nullptr, 0}};
+  Heads in[2] = {}, out[2] = {};
   bool place[2] = {false, false};
   for (int i = 0; i < 2; ++i) {
     kda::dense::RotaryPart& p = part[i];
@@ -198,16 +206,18 @@ kda_status kda_rotary(const void* q, int64_t q_token_stride, int64_t q_head_stri
     // an output's heads and tokens do not lie over one another: the heads of a token side by side, or the tokens of a head
     if ((p.H > 1 && p.yh < D) || (T > 1 && p.yt < D)) return KDA_ERR_INVALID_ARG;
     if (p.H > 1 && T > 1 && p.yt < (p.H - 1) * p.yh + D && p.yh < (T - 1) * p.yt + D) return KDA_ERR_INVALID_ARG;
-    in[i] = {p.x, (size_t)((T - 1) * p.xt + (p.H - 1) * p.xh + D) * eb};
-    out[i] = {p.y, (size_t)((T - 1) * p.yt + (p.H - 1) * p.yh + D) * eb};
+    in[i] = {p.x, p.xt, p.xh, p.H};
+    out[i] = {p.y, p.yt, p.yh, p.H};
     place[i] = p.x == p.y && p.xt == p.yt && p.xh == p.yh;
   }
+  const Range tables[] = {{positions, (size_t)T * 4}, {freqs, (size_t)rot / 2 * 8}};
   for (int i = 0; i < 2; ++i) {
-    if (overlaps(out[i], in[2]) || overlaps(out[i], in[3])) return KDA_ERR_INVALID_ARG;
-    // In place, the other part may lie between the tokens or heads of this one (parts of one projection).
-    if (!place[i] && (overlaps(out[i], in[0]) || overlaps(out[i], in[1]) || overlaps(out[i], out[1 - i]))) return KDA_ERR_INVALID_ARG;
+    for (const Range& r : tables)
+      if (overlaps(out[i].bytes(T, D, eb), r)) return KDA_ERR_INVALID_ARG;
+    for (int j = 0; j < 2; ++j)
+      if (!(i == j && place[i]) && share(out[i], in[j], T, D, eb)) return KDA_ERR_INVALID_ARG;
   }
-  if ((place[0] || place[1]) && part[0].H > 0 && part[1].H > 0 && share(part[0], part[1], in[0], in[1], T, D, eb)) return KDA_ERR_INVALID_ARG;
+  if (share(out[0], out[1], T, D, eb)) return KDA_ERR_INVALID_ARG;
   return done(kda::dense::launch_rotary({part[0], part[1], positions, freqs, T, D, rot, amplitude, flags, dt}, stream));
 }
 

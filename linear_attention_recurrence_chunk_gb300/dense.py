@@ -286,7 +286,7 @@ def kda_rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tens
     strides: the first 2 len(freqs) channels of each head turned by positions ``[T]`` (int32) times
     freqs (fp64), in pairs (i, i + len(freqs)), or (2 i, 2 i + 1) when interleaved.  Tokens with a
     negative position stay as they are.  Returns ``(q_out, k_out)``, new tensors unless given;
-    an output may be its input (in place)."""
+    an output may be its input (in place), and inputs and outputs may be parts of one tensor."""
     dev = _device("q", q)
     if stream is not None or dev != _current_device():
         return _run(dev, stream, lambda _: kda_rotary(q, k, positions, freqs, amplitude, interleaved, inverse, q_out, k_out))
