@@ -7,7 +7,9 @@
  *
  * The conventions of kda.h hold: device pointers owned by the caller, nothing
  * allocated, asynchronous on `stream`, argument errors found on the host before
- * anything is launched.  None of these calls needs scratch memory.
+ * anything is launched.  None of these calls needs scratch memory.  Each may start while
+ * the kernel before it on its stream ends: its blocks then wait on the SMs, and what they
+ * hold (threads, registers, shared and tensor memory) other streams do without meanwhile.
  *
  * 8-bit matrices: codes uint8 [rows][C], an E4M3 value each (sign, 4 exponent
  * bits of bias 7, 3 mantissa bits, no infinities, 0x7f and 0xff NaN, largest
@@ -69,8 +71,8 @@ KDA_API kda_status kda_add_rmsnorm(const void* x, int64_t x_stride, const void* 
  * K (at least 16) and the row strides of a and w are multiples of 16, a and w 16-byte aligned, out aligned to
  * its type.  Products are exact, sums fp32 in an order that depends on M, N, K and the number of the device's SMs
  * alone: the same call gives the same bits, and a bf16 output is the fp32 output rounded.  Their error's rms stays below
- * K 2^-28 of a row's (normally distributed values: 5e-7 of it for K = 12,288, 4e-6 for 2,048 rows of 16,384).  A NaN code of a row of A reaches that row of
- * out, one of W that column; a scale byte 255 its row, or its 128 columns.
+ * K 2^-28 of a row's (normally distributed values: 5e-7 of it for K = 12,288, 4e-6 for 2,048 rows of 16,384).  A NaN
+ * code of a row of A reaches that row of out, one of W that column; a scale byte 255 its row, or its 128 columns.
  * KDA_ERR_UNSUPPORTED: K not a multiple of 16 or beyond 2^27; M or N beyond 2^31 - 512.
  */
 KDA_API kda_status kda_fp8_matmul(const uint8_t* a, int64_t a_stride, const uint8_t* a_scales, const uint8_t* w,

@@ -19,8 +19,8 @@ constexpr int kBlock = 128;   // columns of a scale
 // each could wait for the other.  No kernel touches global memory before all that ran before it is complete and visible, or
 // loads by the read-only path or through __restrict__ pointers, since what they read may be written while it waits.  Taken in
 // turn with plain launches: a product of one row, 16,416 x 4,096, 13.0 us a call against 15.6, 8 x 2,052 x 512 in
-// a graph 2.4 against 3.2, 8,192 x 12,288 to 8 bits and back 92.6 against 96.9, 256 x 4,096 normed (host time) 14.0
-// against 14.6.
+// a graph 2.4 against 3.2, 8,192 x 12,288 to 8 bits and back 92.6 against 96.9.  CTAs that wait keep their threads,
+// registers and shared memory from other streams as long as the kernel before them runs (not timed).
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

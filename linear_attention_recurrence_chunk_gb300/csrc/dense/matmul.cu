@@ -8,8 +8,8 @@
 // fill the chip; each sends the others the sums that they join, through distributed shared memory, and adds its own
 // share in a fixed order, with no scratch memory and one launch.
 // Measured (replayed from a graph): 1 x 16,416 x 4,096 13.0 us (the bytes' floor 9.9; DRAM is busy 56 % of it, the first
-// bytes come after 3 us), 8 x 2,052 x 512 2.4 us, 64 x 4,096 x 12,288 12.2 us (7.6), 256 x 4,096 x 12,288 16.7 us (8.2: a
-// K block takes some 400 cycles, 256 of them products, and the join 2 us).  In a loop of K blocks the issue counts
+// bytes come after 3 us), 8 x 2,052 x 512 2.4 us, 64 x 4,096 x 12,288 12.4 us (7.6), 256 x 4,096 x 12,288 16.7 us (8.2: a
+// K block takes some 400 cycles, 256 of them products, and the join 2 us); with fp32 outputs as long.  In a loop of K blocks the issue counts
 // as much as the products: see mma_block_w and wait_lane.  Not faster: pairs of CTAs on 256 rows of W (256 x
 // 4,096 x 12,288 18.4 us against 18.5), eight-CTA clusters beyond 15 of them (two waves).  Joining by loads from the other
 // CTAs took 14.9 us for 128 x 4,096 x 12,288, stores to them 13.4; stores of four tokens of a weight, whose
@@ -292,9 +292,10 @@ bool cut_fits(const MatmulProblem& p, const Cut& c) {
   return mt <= 65535 && (p.N + 127) / 128 * mt * c.split <= INT32_MAX;
 }
 
-// How the product is cut, by the time in microseconds that it is expected to take.  The constants are fitted to 160
-// sizes (1 to 2,048 rows, N 512 to 16,416, K 512 to 12,288) with every cut timed, 905 times in all: they are within
-// 7 % of the times on average, and the cut that they pick is 0.3 % slower than the fastest on average, 10 % at most.
+// How the product is cut, by the time in microseconds that it is expected to take.  The constants are fitted to 905 times
+// of 160 sizes (1 to 2,048 rows, N 512 to 16,416, K 512 to 12,288).  On 919 times of the same sizes taken later, with
+// every cut that they pick among them, they are within 7 % on average, and the cut that they pick is 0.4 % slower than
+// the fastest on average, 12 % at most.
 //   few rows:  a fixed part; waves of CTAs, a K block of each at so many KB through its SM, and its output; then the
 //              join of the parts of K.
 //   pairs:     a fixed part; waves of pairs, 0.236 us a K block.

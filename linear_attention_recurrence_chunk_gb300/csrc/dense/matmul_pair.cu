@@ -11,7 +11,7 @@
 // Measured: 8,192 x 16,416 x 4,096 276 us of small whole numbers (4.0 PFLOP/s, 2.07 times the measured bf16 rate),
 // 306 us of normally distributed values in single graphs and 361 in long runs, where the power limit holds the clock at
 // 1.39 GHz; the tensor pipe is active 91 % of the cycles.  16,384 x 16,384 x 8,192 1.09 ms (4.0 PFLOP/s).
-// 8,192 x 16,416 x 512 57 us: its output alone takes 41.  Slower: five stages of six (298 us against 283, with
+// 8,192 x 16,416 x 512 57 us: its output alone takes 41; with fp32 outputs 101 us (80), x 4,096 300 us.  Slower: five stages of six (298 us against 283, with
 // eight storing warps); parts of K in clusters of four and six CTAs for few tiles (256 x 4,096 x 12,288: 21.7 us against the
 // other kernel's 20.9); barriers arrived at with a release at cluster scope, 1,000 cycles each (780 us).  An output whose rows
 // are not on 16-byte boundaries takes element stores: 8,192 x 16,417 x 512 106 us (by aligned windows of 64 bytes, more

@@ -6,10 +6,12 @@
 // its output: W warps of a CTA have J x 256 columns each (one warp alone for narrow rows), all
 // loads of a row on their way before the first is used; the 8-bit form takes its block maxima from
 // the same registers, so that nothing is read twice.  Rows of a head's size share a warp.
-// Measured (replayed from a graph): 32,768 x 4,096 of bf16 with a residual 156 us (6.9 TB/s), in 8 bits 142 us (6.6 TB/s;
-// DRAM 80 %, issue slots 73 %); 1,000,000 x 128 153 us (6.7 TB/s); 16,384 x 2,001 of fp32 79 us (6.7 TB/s); bf16 rows of odd
-// width by 2-byte accesses 4.4 TB/s (8,192 x 8,001); 32,000 x 768 of bf16 with a residual 33 us (5.9 TB/s).  256 x 4,096: 3.7 us, one row 2.1 us: launch and latency.  Slower: a
-// block with row after row and the next one's loads ahead (32,768 x 4,096 172 us: half the warps an SM).
+// Measured (replayed from a graph), with a residual, of bf16: 32,768 x 4,096 156 us (6.9 TB/s), in 8 bits 142 us (6.6 TB/s;
+// DRAM 80 %, issue slots 73 %); 1,000,000 x 128 153 us (6.7 TB/s); 32,000 x 768 32 us (6.1 TB/s); rows of odd width by
+// 2-byte accesses 4.4 TB/s, 3.1 without a residual (8,192 x 8,001).  256 x 4,096 3.1 us, one row 1.9 us: launch and
+// latency.  Of fp32: 16,384 x 2,001 79 us (6.7 TB/s); 4,096 x 32,768 333 us (6.5 TB/s); 4,096 x 20,000 232 us (5.7
+// TB/s: 79 chunks are 20 warps of 64 registers, one block an SM), x 20,001 276 us (4.8 TB/s: 116 bytes a thread spill too).
+// Slower: a block with row after row and the next one's loads ahead (32,768 x 4,096 172 us: half the warps an SM).
 #include <type_traits>
 
 #include "internal.cuh"

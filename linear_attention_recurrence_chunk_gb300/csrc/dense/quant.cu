@@ -7,7 +7,7 @@
 // alignment: a warp, four values a lane), four of them at once, whatever rows they lie in.  Blocks of 128 x 128: a CTA
 // holds one in registers between its maximum and its codes.
 // Measured (replayed from a graph), 32,768 x 4,096 of bf16: 62.9 us (6.4 TB/s) by rows, 65.5 us (6.2 TB/s) by
-// squares, read back 61.4 us (6.6 TB/s).  By rows the instructions count (issue slots 69 %): with the sizes compared
+// squares, read back 61 us (6.6 TB/s); 16,384 x 4,096 of fp32 48 us (6.9 TB/s) and 52 us (6.5 TB/s).  By rows the instructions count (issue slots 69 %): with the sizes compared
 // and the values scaled as packed bf16, and the places of a warp's blocks taken from one row, 76 -> 63 us.
 // bf16 rows of odd width, by 2-byte accesses, 2.9 TB/s (8,192 x 8,001).
 #include <type_traits>

@@ -5,14 +5,17 @@
 // The angle is wanted modulo a turn, and positions go to 2^31: the frequency in turns, modulo 1, is held
 // as a 64-bit fixed-point fraction (from fp64 once per block), so that its product with the position p
 // modulo 2^64 is the fraction of a turn to p 2^-63, with no reduction and no table.  The top 32 bits, signed,
-// are half turns in [-1, 1) for sincospi.
+// are half turns in [-1, 1) for sincospi, rounded to fp32's 24 bits: 4.1e-8 radians rms, 9.4e-8 at most.
+// (fp32 outputs are off by 3.9e-8 of their size, with exact angles they would be by 2.9e-8.)
 //
 // Bound: HBM, each value read and written once.  A warp takes a token at a time (a part of its heads when there are
 // few tokens): the first loads go out, then the token's cosines and sines into the warp's shared memory, each once,
 // then all heads of queries and keys, eight pairs (two 16-byte loads of bf16) a lane and three such items on their
 // way at once.
 // Measured (replayed from a graph): 65,536 tokens, 32 + 4 heads of 128 in bf16 187 us (6.5 TB/s), either order of the pairs,
-// half of each head turned 189 us; 256 tokens of 96 + 8 heads 4.8 us; one token 2.9 us.  A block that first makes the
+// half of each head turned 189 us; 256 tokens of 96 + 8 heads 4.4 us, 6.1 where the frequencies come from HBM too; one token
+// 2.8 us.  Pairs that are no multiple of 8, one value a load: 65,536 tokens, 8 + 2 heads of 80, 20 channels turned, 171
+// us (1.2 TB/s), of 96 with 24 turned 183 us; with 32 turned 50 us (5.0 TB/s).  A block that first makes the
 // cosines of a few tokens together and then turns their heads took 328 us: its phases waited for one another.
 #include <algorithm>
 #include <type_traits>
